@@ -7,10 +7,18 @@ an sm_100 GPU, calls raise.
 
     o, lse = fa_fwd(q, k, v, causal=True)            # q, k, v: bf16 [B, H, N, d] on cuda
     o, lse = fa_decode_paged(q, k_pool, v_pool, block_table, seq_lens)
+
+A serving step over an 8-bit cache writes its tokens and then attends to them:
+
+    freqs, amp = rope_frequencies(rot)
+    q = fa_cache_append(k, v, k_pool, v_pool, slots, k_scale=ks, v_scale=vs, positions=pos,
+                        freqs=freqs, amplitude=amp, q=q)
+    o, lse = fa_decode_paged_q8(q, k_pool, v_pool, ks, vs, block_table, seq_lens)
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -20,6 +28,9 @@ from . import build as _build
 __all__ = ["fa_fwd", "fa_bwd", "fa_decode_paged", "fa_decode_paged_noalloc", "fa_prefill_paged",
            "fa_tree_attention", "fa_fwd_keyrange", "fa_merge_partials",
            "fa_decode_workspace_size",
+           "rope_frequencies", "fa_rope", "fa_cache_append", "fa_cache_read",
+           "fa_decode_paged_q8", "fa_prefill_paged_q8", "fa_tree_attention_q8",
+           "fa_q8_workspace_size",
            "NOALLOC_SCRATCH_BYTES", "device_status",
            "FaError", "library_path", "load_library", "EXPORTED_SYMBOLS", "STATUS"]
 
@@ -34,7 +45,9 @@ EXPORTED_SYMBOLS = ("fa_fwd", "fa_decode_workspace_size", "fa_decode_paged",
                     "fa_bwd", "fa_get_device_status",
                     "fa_status_string",
                     "fa_last_error_string", "fa_version", "fa_selftest_wait_timeout",
-                    "fa_probe_ex2_rate", "fa_probe_read_rate", "fa_fwd_schedule")
+                    "fa_probe_ex2_rate", "fa_probe_read_rate", "fa_fwd_schedule",
+                    "fa_rope", "fa_cache_append", "fa_cache_read", "fa_q8_workspace_size",
+                    "fa_decode_paged_q8", "fa_prefill_paged_q8", "fa_tree_attention_q8")
 
 _lib = None
 
@@ -88,6 +101,26 @@ def load_library():
     lib.fa_bwd.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32,
                            f32, vp, ctypes.c_size_t, vp]
     lib.fa_bwd.restype = i32
+    i64, i64p = ctypes.c_longlong, ctypes.POINTER(ctypes.c_longlong)
+    lib.fa_rope.argtypes = [vp, i64p, vp, i64p, vp, i64p, vp, i64p, i32, i32, vp, i64, vp, i32, i32,
+                            f32, i32, i32, i32, i32, i32, i32, vp]
+    lib.fa_rope.restype = i32
+    lib.fa_cache_append.argtypes = [vp, i64p, vp, i64p, vp, vp, vp, vp, i32, vp, i32, vp, i64p, vp,
+                                    i64p, vp, vp, i32, i32, f32, i32, i32, i32, i32, vp]
+    lib.fa_cache_append.restype = i32
+    lib.fa_cache_read.argtypes = [vp, vp, vp, vp, i32, vp, i32, vp, vp, i32, i32, i32, vp]
+    lib.fa_cache_read.restype = i32
+    lib.fa_q8_workspace_size.argtypes = [i32] * 6
+    lib.fa_q8_workspace_size.restype = sz
+    lib.fa_decode_paged_q8.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32, vp, i32, vp, i32, vp, i32,
+                                       i32, i32, i32, f32, vp, sz, vp]
+    lib.fa_decode_paged_q8.restype = i32
+    lib.fa_prefill_paged_q8.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32, vp, i32, vp, i32, vp, i32,
+                                        i32, i32, i32, i32, i32, f32, vp, sz, vp]
+    lib.fa_prefill_paged_q8.restype = i32
+    lib.fa_tree_attention_q8.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32, vp, i32, vp, vp, i32, vp,
+                                         i32, i32, i32, i32, i32, f32, vp, sz, vp]
+    lib.fa_tree_attention_q8.restype = i32
     lib.fa_get_device_status.argtypes = [vp]
     lib.fa_get_device_status.restype = i32
     lib.fa_status_string.argtypes = [i32]
@@ -407,6 +440,353 @@ def fa_decode_paged_noalloc(q, k_pool, v_pool, block_table, seq_lens, out, lse=N
                float(scale) if scale is not None else 0.0, _stream_handle(stream))
     _check(st, "fa_decode_paged_noalloc")
     return out, lse
+
+
+# ------------------------------------------------------------------------------------------------
+# rotary positions, the paged cache's writer and reader, attention over an 8-bit cache
+# ------------------------------------------------------------------------------------------------
+
+_ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+_CACHE_TYPE = {torch.bfloat16: 0, torch.float8_e4m3fn: 1, torch.int8: 2}
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None,
+                     factor: float = 1.0, original_len: int = 4096, fast: float = 32.0,
+                     slow: float = 1.0, device="cuda"):
+    """Frequencies of fa_rope's rot / 2 pairs, in radians per position, and the amplitude that goes
+    with them: (float64 [rot / 2] on `device`, float).
+
+    f_j = base^(-2j / rot).  For contexts `factor` times as long as the trained ones, scaling is
+      "linear"  all positions are shrunk: f_j / factor (position interpolation, Chen et al. 2023);
+      "base"    the base grows to base * factor^(rot / (rot - 2)), which keeps the fastest pair and
+                slows the slowest by `factor`;
+      "ramp"    pairs that turn more than `fast` times in `original_len` positions keep their
+                frequency, those that turn less than `slow` times take f_j / factor, with a linear
+                ramp in the number of turns between, and the amplitude is 0.1 ln(factor) + 1 (YaRN,
+                Peng et al. 2023)."""
+    if rot < 2 or rot % 2:
+        raise ValueError("rot must be a positive even number")
+    if not (base > 0 and factor >= 1.0):
+        raise ValueError("base must be positive and factor at least 1")
+    if scaling == "base":
+        if rot <= 2:
+            raise ValueError("scaling 'base' needs rot > 2")
+        base = base * factor ** (rot / (rot - 2))
+    f = base ** (-2.0 * torch.arange(rot // 2, dtype=torch.float64) / rot)
+    amplitude = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "ramp":
+        if not fast > slow:
+            raise ValueError("scaling 'ramp' needs fast > slow")
+        turns = original_len * f / (2.0 * math.pi)
+        keep = ((turns - slow) / (fast - slow)).clamp(0.0, 1.0)
+        f = f * keep + f / factor * (1.0 - keep)
+        amplitude = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "base"):
+        raise ValueError(f"scaling must be None, 'linear', 'base' or 'ramp', got {scaling!r}")
+    return f.to(device), amplitude
+
+
+def _strides(t, n):
+    return (ctypes.c_longlong * n)(*t.stride()[:n])
+
+
+def _require_rows(t, name, dims, dtypes, device=None):
+    """A CUDA tensor whose last dimension is contiguous; the others may have any strides."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {dtypes}, got {t.dtype}")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions")
+    if t.numel() and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+
+
+def _require_on(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}")
+
+
+def _rope_args(freqs, positions, layout, device):
+    """(freqs pointer, rot, layout code) after the checks both rotating calls share."""
+    if layout not in _ROPE_LAYOUT:
+        raise ValueError("layout must be 'half' or 'interleaved'")
+    if freqs is None:
+        return None, 0, _ROPE_LAYOUT[layout]
+    _require(freqs, "freqs", torch.float64)
+    if freqs.dim() != 1:
+        raise ValueError("freqs must be [rot / 2]")
+    if positions is None:
+        raise ValueError("positions are needed with freqs")
+    _require_on(device, freqs=freqs, positions=positions)
+    return freqs.data_ptr(), 2 * freqs.numel(), _ROPE_LAYOUT[layout]
+
+
+def fa_rope(q, k, positions, freqs, layout: str = "half", amplitude: float = 1.0,
+            inverse: bool = False, out_dtype=None, q_out=None, k_out=None, stream=None):
+    """Rotary positions.  q [B, Hq, N, d] and k [B, Hk, N, d] (or None), bf16 or fp32, any strides
+    with the features contiguous (a projection's [B, N, heads, d] goes in as its transpose(1, 2));
+    positions int32 [N] or [B, N]; freqs float64 [rot / 2], see rope_frequencies; layout "half"
+    (pairs j, j + rot/2) or "interleaved" (2j, 2j + 1).  inverse=True turns back: the gradient.
+
+    Returns (q_out, k_out): the tensors passed, which may be q and k themselves, or new contiguous
+    [B, H, N, d] ones in out_dtype (default: the input's)."""
+    lib = load_library()
+    io = (torch.bfloat16, torch.float32)
+    _require_rows(q, "q", 4, io)
+    dev = q.device
+    B, Hq, N, d = q.shape
+    out_dtype = out_dtype or (q_out.dtype if q_out is not None else q.dtype)
+    out_code = _out_code(out_dtype)
+    Hk, kp, ks, kop, kos = 0, None, None, None, None
+    if k is not None:
+        _require_rows(k, "k", 4, (q.dtype,), dev)
+        Hk = k.shape[1]
+        if k.shape != (B, Hk, N, d):
+            raise ValueError("k must be [B, Hk, N, d] with q's B, N, d")
+    if q_out is None:
+        q_out = torch.empty((B, Hq, N, d), dtype=out_dtype, device=dev)
+    else:
+        _require_rows(q_out, "q_out", 4, (out_dtype,), dev)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty((B, Hk, N, d), dtype=out_dtype, device=dev)
+        else:
+            _require_rows(k_out, "k_out", 4, (out_dtype,), dev)
+            if k_out.shape != k.shape:
+                raise ValueError("k_out must have k's shape")
+        if Hk:
+            kp, ks, kop, kos = k.data_ptr(), _strides(k, 3), k_out.data_ptr(), _strides(k_out, 3)
+    fptr, rot, code = _rope_args(freqs, positions, layout, dev)
+    pos_ptr, pos_stride = None, 0
+    if positions is not None:
+        _require(positions, "positions", torch.int32)
+        if positions.shape not in ((N,), (B, N)):
+            raise ValueError("positions must be [N] or [B, N]")
+        pos_ptr, pos_stride = positions.data_ptr(), N if positions.dim() == 2 else 0
+    with torch.cuda.device(dev):
+        st = lib.fa_rope(q.data_ptr(), _strides(q, 3), q_out.data_ptr(), _strides(q_out, 3), kp, ks,
+                         kop, kos, _out_code(q.dtype), out_code, pos_ptr, pos_stride, fptr, rot,
+                         code, float(amplitude), int(inverse), B, Hq, Hk, N, d,
+                         _stream_handle(stream))
+    _check(st, "fa_rope")
+    return q_out, k_out
+
+
+def _require_pools(k_pool, v_pool, k_scale, v_scale):
+    """(cache type code, num_blocks, heads, d, scale pointers) of a paged pool."""
+    for t, n in ((k_pool, "k_pool"), (v_pool, "v_pool")):
+        if not isinstance(t, torch.Tensor) or t.dtype not in _CACHE_TYPE:
+            raise ValueError(f"{n} must be a bfloat16, float8_e4m3fn or int8 tensor")
+        _require(t, n, t.dtype)
+    if k_pool.dim() != 4 or k_pool.shape[2] != 16 or v_pool.shape != k_pool.shape:
+        raise ValueError("k_pool / v_pool must be [num_blocks, H, 16, d]")
+    if v_pool.dtype != k_pool.dtype:
+        raise ValueError("k_pool and v_pool must have one type")
+    P, H, _, d = k_pool.shape
+    code = _CACHE_TYPE[k_pool.dtype]
+    ptrs = (None, None)
+    if code:
+        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _require(t, n, torch.float32)
+            if t.shape != (P, H, 16):
+                raise ValueError(f"{n} must be [num_blocks, H, 16]")
+        ptrs = (k_scale.data_ptr(), v_scale.data_ptr())
+        _require_on(k_pool.device, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale)
+    else:
+        _require_on(k_pool.device, v_pool=v_pool)
+    return code, P, H, d, ptrs
+
+
+def fa_cache_append(k, v, k_pool, v_pool, slots, k_scale=None, v_scale=None, positions=None,
+                    freqs=None, layout: str = "half", amplitude: float = 1.0, q=None, q_out=None,
+                    stream=None):
+    """Write T tokens' keys and values to their slots of the paged cache, in place.
+
+    k, v bf16 [T, Hk, d] (any strides, features contiguous); k_pool, v_pool [num_blocks, Hk, 16, d]
+    in bfloat16, float8_e4m3fn or int8, the 8-bit types with k_scale, v_scale fp32
+    [num_blocks, Hk, 16]; slots int64 [T] (block * 16 + row; negative: not written).  With freqs
+    (float64 [rot / 2]) and positions (int32 [T]) the keys are rotated first, and q bf16 [T, Hq, d]
+    beside them.  Returns q_out (new and contiguous unless passed), or None without q."""
+    lib = load_library()
+    bf = (torch.bfloat16,)
+    code, P, Hk, d, (ksp, vsp) = _require_pools(k_pool, v_pool, k_scale, v_scale)
+    dev = k_pool.device
+    _require_rows(k, "k", 3, bf, dev)
+    _require_rows(v, "v", 3, bf, dev)
+    T = k.shape[0]
+    if k.shape != (T, Hk, d) or v.shape != k.shape:
+        raise ValueError("k and v must be [T, Hk, d] with the pools' heads and features")
+    _require(slots, "slots", torch.int64)
+    if slots.shape != (T,):
+        raise ValueError("slots must be [T]")
+    _require_on(dev, slots=slots)
+    fptr, rot, lcode = _rope_args(freqs, positions, layout, dev)
+    if positions is not None:
+        _require(positions, "positions", torch.int32)
+        if positions.shape != (T,):
+            raise ValueError("positions must be [T]")
+    Hq, qp, qs, qop, qos = 0, None, None, None, None
+    if q is not None:
+        _require_rows(q, "q", 3, bf, dev)
+        Hq = q.shape[1]
+        if q.shape != (T, Hq, d):
+            raise ValueError("q must be [T, Hq, d]")
+        if q_out is None:
+            q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+        else:
+            _require_rows(q_out, "q_out", 3, bf, dev)
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
+        if Hq:
+            qp, qs, qop, qos = q.data_ptr(), _strides(q, 2), q_out.data_ptr(), _strides(q_out, 2)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    with torch.cuda.device(dev):
+        st = lib.fa_cache_append(k.data_ptr(), _strides(k, 2), v.data_ptr(), _strides(v, 2),
+                                 k_pool.data_ptr(), v_pool.data_ptr(), ksp, vsp, code,
+                                 slots.data_ptr(), P, qp, qs, qop, qos,
+                                 positions.data_ptr() if rot else None, fptr, rot, lcode,
+                                 float(amplitude), T, Hq, Hk, d, _stream_handle(stream))
+    _check(st, "fa_cache_append")
+    return q_out
+
+
+def fa_cache_read(k_pool, v_pool, slots, k_scale=None, v_scale=None, k_out=None, v_out=None,
+                  stream=None):
+    """Read the rows at slots (int64 [T]; negative: zeros) of a paged cache back as bf16: returns
+    (k, v), each [T, H, d].  Pools and scales as for fa_cache_append."""
+    lib = load_library()
+    code, P, H, d, (ksp, vsp) = _require_pools(k_pool, v_pool, k_scale, v_scale)
+    dev = k_pool.device
+    _require(slots, "slots", torch.int64)
+    if slots.dim() != 1:
+        raise ValueError("slots must be [T]")
+    _require_on(dev, slots=slots)
+    T = slots.shape[0]
+    out = []
+    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            t = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
+        else:
+            _require(t, n)
+            if t.shape != (T, H, d):
+                raise ValueError(f"{n} must be [T, H, d]")
+            _require_on(dev, **{n: t})
+        out.append(t)
+    with torch.cuda.device(dev):
+        st = lib.fa_cache_read(k_pool.data_ptr(), v_pool.data_ptr(), ksp, vsp, code,
+                               slots.data_ptr(), P, out[0].data_ptr(), out[1].data_ptr(), T, H, d,
+                               _stream_handle(stream))
+    _check(st, "fa_cache_read")
+    return out[0], out[1]
+
+
+def fa_q8_workspace_size(S: int, Hq: int, Hk: int, Lq: int, d: int, max_blocks_per_seq: int) -> int:
+    """Bytes of workspace fa_decode_paged_q8 (Lq = 1), fa_prefill_paged_q8 and fa_tree_attention_q8
+    need; 0 when none."""
+    return int(load_library().fa_q8_workspace_size(S, Hq, Hk, Lq, d, max_blocks_per_seq))
+
+
+def _attend_q8(where, q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, tree_mask, causal,
+               scale, out_dtype, out, lse, return_lse, workspace, stream):
+    lib = load_library()
+    _require(q, "q")
+    code, P, Hk, d, (ksp, vsp) = _require_pools(k_pool, v_pool, k_scale, v_scale)
+    if not code:
+        raise ValueError("k_pool / v_pool must be float8_e4m3fn or int8")
+    if q.dim() != (3 if causal is None else 4):
+        raise ValueError("q must be [S, Hq, d]" if causal is None else "q must be [S, Hq, Lq, d]")
+    S, Hq, Lq = q.shape[0], q.shape[1], 1 if causal is None else q.shape[2]
+    if q.shape[-1] != d or Hq % Hk:
+        raise ValueError("q must have the pools' d and a multiple of their heads")
+    _require(block_table, "block_table", torch.int32)
+    _require(seq_lens, "seq_lens", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != S or seq_lens.shape != (S,):
+        raise ValueError("block_table must be [S, max_blocks] and seq_lens [S]")
+    dev = q.device
+    _require_on(dev, k_pool=k_pool, block_table=block_table, seq_lens=seq_lens, out=out, lse=lse,
+                workspace=workspace, tree_mask=tree_mask)
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype, device=dev)
+    else:
+        _require(out, "out", out_dtype)
+        if out.shape != q.shape:
+            raise ValueError("out has the wrong shape")
+    if lse is None and return_lse:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+    elif lse is not None:
+        _require(lse, "lse", torch.float32)
+        if lse.shape != q.shape[:-1]:
+            raise ValueError("lse has the wrong shape")
+    maxb = block_table.shape[1]
+    if workspace is None:
+        need = lib.fa_q8_workspace_size(S, Hq, Hk, Lq, d, maxb)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    ws, ws_bytes = (None, 0) if workspace is None else (
+        workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    head = (q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), ksp, vsp, code,
+            block_table.data_ptr(), maxb, seq_lens.data_ptr(), P)
+    tail = (out.data_ptr(), _out_code(out_dtype), lse.data_ptr() if lse is not None else None, S, Hq,
+            Hk)
+    sc = float(scale) if scale is not None else 0.0
+    with torch.cuda.device(dev):
+        sh = _stream_handle(stream)
+        if causal is None:
+            st = lib.fa_decode_paged_q8(*head, *tail, d, sc, ws, ws_bytes, sh)
+        elif tree_mask is not None:
+            st = lib.fa_tree_attention_q8(*head, tree_mask.data_ptr(), *tail, Lq, d, sc, ws, ws_bytes,
+                                          sh)
+        else:
+            st = lib.fa_prefill_paged_q8(*head, *tail, Lq, d, int(causal), sc, ws, ws_bytes, sh)
+    _check(st, where)
+    return out, lse
+
+
+def fa_decode_paged_q8(q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens,
+                       scale: float | None = None, out_dtype=torch.bfloat16, out=None, lse=None,
+                       return_lse: bool = True, workspace=None, stream=None):
+    """One decode step over an 8-bit paged cache (see fa_cache_append), query heads sharing key
+    heads: q bf16 [S, Hq, d]; pools float8_e4m3fn or int8 [num_blocks, Hk, 16, d]; scales fp32
+    [num_blocks, Hk, 16]; block_table int32 [S, max_blocks]; seq_lens int32 [S] (0: an empty slot).
+    Returns (o [S, Hq, d], lse fp32 [S, Hq] or None)."""
+    return _attend_q8("fa_decode_paged_q8", q, k_pool, v_pool, k_scale, v_scale, block_table,
+                      seq_lens, None, None, scale, out_dtype, out, lse, return_lse, workspace, stream)
+
+
+def fa_prefill_paged_q8(q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens,
+                        causal: bool = True, scale: float | None = None, out_dtype=torch.bfloat16,
+                        out=None, lse=None, return_lse: bool = True, workspace=None, stream=None):
+    """Chunked prefill over an 8-bit paged cache: q bf16 [S, Hq, Lq, d] holds the last Lq positions
+    of each sequence, already in the cache; the rest as for fa_decode_paged_q8.
+    Returns (o [S, Hq, Lq, d], lse fp32 [S, Hq, Lq] or None)."""
+    return _attend_q8("fa_prefill_paged_q8", q, k_pool, v_pool, k_scale, v_scale, block_table,
+                      seq_lens, None, bool(causal), scale, out_dtype, out, lse, return_lse, workspace,
+                      stream)
+
+
+def fa_tree_attention_q8(q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, tree_mask,
+                         scale: float | None = None, out_dtype=torch.bfloat16, out=None, lse=None,
+                         return_lse: bool = True, workspace=None, stream=None):
+    """Tree verification over an 8-bit paged cache: q bf16 [S, Hq, T, d] holds the T <= 64 nodes, the
+    last T cached tokens; tree_mask int64 [S, T] as for fa_tree_attention; the rest as for
+    fa_decode_paged_q8.  Returns (o [S, Hq, T, d], lse fp32 [S, Hq, T] or None)."""
+    _require(tree_mask, "tree_mask", torch.int64)
+    if q.dim() != 4 or tree_mask.shape != (q.shape[0], q.shape[2]):
+        raise ValueError("tree_mask must be [S, T]")
+    return _attend_q8("fa_tree_attention_q8", q, k_pool, v_pool, k_scale, v_scale, block_table,
+                      seq_lens, tree_mask, False, scale, out_dtype, out, lse, return_lse, workspace,
+                      stream)
 
 
 def selftest_wait_timeout(limit_us: int = 50_000, stream=None) -> int:

@@ -1,0 +1,225 @@
+// fa_cache.cuh -- writing new tokens' keys and values into the paged pool, and reading rows back.
+//
+// Paging: "LLM study notes" (devocean.sk.com), paged attention.  A token's slot is
+// block * 16 + row in the pool [num_blocks, H, 16, d]; scales lie beside it as [num_blocks, H, 16].
+//
+// 8-bit rows carry one fp32 scale each (per token and head): scale = max|x| / qmax with qmax = 448
+// (e4m3) or 127 (int8), code = the value nearest to x / scale, ties to even, and the row stands for
+// code * scale.  scale and quotient are fp32 divisions rounded to nearest (bf16 inputs fall on the
+// border between two codes too often for a reciprocal's last bit not to matter).  A row whose
+// largest magnitude is below 2^-100 is stored as zeros with scale 0; a row that holds an infinity
+// or a NaN is stored with scale NaN (and reads back as NaN, as a bf16 row would mostly do).
+// Keys are rotated (fa_rope.cuh) and quantised from fp32, with no rounding to bf16 between.
+//
+// Bound: HBM (and launch latency for a decode step's few rows); everything is read and written once.
+#pragma once
+#include <cuda_fp8.h>
+
+#include "fa_rope.cuh"
+
+namespace fa {
+
+constexpr int kCachePage = 16;
+enum CacheType { kCacheBf16 = 0, kCacheE4m3 = 1, kCacheInt8 = 2 };
+constexpr float kCacheTiny = 0x1p-100f;
+
+template <int kType>
+__host__ __device__ constexpr float cache_qmax() { return kType == kCacheE4m3 ? 448.f : 127.f; }
+
+struct AppendParams {
+  // sources and the q output: [T, H, d] with element strides of token and head
+  const uint16_t *q, *k, *v;
+  uint16_t *q_out;
+  long long q_s[2], k_s[2], v_s[2], qo_s[2];
+  void *k_pool, *v_pool;
+  float *k_scale, *v_scale;
+  const int64_t *slots;
+  const int32_t *positions;
+  RopeTable table;
+  int T, Hq, Hk;
+  long long num_slots;
+  int log_tok;
+};
+
+// x / s rounded to nearest, from r = 1 / s rounded to nearest: one residual step after the product
+// (Markstein) gives the correctly rounded quotient; s is a normal number here and |x / s| <= qmax.
+__device__ __forceinline__ float div_by_rcp(float x, float s, float r) {
+  const float y = x * r;
+  return fmaf(fmaf(-y, s, x), r, y);
+}
+
+template <int kType>
+__device__ __forceinline__ uint32_t cache_code4(const float *f, float s, float r) {
+  float y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = div_by_rcp(f[i], s, r);
+  if constexpr (kType == kCacheE4m3) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+  } else {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = max(-127, min(127, __float2int_rn(y[i])));
+      w |= static_cast<uint32_t>(c & 0xff) << (8 * i);
+    }
+    return w;
+  }
+}
+
+// grid: ceil(T / kTok).  Rows of a CTA: q heads, k heads, v heads, its tokens side by side; HD / 16
+// threads a row, 16 features each, the row maximum by shuffles among them.
+template <int HD, int kType>
+__global__ void __launch_bounds__(kRopeThreads) fa_cache_append_kernel(const AppendParams p) {
+  __shared__ float2 cs[kRopeMaxTok * kRopeMaxPairs];
+  __shared__ long long slot_sm[kRopeMaxTok];
+  constexpr int kChunks = HD / 16;
+  const int tok_n = 1 << p.log_tok;
+  const int m0 = blockIdx.x << p.log_tok;
+  const int live = min(tok_n, p.T - m0);
+  const int pairs = p.table.rot / 2;
+  for (int t = threadIdx.x; t < live; t += kRopeThreads) {
+    long long slot = p.slots[m0 + t];
+    if (slot >= p.num_slots) {  // caller broke the contract: report, write nothing for the token
+      atomicExch(&g_device_status, 1 /* FA_ERR_INVALID_ARG */);
+      slot = -1;
+    }
+    slot_sm[t] = slot;
+  }
+  for (int i = threadIdx.x; i < live * pairs; i += kRopeThreads)
+    cs[i] = rope_cos_sin(p.table, p.positions[m0 + i / pairs], i % pairs);
+  __syncthreads();
+  const int rows = (p.Hq + 2 * p.Hk) << p.log_tok;
+  const int chunk = threadIdx.x % kChunks;
+  const int2 rcol = rope_cols(p.table, chunk);
+  constexpr int kStep = kRopeThreads / kChunks;
+  // whole warps stay in the loop together: the shuffles need every lane
+  for (int r0 = 0; r0 < rows; r0 += kStep) {
+    const int r = r0 + threadIdx.x / kChunks;
+    const int t = r & (tok_n - 1);
+    int h = r >> p.log_tok;
+    const bool is_q = h < p.Hq;
+    const bool is_v = h >= p.Hq + p.Hk;
+    if (!is_q) h -= is_v ? p.Hq + p.Hk : p.Hq;
+    const long long slot = t < live ? slot_sm[t] : -1;
+    const bool act = r < rows && t < live && (is_q || slot >= 0);
+    const int2 col = is_v ? make_int2(16 * chunk, 16 * chunk + 8) : rcol;
+    float f[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] = 0.f;
+    if (act) {
+      const long long m = m0 + t;
+      const uint16_t *src = is_q ? p.q + m * p.q_s[0] + h * p.q_s[1]
+                            : is_v ? p.v + m * p.v_s[0] + h * p.v_s[1]
+                                   : p.k + m * p.k_s[0] + h * p.k_s[1];
+      load8(reinterpret_cast<const __nv_bfloat16 *>(src + col.x), f);
+      load8(reinterpret_cast<const __nv_bfloat16 *>(src + col.y), f + 8);
+      if (!is_v) rope_apply(p.table, cs + t * pairs, chunk, f);
+    }
+    float top = 0.f, bad = 0.f;
+    if constexpr (kType != kCacheBf16) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        top = fmaxf(top, fabsf(f[i]));
+        bad += f[i] * 0.f;  // NaN when any feature is infinite or NaN
+      }
+#pragma unroll
+      for (int off = kChunks / 2; off > 0; off >>= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        bad += __shfl_xor_sync(0xffffffffu, bad, off);
+      }
+    }
+    if (!act) continue;
+    if (is_q) {
+      uint16_t *dst = p.q_out + static_cast<long long>(m0 + t) * p.qo_s[0] + h * p.qo_s[1];
+      store8(reinterpret_cast<__nv_bfloat16 *>(dst + col.x), f);
+      store8(reinterpret_cast<__nv_bfloat16 *>(dst + col.y), f + 8);
+      continue;
+    }
+    const long long row = (slot / kCachePage * p.Hk + h) * kCachePage + slot % kCachePage;
+    void *pool = is_v ? p.v_pool : p.k_pool;
+    if constexpr (kType == kCacheBf16) {
+      uint16_t *dst = static_cast<uint16_t *>(pool) + row * HD;
+      store8(reinterpret_cast<__nv_bfloat16 *>(dst + col.x), f);
+      store8(reinterpret_cast<__nv_bfloat16 *>(dst + col.y), f + 8);
+    } else {
+      float scale = top >= kCacheTiny ? __fdiv_rn(top, cache_qmax<kType>()) : 0.f;
+      float rcp = scale > 0.f ? __frcp_rn(scale) : 0.f;
+      if (!(bad == 0.f)) scale = __int_as_float(0x7fc00000), rcp = 0.f;
+      const bool live_row = rcp > 0.f;
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+      if (live_row) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = cache_code4<kType>(f + 4 * i, scale, rcp);
+      }
+      uint8_t *dst = static_cast<uint8_t *>(pool) + row * HD;
+      *reinterpret_cast<uint2 *>(dst + col.x) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2 *>(dst + col.y) = make_uint2(w[2], w[3]);
+      if (chunk == 0) (is_v ? p.v_scale : p.k_scale)[row] = scale;
+    }
+  }
+}
+
+struct ReadParams {
+  const void *k_pool, *v_pool;
+  const float *k_scale, *v_scale;
+  const int64_t *slots;
+  uint16_t *k, *v;  // [T, H, d] contiguous
+  long long rows;   // T * H
+  int H;
+  long long num_slots;
+};
+
+// HD / 16 threads per row of k and of v: grid ceil(2 * rows * HD / 16 / 256).
+template <int HD, int kType>
+__global__ void __launch_bounds__(256) fa_cache_read_kernel(const ReadParams p) {
+  constexpr int kChunks = HD / 16;
+  const long long gt = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  const int chunk = static_cast<int>(gt % kChunks);
+  long long r = gt / kChunks;
+  if (r >= 2 * p.rows) return;
+  const bool is_v = r >= p.rows;
+  if (is_v) r -= p.rows;
+  const long long m = r / p.H;
+  const int h = static_cast<int>(r % p.H);
+  long long slot = p.slots[m];
+  if (slot >= p.num_slots) {
+    if (chunk == 0) atomicExch(&g_device_status, 1 /* FA_ERR_INVALID_ARG */);
+    slot = -1;
+  }
+  float f[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) f[i] = 0.f;
+  if (slot >= 0) {
+    const long long row = (slot / kCachePage * p.H + h) * kCachePage + slot % kCachePage;
+    const void *pool = is_v ? p.v_pool : p.k_pool;
+    if constexpr (kType == kCacheBf16) {
+      const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(pool) + row * HD + 16 * chunk;
+      load8(src, f);
+      load8(src + 8, f + 8);
+    } else {
+      const float scale = (is_v ? p.v_scale : p.k_scale)[row];
+      const uint4 c = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(pool) + row * HD + 16 * chunk);
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t b = (w[i / 4] >> (8 * (i % 4))) & 0xffu;
+        float y;
+        if constexpr (kType == kCacheE4m3) {
+          __nv_fp8_e4m3 e;
+          e.__x = static_cast<__nv_fp8_storage_t>(b);
+          y = static_cast<float>(e);
+        } else {
+          y = static_cast<float>(static_cast<int8_t>(b));
+        }
+        f[i] = y * scale;
+      }
+    }
+  }
+  uint16_t *dst = (is_v ? p.v : p.k) + r * HD + 16 * chunk;
+  store8(reinterpret_cast<__nv_bfloat16 *>(dst), f);
+  store8(reinterpret_cast<__nv_bfloat16 *>(dst + 8), f + 8);
+}
+
+}  // namespace fa

@@ -1,6 +1,7 @@
 // fa_lib.cu -- the C ABI declared in include/fa.h: argument checks, TMA descriptors, launches.
 // Host code only decides shapes and launches; every step of the attention itself runs in the
-// kernels of fa_prefill.cuh, fa_backward.cuh, fa_decode.cuh and fa_merge.cuh.
+// kernels of fa_prefill.cuh, fa_backward.cuh, fa_decode.cuh, fa_merge.cuh, fa_rope.cuh, fa_cache.cuh
+// and fa_q8.cuh.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -9,6 +10,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 #include <cstring>
 #include <mutex>
 #include <string>
@@ -16,9 +18,12 @@
 
 #include "fa.h"
 #include "fa_backward.cuh"
+#include "fa_cache.cuh"
 #include "fa_decode.cuh"
 #include "fa_merge.cuh"
 #include "fa_prefill.cuh"
+#include "fa_q8.cuh"
+#include "fa_rope.cuh"
 
 namespace fa {
 // One thread waits on a barrier that nothing arrives at; the bounded wait must give up.
@@ -87,6 +92,7 @@ struct DeviceInfo {
   int num_sms = 0;
   bool prefill_attr[6] = {};  // (d = 64, 128) x (square, paged, key range)
   bool bwd_attr[2] = {false, false};                    // d = 64, 128
+  bool q8_attr[8] = {};  // (d = 64, 128) x (8, 16 rows) x (e4m3, int8)
 };
 
 std::mutex g_mutex;
@@ -981,5 +987,448 @@ fa_status fa_fwd_schedule(int B, int H, int N, int d, int num_ctas, int *start, 
 }
 
 int fa_version(void) { return kVersion; }
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------------------------
+// Rotary positions, the 8-bit paged cache, and the attention that reads it.
+// ---------------------------------------------------------------------------------------------
+namespace {
+
+bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// The rotation's arguments: rot = 0 turns nothing, and positions and freqs may then be null.
+fa_status check_rope(const int32_t *positions, const double *freqs, int rot, fa_rope_layout layout,
+                     float amplitude, int d, int inverse, fa::RopeTable *out) {
+  if (rot < 0 || rot > d || rot % 16 != 0) return FA_ERR_INVALID_ARG;
+  if (layout != FA_ROPE_HALF && layout != FA_ROPE_INTERLEAVED) return FA_ERR_INVALID_ARG;
+  if (inverse != 0 && inverse != 1) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(amplitude)) return FA_ERR_INVALID_ARG;
+  if (rot > 0 && (!positions || !freqs)) return FA_ERR_INVALID_ARG;
+  if (!aligned(positions, 4) || !aligned(freqs, 8)) return FA_ERR_ALIGNMENT;
+  *out = fa::RopeTable{freqs, rot, layout == FA_ROPE_INTERLEAVED, amplitude, inverse ? -1.f : 1.f};
+  return FA_OK;
+}
+
+// Tokens per CTA (as a power of two): about 1024 row chunks to a CTA, but no fewer than about four
+// CTAs per SM's worth of tokens, so that a decode step's few tokens spread over the GPU.
+int rope_log_tok(long long tokens, int rows_per_token, int d, int num_sms) {
+  int lg = 0;
+  const long long per_token = static_cast<long long>(rows_per_token) * (d / 16);
+  while (lg < 5 && (per_token << (lg + 1)) <= 1024 && (tokens >> (lg + 1)) >= 4LL * num_sms) ++lg;
+  return lg;
+}
+
+template <int HD>
+cudaError_t launch_rope(const fa::RopeParams &p, int in_f32, int out_f32, unsigned grid, cudaStream_t s) {
+  using bf = __nv_bfloat16;
+  if (in_f32 && out_f32) fa::fa_rope_kernel<HD, float, float><<<grid, fa::kRopeThreads, 0, s>>>(p);
+  else if (in_f32) fa::fa_rope_kernel<HD, float, bf><<<grid, fa::kRopeThreads, 0, s>>>(p);
+  else if (out_f32) fa::fa_rope_kernel<HD, bf, float><<<grid, fa::kRopeThreads, 0, s>>>(p);
+  else fa::fa_rope_kernel<HD, bf, bf><<<grid, fa::kRopeThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int HD>
+cudaError_t launch_append(const fa::AppendParams &p, fa_cache_type type, unsigned grid, cudaStream_t s) {
+  if (type == FA_CACHE_BF16) fa::fa_cache_append_kernel<HD, fa::kCacheBf16><<<grid, fa::kRopeThreads, 0, s>>>(p);
+  else if (type == FA_CACHE_E4M3) fa::fa_cache_append_kernel<HD, fa::kCacheE4m3><<<grid, fa::kRopeThreads, 0, s>>>(p);
+  else fa::fa_cache_append_kernel<HD, fa::kCacheInt8><<<grid, fa::kRopeThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int HD>
+cudaError_t launch_read(const fa::ReadParams &p, fa_cache_type type, unsigned grid, cudaStream_t s) {
+  if (type == FA_CACHE_BF16) fa::fa_cache_read_kernel<HD, fa::kCacheBf16><<<grid, 256, 0, s>>>(p);
+  else if (type == FA_CACHE_E4M3) fa::fa_cache_read_kernel<HD, fa::kCacheE4m3><<<grid, 256, 0, s>>>(p);
+  else fa::fa_cache_read_kernel<HD, fa::kCacheInt8><<<grid, 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+bool valid_cache(fa_cache_type t) { return t == FA_CACHE_BF16 || t == FA_CACHE_E4M3 || t == FA_CACHE_INT8; }
+
+// The pool's sides shared by the writer and the reader: pointers, scales (8-bit types only), sizes.
+fa_status check_pool(const void *k_pool, const void *v_pool, const float *k_scale, const float *v_scale,
+                     fa_cache_type type, int num_blocks, int Hk, int d) {
+  if (!valid_cache(type) || !k_pool || !v_pool) return FA_ERR_INVALID_ARG;
+  if (type != FA_CACHE_BF16 && (!k_scale || !v_scale)) return FA_ERR_INVALID_ARG;
+  if (num_blocks < 1 || Hk < 1) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  // pages of one head are numbered block * Hk + head in an int
+  if ((static_cast<long long>(num_blocks) + 1) * Hk > INT_MAX) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_scale) || !aligned16(v_scale))
+    return FA_ERR_ALIGNMENT;
+  return FA_OK;
+}
+
+// 8-bit pool [num_blocks, Hk, 16, d] as pages of one head, 16 x d bytes each, swizzled so that the
+// lanes' 16-byte reads of a page spread over the banks (128-byte rows at d = 128, 64 at d = 64).
+bool encode_pool_q8(CUtensorMap *map, const void *base, int d, long long pages) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), 16, static_cast<cuuint64_t>(pages)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(d) * 16};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(d), 16, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE,
+             d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How a call's rows and context are cut.  It depends on the arguments alone, so that the workspace
+// can be sized before the call.
+struct Q8Plan {
+  int R;            // rows of one key head: group * Lq
+  int nt;           // 8-row tiles of a CTA (1 or 2)
+  int row_tiles, n_split, split_pages;
+  size_t rows;      // S * Hq * Lq
+};
+
+constexpr int kQ8TargetCtas = 148 * 3 * 4;  // a few waves of the three CTAs that fit an SM
+constexpr int kQ8MinPages = 16;             // pages of a chunk: four to a warp
+
+bool q8_plan(int S, int Hq, int Hk, int Lq, int d, int max_blocks, Q8Plan *out) {
+  if (S < 1 || Hq < 1 || Hk < 1 || Hq % Hk != 0 || Lq < 1 || max_blocks < 1) return false;
+  if (d != 64 && d != 128) return false;
+  if (static_cast<long long>(S) * Hq * Lq > INT_MAX / 4) return false;
+  if (static_cast<long long>(max_blocks) * fa::kQ8Page > INT_MAX) return false;
+  Q8Plan p{};
+  p.R = Hq / Hk * Lq;
+  p.nt = p.R > 8 ? 2 : 1;
+  p.row_tiles = (p.R + 8 * p.nt - 1) / (8 * p.nt);
+  const long long units = static_cast<long long>(S) * Hk * p.row_tiles;
+  long long n = std::min<long long>((kQ8TargetCtas + units - 1) / units,
+                                    (max_blocks + kQ8MinPages - 1) / kQ8MinPages);
+  p.split_pages = static_cast<int>((max_blocks + n - 1) / n);
+  p.n_split = (max_blocks + p.split_pages - 1) / p.split_pages;
+  p.rows = static_cast<size_t>(S) * Hq * Lq;
+  if (units * p.n_split > INT_MAX) return false;
+  *out = p;
+  return true;
+}
+
+size_t q8_workspace(const Q8Plan &p, int d) {
+  return p.n_split > 1 ? p.rows * p.n_split * (d + 2) * sizeof(float) : 0;
+}
+
+template <int HD, int NT, int kType>
+fa_status launch_q8_stream(DeviceInfo &dev, const CUtensorMap &tk, const CUtensorMap &tv,
+                           const fa::Q8Params &p, cudaStream_t s) {
+  using C = fa::Q8Cfg<HD>;
+  const int slot = (HD == 128) * 4 + (NT == 2) * 2 + (kType == fa::kQ8Int8);
+  {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (!dev.q8_attr[slot]) {
+      cudaError_t e = cudaFuncSetAttribute(fa::fa_q8_stream_kernel<HD, NT, kType>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+      if (e != cudaSuccess) return launch_failed(e);
+      dev.q8_attr[slot] = true;
+    }
+  }
+  const unsigned grid = static_cast<unsigned>(p.n_split) * p.row_tiles * p.Hk * p.S;
+  fa::fa_q8_stream_kernel<HD, NT, kType><<<grid, fa::kQ8Threads, C::kSmem, s>>>(tk, tv, p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return launch_failed(e);
+  if (p.n_split > 1) {
+    const size_t threads = static_cast<size_t>(p.S) * p.Hk * p.R * (HD / 4);
+    fa::fa_q8_combine_kernel<HD><<<static_cast<unsigned>((threads + 127) / 128), 128, 0, s>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return launch_failed(e);
+  }
+  return FA_OK;
+}
+
+template <int HD>
+fa_status launch_q8(DeviceInfo &dev, const CUtensorMap &tk, const CUtensorMap &tv, const fa::Q8Params &p,
+                    int nt, fa_cache_type type, cudaStream_t s) {
+  if (type == FA_CACHE_E4M3)
+    return nt == 2 ? launch_q8_stream<HD, 2, fa::kQ8E4m3>(dev, tk, tv, p, s)
+                   : launch_q8_stream<HD, 1, fa::kQ8E4m3>(dev, tk, tv, p, s);
+  return nt == 2 ? launch_q8_stream<HD, 2, fa::kQ8Int8>(dev, tk, tv, p, s)
+                 : launch_q8_stream<HD, 1, fa::kQ8Int8>(dev, tk, tv, p, s);
+}
+
+fa_status q8_attention(const void *q, const void *k_pool, const void *v_pool, const float *k_scale,
+                       const float *v_scale, fa_cache_type type, const int32_t *block_table,
+                       int max_blocks_per_seq, const int32_t *seq_lens, int num_blocks,
+                       const uint64_t *tree_mask, void *o, fa_out_dtype o_dtype, float *lse, int S,
+                       int Hq, int Hk, int Lq, int d, int causal, float scale, void *workspace,
+                       size_t workspace_bytes, fa_stream_t stream) {
+  if (!q || !block_table || !seq_lens || !o) return FA_ERR_INVALID_ARG;
+  if (S < 1 || Hq < 1 || Lq < 1 || max_blocks_per_seq < 1) return FA_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
+  if (o_dtype != FA_OUT_BF16 && o_dtype != FA_OUT_F32) return FA_ERR_INVALID_ARG;
+  if (type != FA_CACHE_E4M3 && type != FA_CACHE_INT8) return FA_ERR_INVALID_ARG;
+  fa_status st = check_pool(k_pool, v_pool, k_scale, v_scale, type, num_blocks, Hk, d);
+  if (st != FA_OK) return st;
+  if (Lq > static_cast<long long>(max_blocks_per_seq) * fa::kQ8Page) return FA_ERR_INVALID_ARG;
+  Q8Plan plan;
+  if (!q8_plan(S, Hq, Hk, Lq, d, max_blocks_per_seq, &plan)) return FA_ERR_INVALID_ARG;
+  float sc;
+  if (!resolve_scale(scale, d, &sc)) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o)) return FA_ERR_ALIGNMENT;
+  if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4) || !aligned(tree_mask, 8))
+    return FA_ERR_ALIGNMENT;
+  const size_t need = q8_workspace(plan, d);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return FA_ERR_ALIGNMENT;
+  // nothing that is written may overlap anything that is read, or another output
+  const size_t o_bytes = plan.rows * d * (o_dtype == FA_OUT_F32 ? 4 : 2);
+  const size_t tokens = static_cast<size_t>(num_blocks) * Hk * fa::kQ8Page;
+  const void *ins[8] = {q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, tree_mask};
+  const size_t in_bytes[8] = {plan.rows * d * 2, tokens * d, tokens * d, tokens * 4, tokens * 4,
+                              static_cast<size_t>(S) * max_blocks_per_seq * 4, static_cast<size_t>(S) * 4,
+                              tree_mask ? static_cast<size_t>(S) * Lq * 8 : 0};
+  const void *outs[3] = {o, lse, workspace};
+  const size_t out_bytes[3] = {o_bytes, lse ? plan.rows * 4 : 0, need};
+  for (int a = 0; a < 3; ++a) {
+    if (out_bytes[a] == 0) continue;
+    for (int b = 0; b < 8; ++b)
+      if (in_bytes[b] && overlaps(outs[a], out_bytes[a], ins[b], in_bytes[b])) return FA_ERR_INVALID_ARG;
+    for (int b = a + 1; b < 3; ++b)
+      if (out_bytes[b] && overlaps(outs[a], out_bytes[a], outs[b], out_bytes[b])) return FA_ERR_INVALID_ARG;
+  }
+  DeviceInfo *dev = nullptr;
+  int dev_id = 0;
+  if ((st = current_device(&dev, &dev_id)) != FA_OK) return st;
+  CUtensorMap tk, tv;
+  const long long pages = static_cast<long long>(num_blocks) * Hk;
+  if (!encode_pool_q8(&tk, k_pool, d, pages) || !encode_pool_q8(&tv, v_pool, d, pages)) {
+    t_last_error = "cuTensorMapEncodeTiled failed";
+    return FA_ERR_LAUNCH;
+  }
+  fa::Q8Params p{};
+  p.q = static_cast<const uint16_t *>(q);
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.table = block_table;
+  p.lens = seq_lens;
+  p.tree = tree_mask;
+  p.o = o;
+  p.lse = lse;
+  p.ws_o = static_cast<float *>(workspace);
+  p.ws_ml = reinterpret_cast<float2 *>(static_cast<float *>(workspace) + plan.rows * plan.n_split * d);
+  p.S = S;
+  p.Hq = Hq;
+  p.Hk = Hk;
+  p.T = Lq;
+  p.R = plan.R;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.row_tiles = plan.row_tiles;
+  p.n_split = plan.n_split;
+  p.split_pages = plan.split_pages;
+  p.causal = causal;
+  p.o_f32 = o_dtype == FA_OUT_F32;
+  p.scale_log2 = sc * 1.4426950408889634f;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return d == 128 ? launch_q8<128>(*dev, tk, tv, p, plan.nt, type, s)
+                  : launch_q8<64>(*dev, tk, tv, p, plan.nt, type, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_rope(const void *q, const long long *q_strides, void *q_out,
+                  const long long *q_out_strides, const void *k, const long long *k_strides,
+                  void *k_out, const long long *k_out_strides, fa_out_dtype in_dtype,
+                  fa_out_dtype out_dtype, const int32_t *positions, long long pos_stride,
+                  const double *freqs, int rot, fa_rope_layout layout, float amplitude, int inverse,
+                  int B, int Hq, int Hk, int N, int d, fa_stream_t stream) {
+  if (B < 0 || N < 0 || Hq < 1 || Hk < 0) return FA_ERR_INVALID_ARG;
+  if (in_dtype != FA_OUT_BF16 && in_dtype != FA_OUT_F32) return FA_ERR_INVALID_ARG;
+  if (out_dtype != FA_OUT_BF16 && out_dtype != FA_OUT_F32) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (B == 0 || N == 0) return FA_OK;
+  fa::RopeParams p{};
+  const void *in[2] = {q, k};
+  void *out[2] = {q_out, k_out};
+  const long long *is[2] = {q_strides, k_strides}, *os[2] = {q_out_strides, k_out_strides};
+  const int heads[2] = {Hq, Hk};
+  const int in_unit = in_dtype == FA_OUT_F32 ? 4 : 8, out_unit = out_dtype == FA_OUT_F32 ? 4 : 8;
+  const long long extent[3] = {B, 0, N};
+  for (int i = 0; i < 2; ++i) {
+    if (heads[i] == 0) continue;
+    if (!in[i] || !out[i] || !is[i] || !os[i]) return FA_ERR_INVALID_ARG;
+    if (!aligned16(in[i]) || !aligned16(out[i])) return FA_ERR_ALIGNMENT;
+    p.x[i].in = in[i];
+    p.x[i].out = out[i];
+    p.x[i].H = heads[i];
+    for (int a = 0; a < 3; ++a) {
+      if (is[i][a] % in_unit || os[i][a] % out_unit) return FA_ERR_ALIGNMENT;
+      // rows of the output may not lie on one another
+      const long long n = a == 1 ? heads[i] : extent[a];
+      if (n > 1 && std::llabs(os[i][a]) < d) return FA_ERR_INVALID_ARG;
+      p.x[i].in_s[a] = is[i][a];
+      p.x[i].out_s[a] = os[i][a];
+    }
+  }
+  fa_status st = check_rope(positions, freqs, rot, layout, amplitude, d, inverse, &p.table);
+  if (st != FA_OK) return st;
+  p.positions = positions;
+  p.pos_stride = pos_stride;
+  p.N = N;
+  p.tokens = static_cast<long long>(B) * N;
+  if (p.tokens > INT_MAX || static_cast<long long>(Hq) + Hk > INT_MAX >> 5) return FA_ERR_INVALID_ARG;
+  DeviceInfo *dev = nullptr;
+  int dev_id = 0;
+  if ((st = current_device(&dev, &dev_id)) != FA_OK) return st;
+  p.log_tok = rope_log_tok(p.tokens, Hq + Hk, d, dev->num_sms);
+  const unsigned grid = static_cast<unsigned>((p.tokens + (1 << p.log_tok) - 1) >> p.log_tok);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int inf = in_dtype == FA_OUT_F32, outf = out_dtype == FA_OUT_F32;
+  cudaError_t e = d == 128 ? launch_rope<128>(p, inf, outf, grid, s) : launch_rope<64>(p, inf, outf, grid, s);
+  return e == cudaSuccess ? FA_OK : launch_failed(e);
+}
+
+fa_status fa_cache_append(const void *k, const long long *k_strides, const void *v,
+                          const long long *v_strides, void *k_pool, void *v_pool, float *k_scale,
+                          float *v_scale, fa_cache_type type, const int64_t *slots, int num_blocks,
+                          const void *q, const long long *q_strides, void *q_out,
+                          const long long *q_out_strides, const int32_t *positions,
+                          const double *freqs, int rot, fa_rope_layout layout, float amplitude,
+                          int T, int Hq, int Hk, int d, fa_stream_t stream) {
+  if (T < 0 || Hq < 0) return FA_ERR_INVALID_ARG;
+  fa_status st = check_pool(k_pool, v_pool, k_scale, v_scale, type, num_blocks, Hk, d);
+  if (st != FA_OK) return st;
+  fa::AppendParams p{};
+  st = check_rope(positions, freqs, rot, layout, amplitude, d, 0, &p.table);
+  if (T == 0) return FA_OK;
+  if (st != FA_OK) return st;
+  if (!k || !v || !slots || !k_strides || !v_strides) return FA_ERR_INVALID_ARG;
+  if (Hq > 0 && (!q || !q_out || !q_strides || !q_out_strides)) return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(Hq) + 2LL * Hk > INT_MAX >> 5) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned(slots, 8)) return FA_ERR_ALIGNMENT;
+  if (Hq > 0 && (!aligned16(q) || !aligned16(q_out))) return FA_ERR_ALIGNMENT;
+  const long long *strides[4] = {k_strides, v_strides, q_strides, q_out_strides};
+  long long *to[4] = {p.k_s, p.v_s, p.q_s, p.qo_s};
+  for (int i = 0; i < (Hq > 0 ? 4 : 2); ++i)
+    for (int a = 0; a < 2; ++a) {
+      if (strides[i][a] % 8) return FA_ERR_ALIGNMENT;
+      if (i == 3 && (a == 0 ? T : Hq) > 1 && std::llabs(strides[i][a]) < d) return FA_ERR_INVALID_ARG;
+      to[i][a] = strides[i][a];
+    }
+  p.q = static_cast<const uint16_t *>(q);
+  p.k = static_cast<const uint16_t *>(k);
+  p.v = static_cast<const uint16_t *>(v);
+  p.q_out = static_cast<uint16_t *>(q_out);
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.slots = slots;
+  p.positions = positions;
+  p.T = T;
+  p.Hq = Hq;
+  p.Hk = Hk;
+  p.num_slots = static_cast<long long>(num_blocks) * fa::kCachePage;
+  // the pools and scales are written: they may lie neither on one another nor on the inputs
+  const size_t rows = static_cast<size_t>(num_blocks) * Hk * fa::kCachePage;
+  const size_t pool_bytes = rows * d * (type == FA_CACHE_BF16 ? 2 : 1);
+  const size_t scale_bytes = type == FA_CACHE_BF16 ? 0 : rows * 4;
+  const void *outs[4] = {k_pool, v_pool, k_scale, v_scale};
+  const size_t out_bytes[4] = {pool_bytes, pool_bytes, scale_bytes, scale_bytes};
+  const void *ins[4] = {slots, positions, k, v};
+  const size_t in_bytes[4] = {static_cast<size_t>(T) * 8, rot ? static_cast<size_t>(T) * 4 : 0,
+                              static_cast<size_t>(d) * 2, static_cast<size_t>(d) * 2};
+  for (int a = 0; a < 4; ++a) {
+    if (out_bytes[a] == 0) continue;
+    for (int b = 0; b < 4; ++b)
+      if (in_bytes[b] && overlaps(outs[a], out_bytes[a], ins[b], in_bytes[b])) return FA_ERR_INVALID_ARG;
+    for (int b = a + 1; b < 4; ++b)
+      if (out_bytes[b] && overlaps(outs[a], out_bytes[a], outs[b], out_bytes[b])) return FA_ERR_INVALID_ARG;
+  }
+  DeviceInfo *dev = nullptr;
+  int dev_id = 0;
+  if ((st = current_device(&dev, &dev_id)) != FA_OK) return st;
+  p.log_tok = rope_log_tok(T, Hq + 2 * Hk, d, dev->num_sms);
+  const unsigned grid = static_cast<unsigned>((static_cast<long long>(T) + (1 << p.log_tok) - 1) >> p.log_tok);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = d == 128 ? launch_append<128>(p, type, grid, s) : launch_append<64>(p, type, grid, s);
+  return e == cudaSuccess ? FA_OK : launch_failed(e);
+}
+
+fa_status fa_cache_read(const void *k_pool, const void *v_pool, const float *k_scale,
+                        const float *v_scale, fa_cache_type type, const int64_t *slots,
+                        int num_blocks, void *k, void *v, int T, int H, int d, fa_stream_t stream) {
+  if (T < 0) return FA_ERR_INVALID_ARG;
+  fa_status st = check_pool(k_pool, v_pool, k_scale, v_scale, type, num_blocks, H, d);
+  if (st != FA_OK) return st;
+  if (T == 0) return FA_OK;
+  if (!slots || !k || !v) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned(slots, 8)) return FA_ERR_ALIGNMENT;
+  fa::ReadParams p{};
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.slots = slots;
+  p.k = static_cast<uint16_t *>(k);
+  p.v = static_cast<uint16_t *>(v);
+  p.rows = static_cast<long long>(T) * H;
+  p.H = H;
+  p.num_slots = static_cast<long long>(num_blocks) * fa::kCachePage;
+  const long long blocks = (2 * p.rows * (d / 16) + 255) / 256;
+  if (blocks > INT_MAX) return FA_ERR_INVALID_ARG;
+  const size_t out_bytes = static_cast<size_t>(p.rows) * d * 2;
+  const size_t rows = static_cast<size_t>(num_blocks) * H * fa::kCachePage;
+  const size_t pool_bytes = rows * d * (type == FA_CACHE_BF16 ? 2 : 1);
+  const void *ins[5] = {k_pool, v_pool, k_scale, v_scale, slots};
+  const size_t scale_bytes = type == FA_CACHE_BF16 ? 0 : rows * 4;
+  const size_t in_bytes[5] = {pool_bytes, pool_bytes, scale_bytes, scale_bytes, static_cast<size_t>(T) * 8};
+  for (int b = 0; b < 5; ++b)
+    if (in_bytes[b] && (overlaps(k, out_bytes, ins[b], in_bytes[b]) || overlaps(v, out_bytes, ins[b], in_bytes[b])))
+      return FA_ERR_INVALID_ARG;
+  if (overlaps(k, out_bytes, v, out_bytes)) return FA_ERR_INVALID_ARG;
+  DeviceInfo *dev = nullptr;
+  int dev_id = 0;
+  if ((st = current_device(&dev, &dev_id)) != FA_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const unsigned grid = static_cast<unsigned>(blocks);
+  cudaError_t e = d == 128 ? launch_read<128>(p, type, grid, s) : launch_read<64>(p, type, grid, s);
+  return e == cudaSuccess ? FA_OK : launch_failed(e);
+}
+
+size_t fa_q8_workspace_size(int S, int Hq, int Hk, int Lq, int d, int max_blocks_per_seq) {
+  Q8Plan plan;
+  return q8_plan(S, Hq, Hk, Lq, d, max_blocks_per_seq, &plan) ? q8_workspace(plan, d) : 0;
+}
+
+fa_status fa_decode_paged_q8(const void *q, const void *k_pool, const void *v_pool,
+                             const float *k_scale, const float *v_scale, fa_cache_type type,
+                             const int32_t *block_table, int max_blocks_per_seq,
+                             const int32_t *seq_lens, int num_blocks, void *o, fa_out_dtype o_dtype,
+                             float *lse, int S, int Hq, int Hk, int d, float scale, void *workspace,
+                             size_t workspace_bytes, fa_stream_t stream) {
+  return q8_attention(q, k_pool, v_pool, k_scale, v_scale, type, block_table, max_blocks_per_seq,
+                      seq_lens, num_blocks, nullptr, o, o_dtype, lse, S, Hq, Hk, 1, d, 0, scale,
+                      workspace, workspace_bytes, stream);
+}
+
+fa_status fa_prefill_paged_q8(const void *q, const void *k_pool, const void *v_pool,
+                              const float *k_scale, const float *v_scale, fa_cache_type type,
+                              const int32_t *block_table, int max_blocks_per_seq,
+                              const int32_t *seq_lens, int num_blocks, void *o,
+                              fa_out_dtype o_dtype, float *lse, int S, int Hq, int Hk, int Lq, int d,
+                              int causal, float scale, void *workspace, size_t workspace_bytes,
+                              fa_stream_t stream) {
+  return q8_attention(q, k_pool, v_pool, k_scale, v_scale, type, block_table, max_blocks_per_seq,
+                      seq_lens, num_blocks, nullptr, o, o_dtype, lse, S, Hq, Hk, Lq, d, causal,
+                      scale, workspace, workspace_bytes, stream);
+}
+
+fa_status fa_tree_attention_q8(const void *q, const void *k_pool, const void *v_pool,
+                               const float *k_scale, const float *v_scale, fa_cache_type type,
+                               const int32_t *block_table, int max_blocks_per_seq,
+                               const int32_t *seq_lens, int num_blocks, const uint64_t *tree_mask,
+                               void *o, fa_out_dtype o_dtype, float *lse, int S, int Hq, int Hk,
+                               int T, int d, float scale, void *workspace, size_t workspace_bytes,
+                               fa_stream_t stream) {
+  if (!tree_mask || T < 1 || T > 64) return FA_ERR_INVALID_ARG;
+  return q8_attention(q, k_pool, v_pool, k_scale, v_scale, type, block_table, max_blocks_per_seq,
+                      seq_lens, num_blocks, tree_mask, o, o_dtype, lse, S, Hq, Hk, T, d, 0, scale,
+                      workspace, workspace_bytes, stream);
+}
 
 }  // extern "C"

@@ -1,0 +1,493 @@
+// fa_q8.cuh -- attention of few queries per sequence over an 8-bit paged cache (fa_cache.cuh), query
+// heads sharing key/value heads: the decode step, and any call whose rows are few.
+//
+// The rows of one (sequence, key head) are its group = Hq / Hk query heads times T queries, R in
+// all, numbered head * T + t: consecutive in q and o.  With K_j = ks_j k_j, V_j = vs_j v_j (codes k,
+// v, one scale per token) and everything in log2 units,
+//     s_rj = scale log2(e) ks_j (q_r . k_j),   p_rj = 2^(s_rj - m_r),
+//     O_r = sum_j (p_rj vs_j) v_j / sum_j p_rj,   LSE_r = ln 2 (m_r + log2 sum_j p_rj):
+// the codes go to the tensor cores exactly and the scales stay in fp32, the keys' on the scores and
+// the values' on the probabilities.  p vs is rounded to bf16 for the second product (at most 2^-8 of each, as the
+// 16-bit paths round p); sums and statistics are fp32.
+//
+// Bound: HBM.  Each warp walks its own pages (16 tokens of one head: 16 d bytes of K, as many of V,
+// 64 bytes of scales each), kept kStages ahead in shared memory by TMA; a chunk of the context
+// is shared by the kWarps warps of a CTA and its partials are merged in shared memory.  The scores
+// are computed transposed, S^T = K Q^T: 16 tokens are the rows and 8 query rows the columns of an
+// m16n8k16 product, so a group of up to 8 query heads costs one product per 16 features where the
+// direct form would pad the heads to 16.  O^T = V^T P^T likewise.  (The sm_100 tensor-core path
+// wants 64 or 128 rows per product; with 1 to 16 rows it would multiply padding, and its operands
+// would have to be converted through shared memory.)
+#pragma once
+#include "sm100_ptx.cuh"
+
+namespace fa {
+
+constexpr int kQ8Page = 16;
+constexpr int kQ8Warps = 4;
+constexpr int kQ8Threads = 32 * kQ8Warps;
+constexpr int kQ8Stages = 4;
+
+enum Q8Type { kQ8E4m3 = 1, kQ8Int8 = 2 };
+
+struct Q8Params {
+  const uint16_t *q;
+  const float *ks, *vs;  // [num_blocks, Hk, 16]
+  const int32_t *table, *lens;
+  const uint64_t *tree;  // [S, T] or null
+  void *o;
+  float *lse;
+  float *ws_o;    // [S * Hk * R, n_split, d]: sum of p vs v, in units of the partial's own maximum
+  float2 *ws_ml;  // [S * Hk * R, n_split]: m (log2 units) and the sum of p
+  int S, Hq, Hk, T, R;
+  int max_blocks, num_blocks;
+  int row_tiles, n_split, split_pages;
+  int causal, o_f32;
+  float scale_log2;
+};
+
+// ---- codes to bf16 pairs ---------------------------------------------------------------------
+// e4m3 seeeemmm moved to bf16's s0000eeee mmm0000 is the value times 2^-120, subnormals included;
+// int8 c is (128 + low 7 bits) - (128, or 256 when negative), both exact in bf16.
+// `lo` takes bytes 0 and 2 of the word, `hi` bytes 1 and 3.
+template <int kType>
+__device__ __forceinline__ uint32_t q8_cvt_aligned(uint32_t x) {
+  if constexpr (kType == kQ8E4m3) {  // codes in bytes 1 and 3
+    return (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
+  } else {  // codes in bytes 0 and 2
+    const uint32_t a = (x & 0x007f007fu) | 0x43004300u, b = (x & 0x00800080u) | 0x43004300u;
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+}
+template <int kType>
+__device__ __forceinline__ void q8_cvt4(uint32_t x, uint32_t &lo, uint32_t &hi) {
+  if constexpr (kType == kQ8E4m3) {
+    lo = q8_cvt_aligned<kType>(x << 8);
+    hi = q8_cvt_aligned<kType>(x);
+  } else {
+    lo = q8_cvt_aligned<kType>(x);
+    hi = q8_cvt_aligned<kType>(x >> 8);
+  }
+}
+// e4m3: q is multiplied by 2^64 (exact) so that q . k stays well above fp32's smallest normal; the
+// scores carry 2^(64 - 120), the probabilities take 2^96 and O then carries 2^(96 - 120).
+template <int kType> __device__ constexpr float q8_score_unit() { return kType == kQ8E4m3 ? 0x1p56f : 1.f; }
+template <int kType> __device__ constexpr float q8_p_unit() { return kType == kQ8E4m3 ? 0x1p96f : 1.f; }
+template <int kType> __device__ constexpr float q8_o_unit() { return kType == kQ8E4m3 ? 0x1p24f : 1.f; }
+
+__device__ __forceinline__ uint32_t q8_scale_q(uint32_t bf16x2) {
+  uint32_t r;  // times 2^64 in each half
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(bf16x2), "r"(0x5f805f80u));
+  return r;
+}
+
+__device__ __forceinline__ void mma_bf16_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                                 uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+__device__ __forceinline__ int q8_len(const Q8Params &p, int s) {
+  const int hi = p.max_blocks * kQ8Page;
+  int L = p.lens[s];
+  if (L <= 0) return 0;  // an empty slot of a padded batch
+  return L < p.T ? min(p.T, hi) : (L > hi ? hi : L);
+}
+
+template <int HD>
+struct Q8Cfg {
+  static constexpr int kSlab = kQ8Page * HD;              // bytes of one page of one head
+  static constexpr int kStage = 2 * kSlab;
+  static constexpr int kRing = kQ8Warps * kQ8Stages * kStage;
+  static constexpr int kScales = kQ8Warps * kQ8Stages * 2 * kQ8Page * 4;
+  static constexpr int kBars = kQ8Warps * kQ8Stages * 8;
+  static constexpr int kSmem = kRing + kScales + kBars + 1024;  // + alignment of the ring
+};
+
+// One CTA: one chunk of the context of one (sequence, key head), 8 NT query rows.
+template <int HD, int NT, int kType>
+__global__ void __launch_bounds__(kQ8Threads)
+    fa_q8_stream_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                        const Q8Params p) {
+  using C = Q8Cfg<HD>;
+  constexpr int kUnits = HD / 64;   // 16-byte units of a K row that one lane takes
+  constexpr int kVW = HD / 32;      // 4-byte words of a V row that one lane takes
+  constexpr int kMT = HD / 16;      // 16-feature tiles of O^T
+  constexpr int kRows = 8 * NT;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  float *scales = reinterpret_cast<float *>(ring + C::kRing);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(ring + C::kRing + C::kScales);
+  __shared__ int abort_flag;
+  __shared__ float sm_m[kQ8Warps][kRows], sm_l[kQ8Warps][kRows];
+
+  unsigned u = blockIdx.x;
+  const int split = u % p.n_split;
+  u /= p.n_split;
+  const int tile = u % p.row_tiles;
+  u /= p.row_tiles;
+  const int kh = u % p.Hk, s = u / p.Hk;
+  const int row0 = tile * kRows;
+  const size_t row_base = (static_cast<size_t>(s) * p.Hk + kh) * p.R;  // of q, o, lse, partials
+
+  const int L = q8_len(p, s);
+  const int nblk = (L + kQ8Page - 1) / kQ8Page;
+  const int pg0 = split * p.split_pages;
+  const int pg1 = min(nblk, pg0 + p.split_pages);
+  if (pg0 >= pg1 && !(split == 0 && p.n_split == 1)) return;  // past the sequence's end
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int g = lane / 4, c = lane % 4;
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    if (L != p.lens[s] && p.lens[s] > 0) atomicExch(&g_device_status, 1 /* FA_ERR_INVALID_ARG */);
+    for (int i = 0; i < kQ8Warps * kQ8Stages; ++i) mbar_init(bars + i, 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+
+  // q: column n = g of the score tile is row row0 + 8 nt + g; this lane holds the features that it
+  // reads of K (units kUnits c + i, words w), as (byte 0, byte 2) and (byte 1, byte 3) pairs
+  uint32_t qb[NT][4 * kUnits][2];
+  int tq[NT][2];  // query index t of the two rows (columns 2c, 2c + 1) whose scores this lane holds
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int row = row0 + 8 * nt + g;
+    const uint16_t *src = p.q + (row_base + row) * HD + 16 * kUnits * c;
+#pragma unroll
+    for (int k = 0; k < 4 * kUnits; ++k) {
+      uint2 v = make_uint2(0u, 0u);
+      if (row < p.R) v = *reinterpret_cast<const uint2 *>(src + 4 * k);
+      qb[nt][k][0] = __byte_perm(v.x, v.y, 0x5410);  // features 0, 2
+      qb[nt][k][1] = __byte_perm(v.x, v.y, 0x7632);  // features 1, 3
+      if constexpr (kType == kQ8E4m3) {
+        qb[nt][k][0] = q8_scale_q(qb[nt][k][0]);
+        qb[nt][k][1] = q8_scale_q(qb[nt][k][1]);
+      }
+    }
+    tq[nt][0] = (row0 + 8 * nt + 2 * c) % p.T;
+    tq[nt][1] = (row0 + 8 * nt + 2 * c + 1) % p.T;
+  }
+  const float sc = p.scale_log2 * q8_score_unit<kType>();
+
+  float acc[NT][kMT][4];
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int j = 0; j < kMT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[nt][j][e] = 0.f;
+    m[nt][0] = m[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.f;
+  }
+
+  uint8_t *my_ring = ring + warp * kQ8Stages * C::kStage;
+  float *my_scales = scales + warp * kQ8Stages * 2 * kQ8Page;
+  uint64_t *my_bars = bars + warp * kQ8Stages;
+  const int32_t *trow = p.table + static_cast<size_t>(s) * p.max_blocks;
+  const int n_mine = pg1 - pg0 > warp ? (pg1 - pg0 - warp + kQ8Warps - 1) / kQ8Warps : 0;
+
+  // lane i holds the block of this warp's page (batch of 32) + i; bad entries become -1
+  int tab = -1;
+  auto fetch_table = [&](int first) {
+    tab = -1;
+    const int i = first + lane;
+    if (i < n_mine) {
+      tab = trow[pg0 + warp + kQ8Warps * i];
+      if (tab < 0 || tab >= p.num_blocks) {
+        atomicExch(&g_device_status, 1 /* FA_ERR_INVALID_ARG */);
+        tab = -1;
+      }
+    }
+  };
+  // page i's block is read from the table batch that holds it; a page left out (-1) loads block 0
+  auto issue = [&](int i, int blk) {
+    if (lane == 0) {
+      const int st = i % kQ8Stages;
+      const int page = max(blk, 0) * p.Hk + kh;
+      uint8_t *dst = my_ring + st * C::kStage;
+      float *sd = my_scales + st * 2 * kQ8Page;
+      mbar_arrive_expect_tx(my_bars + st, C::kStage + 2 * kQ8Page * 4);
+      tma_load_3d(dst, &tk, my_bars + st, 0, 0, page);
+      tma_load_3d(dst + C::kSlab, &tv, my_bars + st, 0, 0, page);
+      bulk_load_1d(sd, p.ks + static_cast<size_t>(page) * kQ8Page, kQ8Page * 4, my_bars + st);
+      bulk_load_1d(sd + kQ8Page, p.vs + static_cast<size_t>(page) * kQ8Page, kQ8Page * 4, my_bars + st);
+    }
+  };
+  // Blocks are fetched 32 pages at a time into `tab`, one batch ahead of the loads; `live` keeps a
+  // bit per stage for pages that the table really names.
+  fetch_table(0);
+  uint32_t live = 0;
+#pragma unroll 1
+  for (int i = 0; i < kQ8Stages; ++i) {
+    if (i < n_mine) {
+      const int blk = __shfl_sync(0xffffffffu, tab, i);
+      issue(i, blk);
+      if (blk >= 0) live |= 1u << i;
+    }
+  }
+
+#pragma unroll 1
+  for (int i = 0; i < n_mine; ++i) {
+    const int st = i % kQ8Stages;
+    if (!mbar_wait(my_bars + st, (i / kQ8Stages) & 1, &abort_flag)) break;
+    const uint8_t *kp = my_ring + st * C::kStage, *vp = kp + C::kSlab;
+    const float *sp = my_scales + st * 2 * kQ8Page;
+    const bool named = (live >> st) & 1;
+    const int tok0 = (pg0 + warp + kQ8Warps * i) * kQ8Page;
+
+    // K rows g and g + 8: unit kUnits c + i of a row lies at its swizzled place
+    uint4 kr[2][kUnits];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int k = 0; k < kUnits; ++k) {
+        const int row = g + 8 * r, unit = kUnits * c + k;
+        const int at = HD == 128 ? (unit ^ (row & 7)) : (unit ^ ((row >> 1) & 3));
+        kr[r][k] = *reinterpret_cast<const uint4 *>(kp + row * HD + 16 * at);
+      }
+    float kss[2], vss[2];
+    bool in[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      in[r] = named && tok0 + g + 8 * r < L;
+      kss[r] = in[r] ? sp[g + 8 * r] * sc : 0.f;
+      vss[r] = in[r] ? sp[kQ8Page + g + 8 * r] * q8_p_unit<kType>() : 0.f;
+    }
+    float sa[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sa[nt][e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      const uint32_t w0[4] = {kr[0][k].x, kr[0][k].y, kr[0][k].z, kr[0][k].w};
+      const uint32_t w1[4] = {kr[1][k].x, kr[1][k].y, kr[1][k].z, kr[1][k].w};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t a0, a1, a2, a3;
+        q8_cvt4<kType>(w0[w], a0, a2);
+        q8_cvt4<kType>(w1[w], a1, a3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_bf16_16x8x16(sa[nt], a0, a1, a2, a3, qb[nt][4 * k + w][0], qb[nt][4 * k + w][1]);
+      }
+    }
+    // V: tokens 2c, 2c+1, 2c+8, 2c+9, features (HD / 8) g ..
+    uint32_t vw[4][kVW];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 2 * c + (r & 1) + 8 * (r >> 1);
+      if constexpr (HD == 128) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(vp + row * HD + 16 * (g ^ (row & 7)));
+        vw[r][0] = x.x, vw[r][1] = x.y, vw[r][2] = x.z, vw[r][3] = x.w;
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2 *>(vp + row * HD + 16 * ((g >> 1) ^ ((row >> 1) & 3)) + 8 * (g & 1));
+        vw[r][0] = x.x, vw[r][1] = x.y;
+      }
+    }
+    __syncwarp();  // every lane has read the stage: refill it
+    {
+      const int next = i + kQ8Stages;
+      if ((next & 31) == 0) fetch_table(next);
+      const int blk = __shfl_sync(0xffffffffu, tab, next & 31);
+      live &= ~(1u << st);
+      if (next < n_mine) {
+        issue(next, blk);
+        if (blk >= 0) live |= 1u << st;
+      }
+    }
+
+    // scores: sa[nt][2 r + e] is token g + 8 r against query row 8 nt + 2 c + e
+    // the page reaches the queries' own tokens, where the masks apply
+    const bool edge = (p.causal || p.tree) && tok0 + kQ8Page > L - p.T;
+    float pm[NT][2];
+    bool grow = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float x = sa[nt][2 * r + e] * kss[r];
+          bool see = in[r];
+          if (edge) {
+            const int v = tok0 + g + 8 * r - (L - p.T);  // the token's place among the queries
+            if (v >= 0 && see) {
+              if (p.tree) see = (p.tree[static_cast<size_t>(s) * p.T + tq[nt][e]] >> (v & 63)) & 1;
+              else if (p.causal) see = v <= tq[nt][e];
+            }
+          }
+          // a NaN score counts as +inf, which makes its row NaN through inf - inf below
+          sa[nt][2 * r + e] = !see ? -INFINITY : x == x ? x : INFINITY;
+        }
+      pm[nt][0] = fmaxf(sa[nt][0], sa[nt][2]);
+      pm[nt][1] = fmaxf(sa[nt][1], sa[nt][3]);
+      grow = grow || pm[nt][0] > m[nt][0] + 8.f || pm[nt][1] > m[nt][1] + 8.f;
+    }
+    // the reference m moves only when a score passes it by 2^8: p stays below 2^8 meanwhile, and
+    // O / l does not depend on it
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = pm[nt][e];
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+          const float mn = fmaxf(m[nt][e], x);
+          const float a = mn == -INFINITY ? 1.f : ex2(m[nt][e] - mn);
+          m[nt][e] = mn;
+          l[nt][e] *= a;
+#pragma unroll
+          for (int j = 0; j < kMT; ++j) {
+            acc[nt][j][e] *= a;
+            acc[nt][j][2 + e] *= a;
+          }
+        }
+    }
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float pv[4];
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float x = sa[nt][2 * r + e];
+          // a token that this row does not see: no part in the sums, whatever its scales are
+          const float w = x == -INFINITY ? 0.f : ex2(x - m[nt][e]);
+          l[nt][e] += w;
+          pv[2 * r + e] = x == -INFINITY ? 0.f : w * vss[r];
+        }
+      pb[nt][0] = movmatrix_trans(pack_bf16x2(pv[0], pv[1]));
+      pb[nt][1] = movmatrix_trans(pack_bf16x2(pv[2], pv[3]));
+    }
+#pragma unroll
+    for (int w = 0; w < kVW; ++w) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        constexpr uint32_t kPick[2] = {0x5410u, 0x7632u};  // two features of two tokens
+        uint32_t a0, a1, a2, a3;
+        q8_cvt4<kType>(__byte_perm(vw[0][w], vw[1][w], kPick[half]), a0, a1);
+        q8_cvt4<kType>(__byte_perm(vw[2][w], vw[3][w], kPick[half]), a2, a3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_bf16_16x8x16(acc[nt][2 * w + half], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+      }
+    }
+  }
+
+  // merge the warps: lanes of the same c hold the same rows, their l parts over different tokens
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float x = l[nt][e];
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+      if (g == 0) {
+        sm_m[warp][8 * nt + 2 * c + e] = m[nt][e];
+        sm_l[warp][8 * nt + 2 * c + e] = x;
+      }
+    }
+  __syncthreads();  // (every warp has consumed its own loads: the ring is free)
+  float *part = reinterpret_cast<float *>(ring);  // [warp][row][HD]
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int row = 8 * nt + 2 * c + e;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kQ8Warps; ++w) M = fmaxf(M, sm_m[w][row]);
+      const float f = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - M) * q8_o_unit<kType>();
+      float *dst = part + (warp * kRows + row) * HD + (HD / 8) * g;
+#pragma unroll
+      for (int j = 0; j < kMT; ++j) {
+        // a warp without a visible token has sums of 0: leave them out of a NaN's way
+        dst[2 * j] = f == 0.f ? 0.f : acc[nt][j][e] * f;
+        dst[2 * j + 1] = f == 0.f ? 0.f : acc[nt][j][2 + e] * f;
+      }
+    }
+  __syncthreads();
+  constexpr int kPer = HD / 4;  // threads per row, 4 features each
+  for (int i = threadIdx.x; i < kRows * kPer; i += kQ8Threads) {
+    const int row = i / kPer, e0 = 4 * (i % kPer);
+    if (row0 + row >= p.R) continue;
+    float M = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kQ8Warps; ++w) M = fmaxf(M, sm_m[w][row]);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kQ8Warps; ++w) {
+      if (sm_m[w][row] != -INFINITY) sum += ex2(sm_m[w][row] - M) * sm_l[w][row];
+      const float4 x = *reinterpret_cast<const float4 *>(part + (w * kRows + row) * HD + e0);
+      a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+    }
+    const size_t out = row_base + row0 + row;
+    if (p.n_split > 1) {
+      *reinterpret_cast<float4 *>(p.ws_o + (out * p.n_split + split) * HD + e0) = a;
+      if (e0 == 0) p.ws_ml[out * p.n_split + split] = make_float2(M, sum);
+      continue;
+    }
+    const float inv = M == -INFINITY ? 0.f : 1.f / sum;
+    if (p.o_f32) {
+      *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + out * HD + e0) =
+          make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+    } else {
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + out * HD + e0) =
+          make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+    }
+    if (e0 == 0 && p.lse) p.lse[out] = M == -INFINITY ? -INFINITY : (M + lg2(sum)) * 0.6931471805599453f;
+  }
+}
+
+// Joins the chunks of every row: M = max m_c, l = sum 2^(m_c - M) l_c, O = sum 2^(m_c - M) O_c / l.
+// HD / 4 threads per row; a chunk without a visible token has m = -inf and weight 0.
+template <int HD>
+__global__ void __launch_bounds__(128) fa_q8_combine_kernel(const Q8Params p) {
+  constexpr int kPer = HD / 4;
+  const size_t gt = static_cast<size_t>(blockIdx.x) * 128 + threadIdx.x;
+  const size_t row = gt / kPer;
+  if (row >= static_cast<size_t>(p.S) * p.Hk * p.R) return;
+  const int e0 = 4 * static_cast<int>(gt % kPer);
+  const int s = static_cast<int>(row / (static_cast<size_t>(p.Hk) * p.R));
+  const int nblk = (q8_len(p, s) + kQ8Page - 1) / kQ8Page;
+  const int n = (nblk + p.split_pages - 1) / p.split_pages;
+  const float2 *ml = p.ws_ml + row * p.n_split;
+  const float *po = p.ws_o + row * p.n_split * HD + e0;
+  float M = -INFINITY;
+  for (int i = 0; i < n; ++i) M = fmaxf(M, ml[i].x);
+  float sum = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < n; ++i) {
+    const float2 x = ml[i];
+    if (x.x == -INFINITY) continue;
+    const float f = ex2(x.x - M);
+    const float4 v = *reinterpret_cast<const float4 *>(po + static_cast<size_t>(i) * HD);
+    sum = fmaf(f, x.y, sum);
+    a.x = fmaf(f, v.x, a.x), a.y = fmaf(f, v.y, a.y), a.z = fmaf(f, v.z, a.z), a.w = fmaf(f, v.w, a.w);
+  }
+  const float inv = M == -INFINITY ? 0.f : 1.f / sum;
+  if (p.o_f32) {
+    *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + row * HD + e0) =
+        make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+  } else {
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + row * HD + e0) =
+        make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+  }
+  if (e0 == 0 && p.lse) p.lse[row] = M == -INFINITY ? -INFINITY : (M + lg2(sum)) * 0.6931471805599453f;
+}
+
+}  // namespace fa

@@ -44,7 +44,7 @@ typedef enum {
     FA_ERR_ALIGNMENT = 3,   /* a pointer is not 16-byte aligned                                  */
     FA_ERR_LAUNCH = 4,      /* the CUDA launch failed; fa_last_error_string() has the CUDA text  */
     FA_ERR_TIMEOUT = 5,     /* a kernel gave up waiting (reported by fa_get_device_status)       */
-    FA_ERR_WORKSPACE = 6    /* a workspace is NULL or smaller than required (decode, backward)   */
+    FA_ERR_WORKSPACE = 6    /* a workspace is NULL or smaller than required                      */
 } fa_status;
 
 typedef enum {
@@ -274,6 +274,157 @@ fa_status fa_decode_paged_noalloc(const void *q, const void *k_pool, const void 
                                   const int32_t *seq_lens, int num_blocks, void *o,
                                   fa_out_dtype o_dtype, float *lse, int S, int H, int d,
                                   float scale, fa_stream_t stream);
+
+/*
+ * fa_rope -- rotary positions: q and k rows turned by their tokens' positions, before attention.
+ * No counterpart in the paper: the attention entry points take q and k as they are, and this is
+ * the step in front of them (and, with inverse = 1, the one behind fa_bwd).
+ *
+ * Every pair (a, b) of a row's first `rot` features turns by theta = position * freqs[j]:
+ *     y_a = amplitude (x_a cos theta - x_b sin theta),  y_b = amplitude (x_b cos theta + x_a sin theta);
+ * pair j is features (j, j + rot/2) in FA_ROPE_HALF and (2j, 2j + 1) in FA_ROPE_INTERLEAVED.  The
+ * other d - rot features pass through.  inverse = 1 turns by -theta, with the same amplitude: the
+ * transpose, which takes the gradients of the rotated q and k to those of q and k.  theta is formed
+ * in fp64 and the rotation in fp32; results are rounded once.
+ *
+ *   q, q_out       [B, Hq, N, d] with element strides of b, h and n in q_strides[3] and
+ *                  q_out_strides[3] (host arrays), features contiguous: a projection's
+ *                  [B, N, heads, d] is read and attention's [B, H, N, d] written without a copy, or
+ *                  the other way round.  Input and output may be the same tensor (same pointer,
+ *                  strides and type); otherwise they must not overlap.  Output strides of a
+ *                  dimension longer than 1 are at least d in magnitude.
+ *   k, k_out       the same with Hk heads (Hk = 0: none, pointers ignored).
+ *   in_dtype, out_dtype   bf16 or fp32, for q and k alike.
+ *   positions      int32, device: position of (b, n) at positions[b * pos_stride + n] (pos_stride 0:
+ *                  one row for all b).  Any value.  May be null with rot = 0.
+ *   freqs          double [rot / 2], device: radians per position.  May be null with rot = 0.
+ *   rot            a multiple of 16 in [0, d];  amplitude finite;  d: 64 or 128.
+ *   B, N >= 0 (nothing is launched for 0), B * N <= INT_MAX;  Hq >= 1, Hk >= 0.
+ * Pointers are 16-byte aligned and strides multiples of 16 bytes (else FA_ERR_ALIGNMENT).
+ * Returns FA_OK once the kernel is queued.
+ */
+typedef enum {
+    FA_ROPE_HALF = 0,       /* pairs (j, j + rot/2) */
+    FA_ROPE_INTERLEAVED = 1 /* pairs (2j, 2j + 1)   */
+} fa_rope_layout;
+
+fa_status fa_rope(const void *q, const long long *q_strides, void *q_out,
+                  const long long *q_out_strides, const void *k, const long long *k_strides,
+                  void *k_out, const long long *k_out_strides, fa_out_dtype in_dtype,
+                  fa_out_dtype out_dtype, const int32_t *positions, long long pos_stride,
+                  const double *freqs, int rot, fa_rope_layout layout, float amplitude, int inverse,
+                  int B, int Hq, int Hk, int N, int d, fa_stream_t stream);
+
+/*
+ * fa_cache_append -- writes new tokens' keys and values to their slots of the paged cache ("LLM
+ * study notes", paged attention), rotating the keys on the way and quantising where the pool is
+ * 8 bits wide; the same tokens' queries can be rotated beside them.
+ *
+ * Pools are [num_blocks, Hk, 16, d]; an 8-bit pool has scales fp32 [num_blocks, Hk, 16] beside it,
+ * one per token and head.  A row is stored as scale = max|x| / qmax (448 for e4m3, 127 for int8) and
+ * codes = the values nearest to x / scale, ties to even (both fp32 quotients, rounded to nearest);
+ * it stands for code * scale.  A row whose largest magnitude is below 2^-100 is stored as zeros with
+ * scale 0, one that holds an infinity or a NaN with scale NaN and codes 0.  A bf16 pool takes
+ * the rows rounded to bf16.  Keys are quantised from the fp32 result of the rotation.
+ *
+ *   k, v           bf16 [T, Hk, d] with element strides of token and head in k_strides[2],
+ *                  v_strides[2] (host arrays), features contiguous.
+ *   slots          int64 [T], device: block * 16 + row.  A negative slot writes nothing (padding);
+ *                  one past the pool writes nothing and is reported through fa_get_device_status
+ *                  (FA_ERR_INVALID_ARG).  Two tokens of a call must not name the same slot: what it
+ *                  then holds is some mixture of the two rows.
+ *   k_scale, v_scale   as above for FA_CACHE_E4M3 and FA_CACHE_INT8; ignored (may be null) for
+ *                  FA_CACHE_BF16.
+ *   q, q_out       bf16 [T, Hq, d] with strides as k (Hq = 0: none, pointers ignored); every token's
+ *                  q is rotated, padding too.  May be the same tensor.
+ *   positions      int32 [T], device;  freqs, rot, layout, amplitude as for fa_rope (rot = 0: no
+ *                  rotation, positions and freqs may be null).
+ *   T >= 0 (nothing is launched for 0), Hk >= 1, Hq >= 0;  d: 64 or 128;  (num_blocks + 1) * Hk <=
+ *   INT_MAX.  Slots that no token names are left as they are.
+ * Returns FA_OK once the kernel is queued.
+ */
+typedef enum {
+    FA_CACHE_BF16 = 0,
+    FA_CACHE_E4M3 = 1, /* 8-bit floating point, 4 exponent and 3 fraction bits, no infinities */
+    FA_CACHE_INT8 = 2  /* -127 .. 127                                                         */
+} fa_cache_type;
+
+fa_status fa_cache_append(const void *k, const long long *k_strides, const void *v,
+                          const long long *v_strides, void *k_pool, void *v_pool, float *k_scale,
+                          float *v_scale, fa_cache_type type, const int64_t *slots, int num_blocks,
+                          const void *q, const long long *q_strides, void *q_out,
+                          const long long *q_out_strides, const int32_t *positions,
+                          const double *freqs, int rot, fa_rope_layout layout, float amplitude,
+                          int T, int Hq, int Hk, int d, fa_stream_t stream);
+
+/*
+ * fa_cache_read -- reads rows of the paged cache back as bf16, in the order of a slot list: the
+ * inverse of fa_cache_append's quantisation (code * scale in fp32, rounded to bf16).
+ *
+ *   slots          int64 [T], device; a negative slot gives a row of zeros, one past the pool a row
+ *                  of zeros and FA_ERR_INVALID_ARG through fa_get_device_status.  Slots may repeat.
+ *   k, v           bf16 [T, H, d] contiguous; must not overlap the pools, scales or slots.
+ *   pools, scales, type, num_blocks, d   as for fa_cache_append, with H heads.  T >= 0.
+ * Returns FA_OK once the kernel is queued.
+ */
+fa_status fa_cache_read(const void *k_pool, const void *v_pool, const float *k_scale,
+                        const float *v_scale, fa_cache_type type, const int64_t *slots,
+                        int num_blocks, void *k, void *v, int T, int H, int d, fa_stream_t stream);
+
+/*
+ * fa_q8_workspace_size -- bytes of device workspace the three entry points below need for these
+ * sizes (Lq = 1 for decode, T for trees); 0 when they need none, and on invalid sizes.
+ */
+size_t fa_q8_workspace_size(int S, int Hq, int Hk, int Lq, int d, int max_blocks_per_seq);
+
+/*
+ * fa_decode_paged_q8, fa_prefill_paged_q8, fa_tree_attention_q8 -- fa_decode_paged,
+ * fa_prefill_paged and fa_tree_attention over an 8-bit cache written by fa_cache_append, with query
+ * heads sharing key/value heads: query head h reads key head h / (Hq / Hk).
+ *
+ *   q              bf16 [S, Hq, d] (decode) or [S, Hq, Lq, d], contiguous.
+ *   k_pool, v_pool   codes [num_blocks, Hk, 16, d];  k_scale, v_scale: fp32 [num_blocks, Hk, 16];
+ *                  all 16-byte aligned.  type: FA_CACHE_E4M3 or FA_CACHE_INT8.  A NaN scale makes
+ *                  its token NaN for the rows that see it; e4m3's own NaN codes (0x7f, 0xff), which
+ *                  fa_cache_append never writes, count as +-480.
+ *   block_table    int32 [S, max_blocks_per_seq], device; a page whose entry is outside
+ *                  [0, num_blocks) is left out and reported (FA_ERR_INVALID_ARG).
+ *   seq_lens       int32 [S], device, each in [Lq, 16 * max_blocks_per_seq], or <= 0 for an empty
+ *                  slot of a padded batch: its rows get O = 0, LSE = -inf.  Other lengths are
+ *                  clamped into the interval and reported.
+ *   causal, tree_mask, T, scale, o, o_dtype, lse   as for the 16-bit entry points.  A row that sees
+ *                  no token gets O = 0, LSE = -inf.
+ *   S, Hq, Hk, Lq >= 1, Hq a multiple of Hk;  d: 64 or 128;  S * Hq * Lq <= INT_MAX / 4;
+ *   (num_blocks + 1) * Hk <= INT_MAX.
+ *   workspace      device scratch of at least fa_q8_workspace_size(...) bytes, 16-byte aligned (may
+ *                  be null when that is 0); no initialisation needed, garbage afterwards.  Two calls
+ *                  in flight at once need separate workspaces.
+ * |q| must stay below 2^63 for the e4m3 type (it is scaled by 2^64 on the way).  Results do not
+ * depend on what else runs: there are no atomics in the sums.
+ * Returns FA_OK once the kernels are queued.
+ */
+fa_status fa_decode_paged_q8(const void *q, const void *k_pool, const void *v_pool,
+                             const float *k_scale, const float *v_scale, fa_cache_type type,
+                             const int32_t *block_table, int max_blocks_per_seq,
+                             const int32_t *seq_lens, int num_blocks, void *o, fa_out_dtype o_dtype,
+                             float *lse, int S, int Hq, int Hk, int d, float scale, void *workspace,
+                             size_t workspace_bytes, fa_stream_t stream);
+
+fa_status fa_prefill_paged_q8(const void *q, const void *k_pool, const void *v_pool,
+                              const float *k_scale, const float *v_scale, fa_cache_type type,
+                              const int32_t *block_table, int max_blocks_per_seq,
+                              const int32_t *seq_lens, int num_blocks, void *o,
+                              fa_out_dtype o_dtype, float *lse, int S, int Hq, int Hk, int Lq, int d,
+                              int causal, float scale, void *workspace, size_t workspace_bytes,
+                              fa_stream_t stream);
+
+fa_status fa_tree_attention_q8(const void *q, const void *k_pool, const void *v_pool,
+                               const float *k_scale, const float *v_scale, fa_cache_type type,
+                               const int32_t *block_table, int max_blocks_per_seq,
+                               const int32_t *seq_lens, int num_blocks, const uint64_t *tree_mask,
+                               void *o, fa_out_dtype o_dtype, float *lse, int S, int Hq, int Hk,
+                               int T, int d, float scale, void *workspace, size_t workspace_bytes,
+                               fa_stream_t stream);
 
 /*
  * fa_get_device_status -- synchronises `stream`, then reads and clears the library's device
