@@ -488,12 +488,47 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None
     return f.to(device), amplitude
 
 
+# A decode step makes these calls once per layer, so their own time counts.  Arguments are checked in
+# one expression each and explained only when it fails; the stream is read as a raw handle and the
+# device switched only when it is not the current one.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_stride_arrays: dict = {}
+
+
 def _strides(t, n):
-    return (ctypes.c_longlong * n)(*t.stride()[:n])
+    """The first n strides as a C array (shared by calls with the same strides, never written)."""
+    key = t.stride()[:n]
+    arr = _stride_arrays.get(key)
+    if arr is None:
+        if len(_stride_arrays) >= 4096:
+            _stride_arrays.clear()
+        arr = _stride_arrays[key] = (ctypes.c_longlong * n)(*key)
+    return arr
 
 
-def _require_rows(t, name, dims, dtypes, device=None):
+def _stream_on(index, stream):
+    if stream is not None:
+        return int(stream.cuda_stream)
+    if _raw_stream is not None:
+        return _raw_stream(index)
+    return int(torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on_device(index, where, fn, *args):
+    if torch.cuda.current_device() == index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args)
+    if st != 0:
+        raise FaError(st, where)
+
+
+def _require_rows(t, name, dims, dtypes, index=None):
     """A CUDA tensor whose last dimension is contiguous; the others may have any strides."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.dim() == dims
+            and (t.stride(-1) == 1 or t.numel() == 0) and (index is None or t.get_device() == index)):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
@@ -502,29 +537,37 @@ def _require_rows(t, name, dims, dtypes, device=None):
         raise ValueError(f"{name} must have {dims} dimensions")
     if t.numel() and t.stride(-1) != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}")
+    raise ValueError(f"{name} must be on cuda:{index}")
 
 
-def _require_on(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}")
+def _require_flat(t, name, dtype, shape, index=None):
+    """A contiguous CUDA tensor of the given type and shape (None: any), on the given device."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape) and (index is None or t.get_device() == index)):
+        return
+    _require(t, name, dtype)
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be on cuda:{index}")
 
 
-def _rope_args(freqs, positions, layout, device):
+def _rope_args(freqs, positions, layout, index):
     """(freqs pointer, rot, layout code) after the checks both rotating calls share."""
-    if layout not in _ROPE_LAYOUT:
+    code = _ROPE_LAYOUT.get(layout)
+    if code is None:
         raise ValueError("layout must be 'half' or 'interleaved'")
     if freqs is None:
-        return None, 0, _ROPE_LAYOUT[layout]
-    _require(freqs, "freqs", torch.float64)
+        return None, 0, code
+    _require_flat(freqs, "freqs", torch.float64, None, index)
     if freqs.dim() != 1:
         raise ValueError("freqs must be [rot / 2]")
     if positions is None:
         raise ValueError("positions are needed with freqs")
-    _require_on(device, freqs=freqs, positions=positions)
-    return freqs.data_ptr(), 2 * freqs.numel(), _ROPE_LAYOUT[layout]
+    return freqs.data_ptr(), 2 * freqs.numel(), code
+
+
+_ROPE_IO = (torch.bfloat16, torch.float32)
+_BF16 = (torch.bfloat16,)
 
 
 def fa_rope(q, k, positions, freqs, layout: str = "half", amplitude: float = 1.0,
@@ -537,72 +580,64 @@ def fa_rope(q, k, positions, freqs, layout: str = "half", amplitude: float = 1.0
     Returns (q_out, k_out): the tensors passed, which may be q and k themselves, or new contiguous
     [B, H, N, d] ones in out_dtype (default: the input's)."""
     lib = load_library()
-    io = (torch.bfloat16, torch.float32)
-    _require_rows(q, "q", 4, io)
-    dev = q.device
+    _require_rows(q, "q", 4, _ROPE_IO)
+    dev = q.get_device()
     B, Hq, N, d = q.shape
-    out_dtype = out_dtype or (q_out.dtype if q_out is not None else q.dtype)
+    if out_dtype is None:
+        out_dtype = q_out.dtype if q_out is not None else q.dtype
     out_code = _out_code(out_dtype)
+    if q_out is None:
+        q_out = q.new_empty((B, Hq, N, d), dtype=out_dtype)
+    else:
+        _require_rows(q_out, "q_out", 4, (out_dtype,), dev)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
     Hk, kp, ks, kop, kos = 0, None, None, None, None
     if k is not None:
         _require_rows(k, "k", 4, (q.dtype,), dev)
         Hk = k.shape[1]
         if k.shape != (B, Hk, N, d):
             raise ValueError("k must be [B, Hk, N, d] with q's B, N, d")
-    if q_out is None:
-        q_out = torch.empty((B, Hq, N, d), dtype=out_dtype, device=dev)
-    else:
-        _require_rows(q_out, "q_out", 4, (out_dtype,), dev)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-    if k is not None:
         if k_out is None:
-            k_out = torch.empty((B, Hk, N, d), dtype=out_dtype, device=dev)
+            k_out = q.new_empty((B, Hk, N, d), dtype=out_dtype)
         else:
             _require_rows(k_out, "k_out", 4, (out_dtype,), dev)
             if k_out.shape != k.shape:
                 raise ValueError("k_out must have k's shape")
         if Hk:
             kp, ks, kop, kos = k.data_ptr(), _strides(k, 3), k_out.data_ptr(), _strides(k_out, 3)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
     fptr, rot, code = _rope_args(freqs, positions, layout, dev)
     pos_ptr, pos_stride = None, 0
     if positions is not None:
-        _require(positions, "positions", torch.int32)
-        if positions.shape not in ((N,), (B, N)):
+        _require_flat(positions, "positions", torch.int32, None, dev)
+        pos_stride = N if positions.dim() == 2 else 0
+        if positions.shape != ((B, N) if positions.dim() == 2 else (N,)):
             raise ValueError("positions must be [N] or [B, N]")
-        pos_ptr, pos_stride = positions.data_ptr(), N if positions.dim() == 2 else 0
-    with torch.cuda.device(dev):
-        st = lib.fa_rope(q.data_ptr(), _strides(q, 3), q_out.data_ptr(), _strides(q_out, 3), kp, ks,
-                         kop, kos, _out_code(q.dtype), out_code, pos_ptr, pos_stride, fptr, rot,
-                         code, float(amplitude), int(inverse), B, Hq, Hk, N, d,
-                         _stream_handle(stream))
-    _check(st, "fa_rope")
+        pos_ptr = positions.data_ptr()
+    _on_device(dev, "fa_rope", lib.fa_rope, q.data_ptr(), _strides(q, 3), q_out.data_ptr(),
+               _strides(q_out, 3), kp, ks, kop, kos, _out_code(q.dtype), out_code, pos_ptr, pos_stride,
+               fptr, rot, code, float(amplitude), int(inverse), B, Hq, Hk, N, d, _stream_on(dev, stream))
     return q_out, k_out
 
 
 def _require_pools(k_pool, v_pool, k_scale, v_scale):
-    """(cache type code, num_blocks, heads, d, scale pointers) of a paged pool."""
-    for t, n in ((k_pool, "k_pool"), (v_pool, "v_pool")):
-        if not isinstance(t, torch.Tensor) or t.dtype not in _CACHE_TYPE:
-            raise ValueError(f"{n} must be a bfloat16, float8_e4m3fn or int8 tensor")
-        _require(t, n, t.dtype)
-    if k_pool.dim() != 4 or k_pool.shape[2] != 16 or v_pool.shape != k_pool.shape:
+    """(cache type code, num_blocks, heads, d, scale pointers, device index) of a paged pool."""
+    code = _CACHE_TYPE.get(getattr(k_pool, "dtype", None))
+    if code is None:
+        raise ValueError("k_pool must be a bfloat16, float8_e4m3fn or int8 tensor")
+    _require_flat(k_pool, "k_pool", k_pool.dtype, None)
+    if k_pool.dim() != 4 or k_pool.shape[2] != 16:
         raise ValueError("k_pool / v_pool must be [num_blocks, H, 16, d]")
-    if v_pool.dtype != k_pool.dtype:
-        raise ValueError("k_pool and v_pool must have one type")
     P, H, _, d = k_pool.shape
-    code = _CACHE_TYPE[k_pool.dtype]
-    ptrs = (None, None)
-    if code:
-        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            _require(t, n, torch.float32)
-            if t.shape != (P, H, 16):
-                raise ValueError(f"{n} must be [num_blocks, H, 16]")
-        ptrs = (k_scale.data_ptr(), v_scale.data_ptr())
-        _require_on(k_pool.device, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale)
-    else:
-        _require_on(k_pool.device, v_pool=v_pool)
-    return code, P, H, d, ptrs
+    index = k_pool.get_device()
+    _require_flat(v_pool, "v_pool", k_pool.dtype, k_pool.shape, index)
+    if not code:
+        return code, P, H, d, None, None, index
+    _require_flat(k_scale, "k_scale", torch.float32, (P, H, 16), index)
+    _require_flat(v_scale, "v_scale", torch.float32, (P, H, 16), index)
+    return code, P, H, d, k_scale.data_ptr(), v_scale.data_ptr(), index
 
 
 def fa_cache_append(k, v, k_pool, v_pool, slots, k_scale=None, v_scale=None, positions=None,
@@ -616,46 +651,38 @@ def fa_cache_append(k, v, k_pool, v_pool, slots, k_scale=None, v_scale=None, pos
     (float64 [rot / 2]) and positions (int32 [T]) the keys are rotated first, and q bf16 [T, Hq, d]
     beside them.  Returns q_out (new and contiguous unless passed), or None without q."""
     lib = load_library()
-    bf = (torch.bfloat16,)
-    code, P, Hk, d, (ksp, vsp) = _require_pools(k_pool, v_pool, k_scale, v_scale)
-    dev = k_pool.device
-    _require_rows(k, "k", 3, bf, dev)
-    _require_rows(v, "v", 3, bf, dev)
+    code, P, Hk, d, ksp, vsp, dev = _require_pools(k_pool, v_pool, k_scale, v_scale)
+    _require_rows(k, "k", 3, _BF16, dev)
+    _require_rows(v, "v", 3, _BF16, dev)
     T = k.shape[0]
     if k.shape != (T, Hk, d) or v.shape != k.shape:
         raise ValueError("k and v must be [T, Hk, d] with the pools' heads and features")
-    _require(slots, "slots", torch.int64)
-    if slots.shape != (T,):
-        raise ValueError("slots must be [T]")
-    _require_on(dev, slots=slots)
+    _require_flat(slots, "slots", torch.int64, (T,), dev)
     fptr, rot, lcode = _rope_args(freqs, positions, layout, dev)
+    pos_ptr = None
     if positions is not None:
-        _require(positions, "positions", torch.int32)
-        if positions.shape != (T,):
-            raise ValueError("positions must be [T]")
+        _require_flat(positions, "positions", torch.int32, (T,), dev)
+        pos_ptr = positions.data_ptr()
     Hq, qp, qs, qop, qos = 0, None, None, None, None
     if q is not None:
-        _require_rows(q, "q", 3, bf, dev)
+        _require_rows(q, "q", 3, _BF16, dev)
         Hq = q.shape[1]
         if q.shape != (T, Hq, d):
             raise ValueError("q must be [T, Hq, d]")
         if q_out is None:
-            q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+            q_out = q.new_empty((T, Hq, d))
         else:
-            _require_rows(q_out, "q_out", 3, bf, dev)
+            _require_rows(q_out, "q_out", 3, _BF16, dev)
             if q_out.shape != q.shape:
                 raise ValueError("q_out must have q's shape")
         if Hq:
             qp, qs, qop, qos = q.data_ptr(), _strides(q, 2), q_out.data_ptr(), _strides(q_out, 2)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    with torch.cuda.device(dev):
-        st = lib.fa_cache_append(k.data_ptr(), _strides(k, 2), v.data_ptr(), _strides(v, 2),
-                                 k_pool.data_ptr(), v_pool.data_ptr(), ksp, vsp, code,
-                                 slots.data_ptr(), P, qp, qs, qop, qos,
-                                 positions.data_ptr() if rot else None, fptr, rot, lcode,
-                                 float(amplitude), T, Hq, Hk, d, _stream_handle(stream))
-    _check(st, "fa_cache_append")
+    _on_device(dev, "fa_cache_append", lib.fa_cache_append, k.data_ptr(), _strides(k, 2), v.data_ptr(),
+               _strides(v, 2), k_pool.data_ptr(), v_pool.data_ptr(), ksp, vsp, code, slots.data_ptr(),
+               P, qp, qs, qop, qos, pos_ptr, fptr, rot, lcode, float(amplitude), T, Hq, Hk, d,
+               _stream_on(dev, stream))
     return q_out
 
 
@@ -664,29 +691,23 @@ def fa_cache_read(k_pool, v_pool, slots, k_scale=None, v_scale=None, k_out=None,
     """Read the rows at slots (int64 [T]; negative: zeros) of a paged cache back as bf16: returns
     (k, v), each [T, H, d].  Pools and scales as for fa_cache_append."""
     lib = load_library()
-    code, P, H, d, (ksp, vsp) = _require_pools(k_pool, v_pool, k_scale, v_scale)
-    dev = k_pool.device
-    _require(slots, "slots", torch.int64)
+    code, P, H, d, ksp, vsp, dev = _require_pools(k_pool, v_pool, k_scale, v_scale)
+    _require_flat(slots, "slots", torch.int64, None, dev)
     if slots.dim() != 1:
         raise ValueError("slots must be [T]")
-    _require_on(dev, slots=slots)
     T = slots.shape[0]
-    out = []
-    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is None:
-            t = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
-        else:
-            _require(t, n)
-            if t.shape != (T, H, d):
-                raise ValueError(f"{n} must be [T, H, d]")
-            _require_on(dev, **{n: t})
-        out.append(t)
-    with torch.cuda.device(dev):
-        st = lib.fa_cache_read(k_pool.data_ptr(), v_pool.data_ptr(), ksp, vsp, code,
-                               slots.data_ptr(), P, out[0].data_ptr(), out[1].data_ptr(), T, H, d,
-                               _stream_handle(stream))
-    _check(st, "fa_cache_read")
-    return out[0], out[1]
+    if k_out is None:
+        k_out = k_pool.new_empty((T, H, d), dtype=torch.bfloat16)
+    else:
+        _require_flat(k_out, "k_out", torch.bfloat16, (T, H, d), dev)
+    if v_out is None:
+        v_out = k_pool.new_empty((T, H, d), dtype=torch.bfloat16)
+    else:
+        _require_flat(v_out, "v_out", torch.bfloat16, (T, H, d), dev)
+    _on_device(dev, "fa_cache_read", lib.fa_cache_read, k_pool.data_ptr(), v_pool.data_ptr(), ksp, vsp,
+               code, slots.data_ptr(), P, k_out.data_ptr(), v_out.data_ptr(), T, H, d,
+               _stream_on(dev, stream))
+    return k_out, v_out
 
 
 def fa_q8_workspace_size(S: int, Hq: int, Hk: int, Lq: int, d: int, max_blocks_per_seq: int) -> int:
@@ -698,58 +719,51 @@ def fa_q8_workspace_size(S: int, Hq: int, Hk: int, Lq: int, d: int, max_blocks_p
 def _attend_q8(where, q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, tree_mask, causal,
                scale, out_dtype, out, lse, return_lse, workspace, stream):
     lib = load_library()
-    _require(q, "q")
-    code, P, Hk, d, (ksp, vsp) = _require_pools(k_pool, v_pool, k_scale, v_scale)
+    code, P, Hk, d, ksp, vsp, dev = _require_pools(k_pool, v_pool, k_scale, v_scale)
     if not code:
         raise ValueError("k_pool / v_pool must be float8_e4m3fn or int8")
-    if q.dim() != (3 if causal is None else 4):
+    _require_flat(q, "q", torch.bfloat16, None, dev)
+    shape = q.shape
+    if len(shape) != (3 if causal is None else 4):
         raise ValueError("q must be [S, Hq, d]" if causal is None else "q must be [S, Hq, Lq, d]")
-    S, Hq, Lq = q.shape[0], q.shape[1], 1 if causal is None else q.shape[2]
-    if q.shape[-1] != d or Hq % Hk:
+    S, Hq, Lq = shape[0], shape[1], 1 if causal is None else shape[2]
+    if shape[-1] != d or Hk == 0 or Hq % Hk:
         raise ValueError("q must have the pools' d and a multiple of their heads")
-    _require(block_table, "block_table", torch.int32)
-    _require(seq_lens, "seq_lens", torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] != S or seq_lens.shape != (S,):
-        raise ValueError("block_table must be [S, max_blocks] and seq_lens [S]")
-    dev = q.device
-    _require_on(dev, k_pool=k_pool, block_table=block_table, seq_lens=seq_lens, out=out, lse=lse,
-                workspace=workspace, tree_mask=tree_mask)
+    _require_flat(block_table, "block_table", torch.int32, None, dev)
+    if block_table.dim() != 2 or block_table.shape[0] != S:
+        raise ValueError("block_table must be [S, max_blocks]")
+    _require_flat(seq_lens, "seq_lens", torch.int32, (S,), dev)
+    if tree_mask is not None:
+        _require_flat(tree_mask, "tree_mask", torch.int64, (S, Lq), dev)
+    code_o = _out_code(out_dtype)
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=dev)
+        out = q.new_empty(shape, dtype=out_dtype)
     else:
-        _require(out, "out", out_dtype)
-        if out.shape != q.shape:
-            raise ValueError("out has the wrong shape")
-    if lse is None and return_lse:
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
-    elif lse is not None:
-        _require(lse, "lse", torch.float32)
-        if lse.shape != q.shape[:-1]:
-            raise ValueError("lse has the wrong shape")
+        _require_flat(out, "out", out_dtype, shape, dev)
+    if lse is not None:
+        _require_flat(lse, "lse", torch.float32, shape[:-1], dev)
+    elif return_lse:
+        lse = q.new_empty(shape[:-1], dtype=torch.float32)
     maxb = block_table.shape[1]
+    ws, ws_bytes = None, 0
     if workspace is None:
-        need = lib.fa_q8_workspace_size(S, Hq, Hk, Lq, d, maxb)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif not (workspace.is_cuda and workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    ws, ws_bytes = (None, 0) if workspace is None else (
-        workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        ws_bytes = lib.fa_q8_workspace_size(S, Hq, Hk, Lq, d, maxb)
+        if ws_bytes:
+            workspace = q.new_empty(ws_bytes, dtype=torch.uint8)
+            ws = workspace.data_ptr()
+    else:
+        _require_flat(workspace, "workspace", workspace.dtype, None, dev)
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     head = (q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), ksp, vsp, code,
             block_table.data_ptr(), maxb, seq_lens.data_ptr(), P)
-    tail = (out.data_ptr(), _out_code(out_dtype), lse.data_ptr() if lse is not None else None, S, Hq,
-            Hk)
-    sc = float(scale) if scale is not None else 0.0
-    with torch.cuda.device(dev):
-        sh = _stream_handle(stream)
-        if causal is None:
-            st = lib.fa_decode_paged_q8(*head, *tail, d, sc, ws, ws_bytes, sh)
-        elif tree_mask is not None:
-            st = lib.fa_tree_attention_q8(*head, tree_mask.data_ptr(), *tail, Lq, d, sc, ws, ws_bytes,
-                                          sh)
-        else:
-            st = lib.fa_prefill_paged_q8(*head, *tail, Lq, d, int(causal), sc, ws, ws_bytes, sh)
-    _check(st, where)
+    outs = (out.data_ptr(), code_o, None if lse is None else lse.data_ptr(), S, Hq, Hk)
+    tail = (0.0 if scale is None else float(scale), ws, ws_bytes, _stream_on(dev, stream))
+    if causal is None:
+        _on_device(dev, where, lib.fa_decode_paged_q8, *head, *outs, d, *tail)
+    elif tree_mask is not None:
+        _on_device(dev, where, lib.fa_tree_attention_q8, *head, tree_mask.data_ptr(), *outs, Lq, d, *tail)
+    else:
+        _on_device(dev, where, lib.fa_prefill_paged_q8, *head, *outs, Lq, d, int(causal), *tail)
     return out, lse
 
 
@@ -781,8 +795,7 @@ def fa_tree_attention_q8(q, k_pool, v_pool, k_scale, v_scale, block_table, seq_l
     """Tree verification over an 8-bit paged cache: q bf16 [S, Hq, T, d] holds the T <= 64 nodes, the
     last T cached tokens; tree_mask int64 [S, T] as for fa_tree_attention; the rest as for
     fa_decode_paged_q8.  Returns (o [S, Hq, T, d], lse fp32 [S, Hq, T] or None)."""
-    _require(tree_mask, "tree_mask", torch.int64)
-    if q.dim() != 4 or tree_mask.shape != (q.shape[0], q.shape[2]):
+    if tree_mask is None:
         raise ValueError("tree_mask must be [S, T]")
     return _attend_q8("fa_tree_attention_q8", q, k_pool, v_pool, k_scale, v_scale, block_table,
                       seq_lens, tree_mask, False, scale, out_dtype, out, lse, return_lse, workspace,

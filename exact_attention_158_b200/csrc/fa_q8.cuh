@@ -7,8 +7,12 @@
 //     s_rj = scale log2(e) ks_j (q_r . k_j),   p_rj = 2^(s_rj - m_r),
 //     O_r = sum_j (p_rj vs_j) v_j / sum_j p_rj,   LSE_r = ln 2 (m_r + log2 sum_j p_rj):
 // the codes go to the tensor cores exactly and the scales stay in fp32, the keys' on the scores and
-// the values' on the probabilities.  p vs is rounded to bf16 for the second product (at most 2^-8 of each, as the
-// 16-bit paths round p); sums and statistics are fp32.
+// the values' on the probabilities.  For the second product p vs is rounded to fp16 (2^-11, against
+// bf16's 2^-8); sums and statistics are fp32.
+// The reference m_r is chosen for that product: the largest s + log2 vs so far, so that the largest
+// p vs lies near 1 and fp16 loses 2^-25 of it at most, whatever the scales are.  It moves only when a
+// p vs passes 2^10 (fp16 ends at 2^16) or a p 2^100 (the fp32 sum; values of scale 0 set no
+// reference, so the scores hold one 2^64 below their own maximum).
 //
 // Bound: HBM.  Each warp walks its own pages (16 tokens of one head: 16 d bytes of K, as many of V,
 // 64 bytes of scales each), kept kStages ahead in shared memory by TMA; a chunk of the context
@@ -27,6 +31,8 @@ constexpr int kQ8Page = 16;
 constexpr int kQ8Warps = 4;
 constexpr int kQ8Threads = 32 * kQ8Warps;
 constexpr int kQ8Stages = 4;
+constexpr float kQ8MostPv = 0x1p10f, kQ8MostP = 0x1p100f;  // past these the reference moves
+constexpr float kQ8Slack = 64.f;                           // log2: p stays below 2^64 after a move
 
 enum Q8Type { kQ8E4m3 = 1, kQ8Int8 = 2 };
 
@@ -46,36 +52,53 @@ struct Q8Params {
   float scale_log2;
 };
 
-// ---- codes to bf16 pairs ---------------------------------------------------------------------
-// e4m3 seeeemmm moved to bf16's s0000eeee mmm0000 is the value times 2^-120, subnormals included;
-// int8 c is (128 + low 7 bits) - (128, or 256 when negative), both exact in bf16.
-// `lo` takes bytes 0 and 2 of the word, `hi` bytes 1 and 3.
+// ---- codes to 16-bit pairs -------------------------------------------------------------------
+// Keys, against bf16 queries: e4m3 seeeemmm moved to bf16's s0000eeee mmm0000 is the value times
+// 2^-120, subnormals included; int8 c is (128 + low 7 bits) - (128, or 256 when negative), both
+// exact in bf16.  Values, against fp16 weights: e4m3 moved to fp16's s0eeeemm m000000 is the value
+// times 2^-8; int8 c is fp16's 1024 + (c + 128) less 1152.
+// lo takes bytes 0 and 2 of the word, hi bytes 1 and 3.
+__device__ __forceinline__ uint32_t q8_bf16_e4m3(uint32_t x) {  // codes in bytes 1 and 3
+  return (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
+}
+__device__ __forceinline__ uint32_t q8_bf16_int8(uint32_t x) {  // codes in bytes 0 and 2
+  const uint32_t a = (x & 0x007f007fu) | 0x43004300u, b = (x & 0x00800080u) | 0x43004300u;
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t q8_fp16_e4m3(uint32_t x) {
+  return (x & 0x80008000u) | ((x >> 1) & 0x3f803f80u);
+}
+__device__ __forceinline__ uint32_t q8_fp16_int8(uint32_t x) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"((x & 0x00ff00ffu) ^ 0x64806480u), "r"(0x64806480u));
+  return r;
+}
 template <int kType>
-__device__ __forceinline__ uint32_t q8_cvt_aligned(uint32_t x) {
-  if constexpr (kType == kQ8E4m3) {  // codes in bytes 1 and 3
-    return (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
-  } else {  // codes in bytes 0 and 2
-    const uint32_t a = (x & 0x007f007fu) | 0x43004300u, b = (x & 0x00800080u) | 0x43004300u;
-    uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
+__device__ __forceinline__ void q8_key4(uint32_t x, uint32_t &lo, uint32_t &hi) {
+  if constexpr (kType == kQ8E4m3) {
+    lo = q8_bf16_e4m3(x << 8);
+    hi = q8_bf16_e4m3(x);
+  } else {
+    lo = q8_bf16_int8(x);
+    hi = q8_bf16_int8(x >> 8);
   }
 }
 template <int kType>
-__device__ __forceinline__ void q8_cvt4(uint32_t x, uint32_t &lo, uint32_t &hi) {
+__device__ __forceinline__ void q8_value4(uint32_t x, uint32_t &lo, uint32_t &hi) {
   if constexpr (kType == kQ8E4m3) {
-    lo = q8_cvt_aligned<kType>(x << 8);
-    hi = q8_cvt_aligned<kType>(x);
+    lo = q8_fp16_e4m3(x << 8);
+    hi = q8_fp16_e4m3(x);
   } else {
-    lo = q8_cvt_aligned<kType>(x);
-    hi = q8_cvt_aligned<kType>(x >> 8);
+    lo = q8_fp16_int8(x);
+    hi = q8_fp16_int8(x >> 8);
   }
 }
 // e4m3: q is multiplied by 2^64 (exact) so that q . k stays well above fp32's smallest normal; the
-// scores carry 2^(64 - 120), the probabilities take 2^96 and O then carries 2^(96 - 120).
+// scores then carry 2^(64 - 120), and O carries the values' 2^-8.
 template <int kType> __device__ constexpr float q8_score_unit() { return kType == kQ8E4m3 ? 0x1p56f : 1.f; }
-template <int kType> __device__ constexpr float q8_p_unit() { return kType == kQ8E4m3 ? 0x1p96f : 1.f; }
-template <int kType> __device__ constexpr float q8_o_unit() { return kType == kQ8E4m3 ? 0x1p24f : 1.f; }
+template <int kType> __device__ constexpr float q8_o_unit() { return kType == kQ8E4m3 ? 0x1p8f : 1.f; }
 
 __device__ __forceinline__ uint32_t q8_scale_q(uint32_t bf16x2) {
   uint32_t r;  // times 2^64 in each half
@@ -89,6 +112,18 @@ __device__ __forceinline__ void mma_bf16_16x8x16(float (&d)[4], uint32_t a0, uin
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_fp16_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                                 uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_fp16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t r;
@@ -112,6 +147,31 @@ struct Q8Cfg {
   static constexpr int kBars = kQ8Warps * kQ8Stages * 8;
   static constexpr int kSmem = kRing + kScales + kBars + 1024;  // + alignment of the ring
 };
+
+// ln 2 (M + log2 l).  M holds the values' log2 vs, which l undoes: l's exponent is added to M first
+// (small numbers of opposite sign), and only the fraction's logarithm is approximated.
+__device__ __forceinline__ float q8_lse(float M, float l) {
+  if (l == 0.f) return -INFINITY;
+  const int k = static_cast<int>((__float_as_uint(l) >> 23) & 0xffu) - 127;
+  if (k == -127 || k == 128) return (M + lg2(l)) * 0.6931471805599453f;  // not a normal number
+  const float f = __uint_as_float((__float_as_uint(l) & 0x007fffffu) | 0x3f800000u);
+  return ((M + static_cast<float>(k)) + lg2(f)) * 0.6931471805599453f;
+}
+
+// Four features of an output row from its sums: O = a / l, LSE = ln 2 (M + log2 l); a row that saw
+// no token has l = 0 and gets O = 0, LSE = -inf.
+template <int HD>
+__device__ __forceinline__ void q8_write4(const Q8Params &p, size_t row, int e0, const float4 &a, float M,
+                                          float l) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  if (p.o_f32)
+    *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + row * HD + e0) =
+        make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+  else
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + row * HD + e0) =
+        make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+  if (e0 == 0 && p.lse) p.lse[row] = q8_lse(M, l);
+}
 
 // One CTA: one chunk of the context of one (sequence, key head), 8 NT query rows.
 template <int HD, int NT, int kType>
@@ -262,7 +322,7 @@ __global__ void __launch_bounds__(kQ8Threads)
     for (int r = 0; r < 2; ++r) {
       in[r] = named && tok0 + g + 8 * r < L;
       kss[r] = in[r] ? sp[g + 8 * r] * sc : 0.f;
-      vss[r] = in[r] ? sp[kQ8Page + g + 8 * r] * q8_p_unit<kType>() : 0.f;
+      vss[r] = in[r] ? sp[kQ8Page + g + 8 * r] : 0.f;
     }
     float sa[NT][4];
 #pragma unroll
@@ -276,8 +336,8 @@ __global__ void __launch_bounds__(kQ8Threads)
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         uint32_t a0, a1, a2, a3;
-        q8_cvt4<kType>(w0[w], a0, a2);
-        q8_cvt4<kType>(w1[w], a1, a3);
+        q8_key4<kType>(w0[w], a0, a2);
+        q8_key4<kType>(w1[w], a1, a3);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
           mma_bf16_16x8x16(sa[nt], a0, a1, a2, a3, qb[nt][4 * k + w][0], qb[nt][4 * k + w][1]);
@@ -311,15 +371,13 @@ __global__ void __launch_bounds__(kQ8Threads)
     // scores: sa[nt][2 r + e] is token g + 8 r against query row 8 nt + 2 c + e
     // the page reaches the queries' own tokens, where the masks apply
     const bool edge = (p.causal || p.tree) && tok0 + kQ8Page > L - p.T;
-    float pm[NT][2];
-    bool grow = false;
+    float pv[NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float x = sa[nt][2 * r + e] * kss[r];
           bool see = in[r];
           if (edge) {
             const int v = tok0 + g + 8 * r - (L - p.T);  // the token's place among the queries
@@ -328,26 +386,49 @@ __global__ void __launch_bounds__(kQ8Threads)
               else if (p.causal) see = v <= tq[nt][e];
             }
           }
-          // a NaN score counts as +inf, which makes its row NaN through inf - inf below
-          sa[nt][2 * r + e] = !see ? -INFINITY : x == x ? x : INFINITY;
+          sa[nt][2 * r + e] = see ? sa[nt][2 * r + e] * kss[r] : -INFINITY;
         }
-      pm[nt][0] = fmaxf(sa[nt][0], sa[nt][2]);
-      pm[nt][1] = fmaxf(sa[nt][1], sa[nt][3]);
-      grow = grow || pm[nt][0] > m[nt][0] + 8.f || pm[nt][1] > m[nt][1] + 8.f;
-    }
-    // the reference m moves only when a score passes it by 2^8: p stays below 2^8 meanwhile, and
-    // O / l does not depend on it
-    if (__any_sync(0xffffffffu, grow)) {
+    float pw[NT][4];
+    auto weigh = [&]() {  // p and p vs against the present references; true when one passes its limit
+      bool over = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float x = sa[nt][2 * r + e];
+            // a token that this row does not see: no part in the sums, whatever its scales are
+            const float w = x == -INFINITY ? 0.f : ex2(x - m[nt][e]);
+            pw[nt][2 * r + e] = w;
+            pv[nt][2 * r + e] = x == -INFINITY ? 0.f : w * vss[r];
+            over = over || w > kQ8MostP || pv[nt][2 * r + e] > kQ8MostPv;
+          }
+      return over;
+    };
+    if (__any_sync(0xffffffffu, weigh())) {
+      const float lv[2] = {lg2(vss[0]), lg2(vss[1])};  // -inf for scale 0
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float x = pm[nt][e];
+          const bool mine = pw[nt][e] > kQ8MostP || pw[nt][2 + e] > kQ8MostP ||
+                            pv[nt][e] > kQ8MostPv || pv[nt][2 + e] > kQ8MostPv;
+          float x = -INFINITY;
 #pragma unroll
-          for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-          const float mn = fmaxf(m[nt][e], x);
-          const float a = mn == -INFINITY ? 1.f : ex2(m[nt][e] - mn);
-          m[nt][e] = mn;
+          for (int r = 0; r < 2; ++r) {
+            const float y = sa[nt][2 * r + e];
+            if (y != -INFINITY) x = fmaxf(x, fmaxf(y - kQ8Slack, y + lv[r]));
+          }
+          float go = mine ? 1.f : 0.f;
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) {
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+            go = fmaxf(go, __shfl_xor_sync(0xffffffffu, go, off));
+          }
+          if (go == 0.f) continue;
+          const float a = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - x);
+          m[nt][e] = x;
           l[nt][e] *= a;
 #pragma unroll
           for (int j = 0; j < kMT; ++j) {
@@ -355,23 +436,15 @@ __global__ void __launch_bounds__(kQ8Threads)
             acc[nt][j][2 + e] *= a;
           }
         }
+      weigh();
     }
     uint32_t pb[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float pv[4];
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float x = sa[nt][2 * r + e];
-          // a token that this row does not see: no part in the sums, whatever its scales are
-          const float w = x == -INFINITY ? 0.f : ex2(x - m[nt][e]);
-          l[nt][e] += w;
-          pv[2 * r + e] = x == -INFINITY ? 0.f : w * vss[r];
-        }
-      pb[nt][0] = movmatrix_trans(pack_bf16x2(pv[0], pv[1]));
-      pb[nt][1] = movmatrix_trans(pack_bf16x2(pv[2], pv[3]));
+      l[nt][0] += pw[nt][0] + pw[nt][2];
+      l[nt][1] += pw[nt][1] + pw[nt][3];
+      pb[nt][0] = movmatrix_trans(pack_fp16x2(pv[nt][0], pv[nt][1]));
+      pb[nt][1] = movmatrix_trans(pack_fp16x2(pv[nt][2], pv[nt][3]));
     }
 #pragma unroll
     for (int w = 0; w < kVW; ++w) {
@@ -379,11 +452,11 @@ __global__ void __launch_bounds__(kQ8Threads)
       for (int half = 0; half < 2; ++half) {
         constexpr uint32_t kPick[2] = {0x5410u, 0x7632u};  // two features of two tokens
         uint32_t a0, a1, a2, a3;
-        q8_cvt4<kType>(__byte_perm(vw[0][w], vw[1][w], kPick[half]), a0, a1);
-        q8_cvt4<kType>(__byte_perm(vw[2][w], vw[3][w], kPick[half]), a2, a3);
+        q8_value4<kType>(__byte_perm(vw[0][w], vw[1][w], kPick[half]), a0, a1);
+        q8_value4<kType>(__byte_perm(vw[2][w], vw[3][w], kPick[half]), a2, a3);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          mma_bf16_16x8x16(acc[nt][2 * w + half], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+          mma_fp16_16x8x16(acc[nt][2 * w + half], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
       }
     }
   }
@@ -411,13 +484,14 @@ __global__ void __launch_bounds__(kQ8Threads)
       float M = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kQ8Warps; ++w) M = fmaxf(M, sm_m[w][row]);
-      const float f = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - M) * q8_o_unit<kType>();
+      // a warp that saw no token has l = 0 and takes no part; a NaN stays one
+      const bool none = sm_l[warp][row] == 0.f;
+      const float f = ex2(m[nt][e] - M) * q8_o_unit<kType>();
       float *dst = part + (warp * kRows + row) * HD + (HD / 8) * g;
 #pragma unroll
       for (int j = 0; j < kMT; ++j) {
-        // a warp without a visible token has sums of 0: leave them out of a NaN's way
-        dst[2 * j] = f == 0.f ? 0.f : acc[nt][j][e] * f;
-        dst[2 * j + 1] = f == 0.f ? 0.f : acc[nt][j][2 + e] * f;
+        dst[2 * j] = none ? 0.f : acc[nt][j][e] * f;
+        dst[2 * j + 1] = none ? 0.f : acc[nt][j][2 + e] * f;
       }
     }
   __syncthreads();
@@ -431,7 +505,7 @@ __global__ void __launch_bounds__(kQ8Threads)
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kQ8Warps; ++w) {
-      if (sm_m[w][row] != -INFINITY) sum += ex2(sm_m[w][row] - M) * sm_l[w][row];
+      if (sm_l[w][row] != 0.f) sum += ex2(sm_m[w][row] - M) * sm_l[w][row];
       const float4 x = *reinterpret_cast<const float4 *>(part + (w * kRows + row) * HD + e0);
       a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
     }
@@ -441,20 +515,12 @@ __global__ void __launch_bounds__(kQ8Threads)
       if (e0 == 0) p.ws_ml[out * p.n_split + split] = make_float2(M, sum);
       continue;
     }
-    const float inv = M == -INFINITY ? 0.f : 1.f / sum;
-    if (p.o_f32) {
-      *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + out * HD + e0) =
-          make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-    } else {
-      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + out * HD + e0) =
-          make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-    }
-    if (e0 == 0 && p.lse) p.lse[out] = M == -INFINITY ? -INFINITY : (M + lg2(sum)) * 0.6931471805599453f;
+    q8_write4<HD>(p, out, e0, a, M, sum);
   }
 }
 
 // Joins the chunks of every row: M = max m_c, l = sum 2^(m_c - M) l_c, O = sum 2^(m_c - M) O_c / l.
-// HD / 4 threads per row; a chunk without a visible token has m = -inf and weight 0.
+// HD / 4 threads per row; a chunk without a visible token has l = 0 and takes no part.
 template <int HD>
 __global__ void __launch_bounds__(128) fa_q8_combine_kernel(const Q8Params p) {
   constexpr int kPer = HD / 4;
@@ -473,21 +539,13 @@ __global__ void __launch_bounds__(128) fa_q8_combine_kernel(const Q8Params p) {
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i = 0; i < n; ++i) {
     const float2 x = ml[i];
-    if (x.x == -INFINITY) continue;
+    if (x.y == 0.f) continue;
     const float f = ex2(x.x - M);
     const float4 v = *reinterpret_cast<const float4 *>(po + static_cast<size_t>(i) * HD);
     sum = fmaf(f, x.y, sum);
     a.x = fmaf(f, v.x, a.x), a.y = fmaf(f, v.y, a.y), a.z = fmaf(f, v.z, a.z), a.w = fmaf(f, v.w, a.w);
   }
-  const float inv = M == -INFINITY ? 0.f : 1.f / sum;
-  if (p.o_f32) {
-    *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + row * HD + e0) =
-        make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-  } else {
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + row * HD + e0) =
-        make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-  }
-  if (e0 == 0 && p.lse) p.lse[row] = M == -INFINITY ? -INFINITY : (M + lg2(sum)) * 0.6931471805599453f;
+  q8_write4<HD>(p, row, e0, a, M, sum);
 }
 
 }  // namespace fa

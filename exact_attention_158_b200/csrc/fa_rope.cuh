@@ -6,8 +6,8 @@
 // gradient is the transposed rotation: sin with its sign changed, the same amplitude.
 //
 // Angles.  At position 10^6 an fp32 product p * f_j is off by up to 0.06 rad, so p * f_j / (2 pi) is
-// formed in fp64 and only its fraction, in [-1/2, 1/2], goes to fp32 (off by 2^-26 turns).  One
-// sine and cosine serve every head of the token: a CTA takes kTok tokens, makes their tables in
+// formed in fp64 and only its fraction, in [-1/2, 1/2], goes to fp32, the rest (2^-26 turns) as a
+// first-order correction of the sine and cosine.  One sine and cosine serve every head of the token: a CTA takes kTok tokens, makes their tables in
 // shared memory once, and applies them to all heads of q and k.
 //
 // Bound: HBM, each element read and written once.  16-byte accesses; the strided side (a
@@ -35,9 +35,14 @@ struct RopeTable {
 // amp * (cos, sign * sin) of position * freq.
 __device__ __forceinline__ float2 rope_cos_sin(const RopeTable &t, int position, int pair) {
   const double turns = static_cast<double>(position) * t.freqs[pair] * 0.15915494309189535;
-  const float frac = static_cast<float>(turns - rint(turns));
+  const double part = turns - rint(turns);
+  const float frac = static_cast<float>(part);
+  const float rest = static_cast<float>(part - frac) * 6.2831853f;  // radians that fp32 left out
   float s, c;
   sincospif(2.f * frac, &s, &c);
+  const float c0 = c;
+  c = fmaf(-s, rest, c);
+  s = fmaf(c0, rest, s);
   return make_float2(t.amplitude * c, t.amplitude * t.sign * s);
 }
 

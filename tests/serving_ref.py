@@ -71,8 +71,10 @@ def attention(q, k_pool, v_pool, ks, vs, table, lens, scale, causal=False, tree=
     Bounds.  Scores: products of bf16 and 8-bit values are exact, and each of the d / 16 tensor-core
     steps aligns and rounds its sum within 2^-23 of the largest partial sum, twice: below 2^-18 of
     e = scale sum |q||K|; scaling adds 2^-23.  A weight is then off by e 2^-18 (times 2 for the
-    normaliser), by exp2's 2^-21 and by the rounding of p vs to bf16, 2^-8.  LSE moves by the
-    scores' error, plus the logarithm's."""
+    normaliser) and by exp2's 2^-21.  p vs is rounded to fp16 against a reference that puts the row's
+    largest p vs at 1 or above, or its largest p at 2^64 (values of scale 0): half a step is 2^-11 of
+    it, or 2^-25 where it is below fp16's normal range, which is 2^-25 max(max w vs, 2^-64) of the
+    row's weights, and adds up over the codes.  LSE moves by the scores' error, plus the logarithm's."""
     q = q.double().cpu()
     S, Hq, T, d = q.shape
     Hk = k_pool.shape[1]
@@ -82,8 +84,9 @@ def attention(q, k_pool, v_pool, ks, vs, table, lens, scale, causal=False, tree=
     ob, lb = torch.zeros_like(o), torch.zeros_like(lse)
 
     def rows(pool, sc, pages, h, L):
-        c = pool[pages.to(pool.device), h].double().cpu() * sc[pages.to(sc.device), h].double().cpu()[..., None]
-        return c.reshape(-1, d)[:L]
+        c = pool[pages.to(pool.device), h].double().cpu().reshape(-1, d)[:L]
+        f = sc[pages.to(sc.device), h].double().cpu().reshape(-1, 1)[:L]
+        return c * f, c, f
 
     P = k_pool.shape[0]
     for s, L in enumerate(lens):
@@ -99,7 +102,8 @@ def attention(q, k_pool, v_pool, ks, vs, table, lens, scale, causal=False, tree=
         elif causal:
             see &= torch.ones(T, L, dtype=torch.bool).tril(L - T)
         for h in range(Hq):
-            K, V = (rows(pool, sc, pages, h // (Hq // Hk), L) for pool, sc in ((k_pool, ks), (v_pool, vs)))
+            K = rows(k_pool, ks, pages, h // (Hq // Hk), L)[0]
+            V, codes, f = rows(v_pool, vs, pages, h // (Hq // Hk), L)
             z = q[s, h] @ K.T * scale
             z = torch.where(see, z, -math.inf)
             some = see.any(-1)
@@ -107,10 +111,14 @@ def attention(q, k_pool, v_pool, ks, vs, table, lens, scale, causal=False, tree=
             lse[s, h] = torch.logsumexp(z, -1)
             w = torch.where(some[:, None], torch.softmax(z, -1), 0.0)
             live = see.any(0)  # a token that no row sees takes no part, whatever it holds
-            w, V = w[:, live], V[live]
+            w, V, codes, f = w[:, live], V[live], codes[live].abs(), f[live]
             o[s, h] = w @ V
-            lb[s, h] = 2.0 ** -18 * e + 2.0 ** -20 * (1.0 + lse[s, h].abs().nan_to_num(0.0, posinf=0.0))
-            ob[s, h] = (U_BF16 + 2.0 ** -17 * e + 2.0 ** -18)[:, None] * (w @ V.abs()) + 2.0 ** -100
+            far = torch.log2(f[f > 0]).abs().max() if bool((f > 0).any()) else 0.0
+            lb[s, h] = (2.0 ** -18 * e + 2.0 ** -20 * (1.0 + lse[s, h].abs().nan_to_num(0.0, posinf=0.0))
+                        + 2.0 ** -24 * (16.0 + far))
+            top = (w * f[:, 0]).amax(-1, keepdim=True).clamp(min=2.0 ** -64) if len(f) else 0.0
+            ob[s, h] = ((2.0 ** -11 + 2.0 ** -17 * e + 2.0 ** -18)[:, None] * (w @ V.abs())
+                        + 2.0 ** -25 * top * (w > 0).double() @ codes)
     return o, lse, ob, lb
 
 
