@@ -23,6 +23,7 @@
 #include "fa_merge.cuh"
 #include "fa_prefill.cuh"
 #include "fa_q8.cuh"
+#include "fa_q8_tile.cuh"
 #include "fa_rope.cuh"
 
 namespace fa {
@@ -92,7 +93,7 @@ struct DeviceInfo {
   int num_sms = 0;
   bool prefill_attr[6] = {};  // (d = 64, 128) x (square, paged, key range)
   bool bwd_attr[2] = {false, false};                    // d = 64, 128
-  bool q8_attr[8] = {};  // (d = 64, 128) x (8, 16 rows) x (e4m3, int8)
+  bool q8_attr[16] = {};  // (few, many rows) x (d = 64, 128) x (one, two row tiles) x (e4m3, int8)
 };
 
 std::mutex g_mutex;
@@ -1080,27 +1081,35 @@ bool encode_pool_q8(CUtensorMap *map, const void *base, int d, long long pages) 
 // can be sized before the call.
 struct Q8Plan {
   int R;            // rows of one key head: group * Lq
-  int nt;           // 8-row tiles of a CTA (1 or 2)
+  bool tile;        // many rows: the tcgen05 kernel
+  int nt;           // row tiles of a CTA, 1 or 2 (of 8 rows, or of 128)
   int row_tiles, n_split, split_pages;
   size_t rows;      // S * Hq * Lq
 };
 
 constexpr int kQ8TargetCtas = 148 * 3 * 4;  // a few waves of the three CTAs that fit an SM
 constexpr int kQ8MinPages = 16;             // pages of a chunk: four to a warp
+constexpr int kQ8StreamRows = 16;           // up to here fa_q8_stream_kernel, beyond fa_q8_tile_kernel
+constexpr int kQ8TileTargetCtas = 148;      // one CTA per SM
+constexpr int kQ8TileMinPages = 16;         // two token tiles to a chunk
 
 bool q8_plan(int S, int Hq, int Hk, int Lq, int d, int max_blocks, Q8Plan *out) {
   if (S < 1 || Hq < 1 || Hk < 1 || Hq % Hk != 0 || Lq < 1 || max_blocks < 1) return false;
   if (d != 64 && d != 128) return false;
   if (static_cast<long long>(S) * Hq * Lq > INT_MAX / 4) return false;
-  if (static_cast<long long>(max_blocks) * fa::kQ8Page > INT_MAX) return false;
+  // token numbers, up to a tile past the last, are ints
+  if (static_cast<long long>(max_blocks) * fa::kQ8Page > INT_MAX - 2 * fa::kQ8Tok) return false;
   Q8Plan p{};
   p.R = Hq / Hk * Lq;
-  p.nt = p.R > 8 ? 2 : 1;
-  p.row_tiles = (p.R + 8 * p.nt - 1) / (8 * p.nt);
+  p.tile = p.R > kQ8StreamRows;
+  const int tile_rows = p.tile ? 128 : 8;
+  p.nt = p.R > tile_rows ? 2 : 1;
+  p.row_tiles = (p.R + tile_rows * p.nt - 1) / (tile_rows * p.nt);
   const long long units = static_cast<long long>(S) * Hk * p.row_tiles;
-  long long n = std::min<long long>((kQ8TargetCtas + units - 1) / units,
-                                    (max_blocks + kQ8MinPages - 1) / kQ8MinPages);
+  const int target = p.tile ? kQ8TileTargetCtas : kQ8TargetCtas, least = p.tile ? kQ8TileMinPages : kQ8MinPages;
+  const long long n = std::min<long long>((target + units - 1) / units, (max_blocks + least - 1) / least);
   p.split_pages = static_cast<int>((max_blocks + n - 1) / n);
+  if (p.tile) p.split_pages = (p.split_pages + 7) / 8 * 8;  // whole tiles of 128 tokens
   p.n_split = (max_blocks + p.split_pages - 1) / p.split_pages;
   p.rows = static_cast<size_t>(S) * Hq * Lq;
   if (units * p.n_split > INT_MAX) return false;
@@ -1110,6 +1119,19 @@ bool q8_plan(int S, int Hq, int Hk, int Lq, int d, int max_blocks, Q8Plan *out) 
 
 size_t q8_workspace(const Q8Plan &p, int d) {
   return p.n_split > 1 ? p.rows * p.n_split * (d + 2) * sizeof(float) : 0;
+}
+
+// After the kernel that wrote the chunks' partials: joins them where there are several.
+template <int HD>
+fa_status q8_combine(const fa::Q8Params &p, cudaStream_t s) {
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return launch_failed(e);
+  if (p.n_split > 1) {
+    const size_t threads = static_cast<size_t>(p.S) * p.Hk * p.R * (HD / 4);
+    fa::fa_q8_combine_kernel<HD><<<static_cast<unsigned>((threads + 127) / 128), 128, 0, s>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return launch_failed(e);
+  }
+  return FA_OK;
 }
 
 template <int HD, int NT, int kType>
@@ -1128,24 +1150,42 @@ fa_status launch_q8_stream(DeviceInfo &dev, const CUtensorMap &tk, const CUtenso
   }
   const unsigned grid = static_cast<unsigned>(p.n_split) * p.row_tiles * p.Hk * p.S;
   fa::fa_q8_stream_kernel<HD, NT, kType><<<grid, fa::kQ8Threads, C::kSmem, s>>>(tk, tv, p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return launch_failed(e);
-  if (p.n_split > 1) {
-    const size_t threads = static_cast<size_t>(p.S) * p.Hk * p.R * (HD / 4);
-    fa::fa_q8_combine_kernel<HD><<<static_cast<unsigned>((threads + 127) / 128), 128, 0, s>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return launch_failed(e);
-  }
-  return FA_OK;
+  return q8_combine<HD>(p, s);
 }
 
-template <int HD>
-fa_status launch_q8(DeviceInfo &dev, const CUtensorMap &tk, const CUtensorMap &tv, const fa::Q8Params &p,
-                    int nt, fa_cache_type type, cudaStream_t s) {
-  if (type == FA_CACHE_E4M3)
-    return nt == 2 ? launch_q8_stream<HD, 2, fa::kQ8E4m3>(dev, tk, tv, p, s)
-                   : launch_q8_stream<HD, 1, fa::kQ8E4m3>(dev, tk, tv, p, s);
-  return nt == 2 ? launch_q8_stream<HD, 2, fa::kQ8Int8>(dev, tk, tv, p, s)
-                 : launch_q8_stream<HD, 1, fa::kQ8Int8>(dev, tk, tv, p, s);
+template <int HD, int kType, bool kTwo>
+fa_status launch_q8_tile(DeviceInfo &dev, const fa::Q8Params &p, cudaStream_t s) {
+  using C = fa::Q8TileCfg<HD>;
+  const int slot = 8 + (HD == 128) * 4 + kTwo * 2 + (kType == fa::kQ8Int8);
+  {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (!dev.q8_attr[slot]) {
+      cudaError_t e = cudaFuncSetAttribute(fa::fa_q8_tile_kernel<HD, kType, kTwo>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           static_cast<int>(C::kSmem));
+      if (e != cudaSuccess) return launch_failed(e);
+      dev.q8_attr[slot] = true;
+    }
+  }
+  const unsigned grid = static_cast<unsigned>(p.n_split) * p.row_tiles * p.Hk * p.S;
+  fa::fa_q8_tile_kernel<HD, kType, kTwo><<<grid, fa::kQ8TileThreads, C::kSmem, s>>>(p);
+  return q8_combine<HD>(p, s);
+}
+
+template <int HD, int kType>
+fa_status launch_q8(DeviceInfo &dev, const void *k_pool, const void *v_pool, const fa::Q8Params &p,
+                    const Q8Plan &plan, cudaStream_t s) {
+  if (plan.tile)
+    return plan.nt == 2 ? launch_q8_tile<HD, kType, true>(dev, p, s)
+                        : launch_q8_tile<HD, kType, false>(dev, p, s);
+  CUtensorMap tk, tv;
+  const long long pages = static_cast<long long>(p.num_blocks) * p.Hk;
+  if (!encode_pool_q8(&tk, k_pool, HD, pages) || !encode_pool_q8(&tv, v_pool, HD, pages)) {
+    t_last_error = "cuTensorMapEncodeTiled failed";
+    return FA_ERR_LAUNCH;
+  }
+  return plan.nt == 2 ? launch_q8_stream<HD, 2, kType>(dev, tk, tv, p, s)
+                      : launch_q8_stream<HD, 1, kType>(dev, tk, tv, p, s);
 }
 
 fa_status q8_attention(const void *q, const void *k_pool, const void *v_pool, const float *k_scale,
@@ -1191,14 +1231,10 @@ fa_status q8_attention(const void *q, const void *k_pool, const void *v_pool, co
   DeviceInfo *dev = nullptr;
   int dev_id = 0;
   if ((st = current_device(&dev, &dev_id)) != FA_OK) return st;
-  CUtensorMap tk, tv;
-  const long long pages = static_cast<long long>(num_blocks) * Hk;
-  if (!encode_pool_q8(&tk, k_pool, d, pages) || !encode_pool_q8(&tv, v_pool, d, pages)) {
-    t_last_error = "cuTensorMapEncodeTiled failed";
-    return FA_ERR_LAUNCH;
-  }
   fa::Q8Params p{};
   p.q = static_cast<const uint16_t *>(q);
+  p.k_codes = static_cast<const uint8_t *>(k_pool);
+  p.v_codes = static_cast<const uint8_t *>(v_pool);
   p.ks = k_scale;
   p.vs = v_scale;
   p.table = block_table;
@@ -1222,8 +1258,11 @@ fa_status q8_attention(const void *q, const void *k_pool, const void *v_pool, co
   p.o_f32 = o_dtype == FA_OUT_F32;
   p.scale_log2 = sc * 1.4426950408889634f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return d == 128 ? launch_q8<128>(*dev, tk, tv, p, plan.nt, type, s)
-                  : launch_q8<64>(*dev, tk, tv, p, plan.nt, type, s);
+  if (type == FA_CACHE_E4M3)
+    return d == 128 ? launch_q8<128, fa::kQ8E4m3>(*dev, k_pool, v_pool, p, plan, s)
+                    : launch_q8<64, fa::kQ8E4m3>(*dev, k_pool, v_pool, p, plan, s);
+  return d == 128 ? launch_q8<128, fa::kQ8Int8>(*dev, k_pool, v_pool, p, plan, s)
+                  : launch_q8<64, fa::kQ8Int8>(*dev, k_pool, v_pool, p, plan, s);
 }
 
 }  // namespace

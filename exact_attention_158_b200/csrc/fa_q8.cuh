@@ -38,7 +38,8 @@ enum Q8Type { kQ8E4m3 = 1, kQ8Int8 = 2 };
 
 struct Q8Params {
   const uint16_t *q;
-  const float *ks, *vs;  // [num_blocks, Hk, 16]
+  const uint8_t *k_codes, *v_codes;  // [num_blocks, Hk, 16, d] (the tile kernel's; else tensor maps)
+  const float *ks, *vs;              // [num_blocks, Hk, 16]
   const int32_t *table, *lens;
   const uint64_t *tree;  // [S, T] or null
   void *o;
