@@ -1,36 +1,52 @@
 // fa_q8_tile.cuh -- attention of many rows (a prompt chunk, a draft tree, large groups) over an 8-bit
-// paged cache on the tcgen05 tensor cores.  The mathematics, the scales' places and the row reference
-// are those of fa_q8.cuh.
+// paged cache on the tcgen05 tensor cores.  The mathematics is that of fa_q8.cuh; only the values'
+// scales sit elsewhere.
 //
 // One CTA takes up to 256 of the R rows of one (sequence, key head) and a range of its 128-token
 // tiles.  Codes cannot feed a 16-bit product, so they are converted once per tile for all of the
 // CTA's rows:
-//   warps 0-3    row tile 0: one TMEM lane = one row.  Scores out of TMEM, p and p vs, P to shared
-//   warps 4-7    row tile 1: the same; idle with one row tile (kTwo = false)
-//   warps 8-11   codes: global (two 16-bit-wide tiles ahead in registers) -> bf16 K / fp16 V tiles in
-//                the swizzled layout the tensor core reads; the tile's scales and its live tokens
-//   warp  12     tensor-memory owner and issuer of every product (one thread)
+//   warps 0-3    one side: a thread holds a row (a TMEM lane).  Scores out of TMEM, p to shared
+//                memory; one thread issues the side's products
+//   warps 4-7    the other side
+//   warps 8-11   codes: global (one tile ahead, in registers) -> bf16 K / fp16 V tiles in the
+//                swizzled layout the tensor core reads; the tile's key scales and its live tokens
+// TMEM (512 columns): S0 [0,128)  S1 [128,256)  O0 [256,256+d)  O1 [256+d,256+2d).
+// With more than 128 rows the sides hold two row tiles; with fewer they share one row tile and take
+// the tiles of tokens in turn.  Either way one side's products run while the other's softmax does.
+// An issuer needs no warp of its own, since its side waits for what it issues; a thirteenth warp
+// would leave a thread 128 registers instead of 168.
+//
+// Scales.  A key's scale multiplies its column of scores in fp32, read from shared memory by every
+// row: 32 broadcast 16-byte loads per row and tile, which cost the SM about half as much as the
+// exponentials.  A value's scale is folded into V instead (a second set of such loads measured
+// 5900 cycles per tile of tokens where this form takes QQQQ): V = code * f in fp16, f = vs 2^a / F
+// with F a power of two no smaller than any vs so far; O is rescaled when F has to grow.  f and the
+// product are rounded to fp16 (2^-11 each, like p).  V uses fp16 from its top (2^15) down and p from
+// 2^6 to 2^15, so a token whose values are 2^20 times the others' and whose weight is 2^-20 takes
+// nothing from either.  A value scale that is not finite would reach rows that do not see its token
+// as 0 * NaN: V is 0 there, and rows that do see it are marked and written as NaN.
+//
+// A row's softmax is one pass: p = 2^(s ks - m) against the reference it has, summed and stored;
+// only when their sum passes 2^15 (always on a row's first tile) or F has grown does the warp go back to
+// S, move the references so that the largest p is 2^6, rescale O in TMEM and do the pass again.
+//
 // The conversion leaves every four features in the order 0, 2, 1, 3; q is stored in that order too, and
 // O's columns are put back when it is written.
-// TMEM (512 columns): S0 [0,128)  S1 [128,256)  O0 [256,256+d)  O1 [256+d,256+2d).
-// With two row tiles the products of one run while the other's softmax does.  With one, its tiles
-// alternate between the two S and P buffers: Q K^T of tile j + 1 runs during the softmax of tile j.
 //
-// A row's softmax is one pass: p = 2^(s ks - m) with the reference it has, summed and multiplied by vs
-// on the way to P; only when a limit is passed (always on a row's first tile) the warp goes back to S,
-// moves the references, rescales O in TMEM and does the pass again.
-//
-// Bound: per 128 x 128 scores the products take about 1020 cycles at d = 128, the exponentials 1020
-// (16 a cycle), the conversion's instructions 600 per tile of tokens and the softmax's 550 per row
-// tile on each of the SM's four schedulers, and the tile's 32 KB of codes about 1400 cycles of the
-// SM's share of HBM: few rows are bound by HBM, many by the tensor cores and the exponentials.
+// Bound: per 128 x 128 scores the products take about 1020 cycles at d = 128 and the exponentials
+// 1024 (16 a cycle); the tile's 32 KB of codes take about 1400 cycles of the SM's share of HBM.
+// Few rows are bound by HBM, many by the tensor cores and the exponentials together.
 #pragma once
 #include "fa_q8.cuh"
 
 namespace fa {
 
-constexpr int kQ8TileThreads = 13 * 32;
-constexpr int kQ8Tok = 128;  // tokens of a tile
+constexpr int kQ8TileThreads = 12 * 32;
+constexpr int kQ8Tok = 128;                 // tokens of a tile
+constexpr float kQ8TileMost = 0x1p15f;      // a tile's sum of p, and so any p: fp16 ends at 2^16
+constexpr float kQ8TileStart = 6.f;         // log2 of the largest p after the reference has moved
+// f at the largest vs: e4m3 codes are at most 1.75 in fp16 units (448 2^-8), int8 codes 127
+template <int kType> __device__ constexpr float q8_vtop() { return kType == kQ8E4m3 ? 0x1p14f : 0x1p8f; }
 
 template <int HD>
 struct Q8TileCfg {
@@ -39,9 +55,9 @@ struct Q8TileCfg {
   static constexpr int kTileBytes = kChunks * kChunkBytes;
   static constexpr int kPBytes = 2 * kChunkBytes;     // 128 x 128 fp16
   static constexpr int kScaleBufs = 4;
-  static constexpr int kBars = 24;
+  static constexpr int kBars = 30;
   static constexpr size_t kSmem = 1024 + 2 * kTileBytes + 2 * kTileBytes + 2 * kPBytes +
-                                  kScaleBufs * (2 * kQ8Tok * 4 + 16) + kBars * 8 + 16;
+                                  kScaleBufs * (kQ8Tok * 4 + 48) + kBars * 8 + 16;
   static constexpr uint32_t kColS = 0, kColO = 256;
   static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, 0, 0);
   // fp16 operands: the type fields of A and B are 0
@@ -55,10 +71,111 @@ __device__ __forceinline__ uint32_t q8_swz(int row, int unit) {
   return static_cast<uint32_t>(row * 128 + ((unit ^ (row & 7)) << 4));
 }
 
+__device__ __forceinline__ uint32_t mul_fp16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Keeps uses of registers that a tcgen05.ld fills behind the wait that precedes this.
 __device__ __forceinline__ void q8_pin(float (&x)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(x[i]));
+}
+
+// 32 scores of a row -> p: added to sum, rounded to fp16 into units unit0.. of the row of P.  kMasked:
+// only the tokens in k take part.  The steps are kept apart (all loads of ks, all arguments, all
+// exponentials, then sums and stores): interleaved per few scores, each waits for the one before it,
+// and loads of ks cannot move above stores of p, which the compiler cannot tell apart.
+template <bool kMasked>
+__device__ __forceinline__ void q8_weigh32(float (&x)[32], uint32_t k, const float *ks, uint64_t neg2,
+                                           uint64_t (&sum)[4], uint8_t *p_chunk, int row, int unit0) {
+  uint64_t f[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const ulonglong2 v = reinterpret_cast<const ulonglong2 *>(ks)[i];
+    f[2 * i] = v.x;
+    f[2 * i + 1] = v.y;
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), f[i], neg2), x[2 * i], x[2 * i + 1]);
+    if (kMasked) {
+      x[2 * i] = (k >> (2 * i)) & 1 ? x[2 * i] : -INFINITY;
+      x[2 * i + 1] = (k >> (2 * i + 1)) & 1 ? x[2 * i + 1] : -INFINITY;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) x[i] = ex2(x[i]);
+  uint32_t pk[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    sum[i % 4] = f2_add(sum[i % 4], f2_pack(x[2 * i], x[2 * i + 1]));
+    pk[i] = pack_fp16x2(x[2 * i], x[2 * i + 1]);
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    *reinterpret_cast<uint4 *>(p_chunk + q8_swz(row, unit0 + u)) =
+        make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+}
+
+// A row's 128 scores (TMEM) -> P (shared memory) and the sum of p, against the reference m.  k: the
+// tokens that the row sees.
+template <int HD, bool kMasked>
+__device__ __forceinline__ float q8_weigh(uint32_t s_tmem, const uint32_t (&k)[4], const float *ks, float m,
+                                          uint8_t *pt, int row) {
+  const uint64_t neg2 = f2_pack(-m, -m);
+  uint64_t sum[4] = {0, 0, 0, 0};
+  float x[2][32];
+  tmem_ld32(s_tmem, reinterpret_cast<uint32_t *>(x[0]));
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    tmem_wait_ld();
+    q8_pin(x[c & 1]);
+    if (c < 3) tmem_ld32(s_tmem + 32 * (c + 1), reinterpret_cast<uint32_t *>(x[(c + 1) & 1]));
+    q8_weigh32<kMasked>(x[c & 1], k[c], ks + 32 * c, neg2, sum,
+                        pt + (c / 2) * Q8TileCfg<HD>::kChunkBytes, row, 4 * (c & 1));
+  }
+  float a, b;
+  f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), a, b);
+  return a + b;
+}
+
+// The largest scaled score among the tokens in k.
+__device__ __forceinline__ float q8_row_max(uint32_t s_tmem, const uint32_t (&k)[4], const float *ks) {
+  float x = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    float sc[32];
+    tmem_ld32(s_tmem + 32 * c, reinterpret_cast<uint32_t *>(sc));
+    const uint32_t kc = c == 0 ? k[0] : c == 1 ? k[1] : c == 2 ? k[2] : k[3];
+    tmem_wait_ld();
+    q8_pin(sc);
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      const float4 f = *reinterpret_cast<const float4 *>(ks + 32 * c + i);
+      const float y[4] = {sc[i] * f.x, sc[i + 1] * f.y, sc[i + 2] * f.z, sc[i + 3] * f.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x = fmaxf(x, (kc >> (i + e)) & 1 ? y[e] : -INFINITY);
+    }
+  }
+  return x;
+}
+
+// 32 features of a row, in the conversion's order, from its sums: to the output, or as a partial.
+template <int HD>
+__device__ __forceinline__ void q8_write32(const Q8Params &p, size_t row, int split, int c, const float (&o)[32],
+                                           float m, float l, bool poison) {
+  const float nan = __int_as_float(0x7fc00000);
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const float4 v = poison ? make_float4(nan, nan, nan, nan) : make_float4(o[i], o[i + 2], o[i + 1], o[i + 3]);
+    if (p.n_split > 1)
+      *reinterpret_cast<float4 *>(p.ws_o + (row * p.n_split + split) * HD + c + i) = v;
+    else
+      q8_write4<HD>(p, row, c + i, v, m, l);
+  }
+  if (c == 0 && p.n_split > 1) p.ws_ml[row * p.n_split + split] = make_float2(m, l);
 }
 
 // Token tiles that the rows [r0, r1) can see: all of them, or up to the last row's own token.
@@ -70,25 +187,64 @@ __device__ __forceinline__ int q8_tiles(const Q8Params &p, int L, int r0, int r1
   return (L - p.T + t) / kQ8Tok + 1;
 }
 
+// S (TMEM) = Q K^T: both K-major in 64-feature swizzled chunks.
+template <int HD>
+__device__ __forceinline__ void q8_issue_qk(uint32_t d_tmem, const uint8_t *q, const uint8_t *k) {
+  using C = Q8TileCfg<HD>;
+  const uint64_t qd = smem_desc_sw128(smem_u32(q), 16, 1024), kd = smem_desc_sw128(smem_u32(k), 16, 1024);
+#pragma unroll
+  for (int kk = 0; kk < HD / 16; ++kk) {
+    const uint64_t off = static_cast<uint64_t>(((kk / 4) * C::kChunkBytes + (kk % 4) * 32) >> 4);
+    umma_ss(d_tmem, qd + off, kd + off, C::kIdescQK, kk > 0 ? 1u : 0u);
+  }
+}
+
+// O (TMEM) (+)= P V: P K-major over the tokens, V MN-major (chunks of 64 features, 8-token groups).
+template <int HD>
+__device__ __forceinline__ void q8_issue_pv(uint32_t d_tmem, const uint8_t *pt, const uint8_t *v, bool accumulate) {
+  using C = Q8TileCfg<HD>;
+  const uint64_t pd = smem_desc_sw128(smem_u32(pt), 16, 1024);
+  const uint64_t vd = smem_desc_sw128(smem_u32(v), C::kChunkBytes, 1024);
+#pragma unroll
+  for (int kk = 0; kk < kQ8Tok / 16; ++kk) {
+    const uint64_t off = static_cast<uint64_t>(((kk / 4) * C::kChunkBytes + (kk % 4) * 32) >> 4);
+    umma_ss(d_tmem, pd + off, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), C::kIdescPV,
+            (accumulate || kk > 0) ? 1u : 0u);
+  }
+}
+
+// Every thread of warps 0-7 (none of them leaves before it; the waits on the way are bounded).
+__device__ __forceinline__ void q8_sides_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// kTwo: two tiles of 128 rows, warps 0-3 and 4-7, every tile of tokens.  Else one tile of rows: warps
+// 0-3 take the even tiles of tokens and warps 4-7 the odd ones, each with its own S, P, O and row
+// sums, joined at the end.  A "side" below is either group of four warps.
 template <int HD, int kType, bool kTwo>
 __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8Params p) {
   using C = Q8TileCfg<HD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t *sQ = smem;
+  uint8_t *sQ = smem;                     // two row tiles; with one, the other holds odd K tiles
   uint8_t *sK = sQ + 2 * C::kTileBytes;
   uint8_t *sV = sK + C::kTileBytes;
   uint8_t *sP = sV + C::kTileBytes;
   float *sKs = reinterpret_cast<float *>(sP + 2 * C::kPBytes);  // [buffer][token]: ks scale log2(e)
-  float *sVs = sKs + C::kScaleBufs * kQ8Tok;
-  uint32_t *sLive = reinterpret_cast<uint32_t *>(sVs + C::kScaleBufs * kQ8Tok);  // [buffer][4]
-  uint64_t *bars = reinterpret_cast<uint64_t *>(sLive + C::kScaleBufs * 4);
-  uint64_t *q_full = bars, *k_full = bars + 1, *k_free = bars + 2, *v_full = bars + 3, *v_free = bars + 4;
-  uint64_t *sc_full = bars + 5;            // [4]
-  uint64_t *s_full = bars + 9;             // [2]
-  uint64_t *p_full = bars + 11;            // [2]
-  uint64_t *pv_done = bars + 13;           // [2]
-  uint64_t *drain = bars + 15;
+  uint32_t *sLive = reinterpret_cast<uint32_t *>(sKs + C::kScaleBufs * kQ8Tok);  // [buffer][4]
+  uint32_t *sBad = sLive + C::kScaleBufs * 4;  // [buffer][4]: live tokens whose vs is not finite
+  float *sF = reinterpret_cast<float *>(sBad + C::kScaleBufs * 4);  // [buffer][4]: F of the tile
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sF + C::kScaleBufs * 4);
+  // Landing barriers of tile j are [j & 1], so that a side that waits for every other tile of tokens
+  // sees each phase of its own.  Buffers are freed by an arrival from each issuer that reads them.
+  uint64_t *k_full = bars, *v_full = bars + 2;  // [2]
+  uint64_t *k_free = bars + 4;                  // [2] (kTwo: [0])
+  uint64_t *v_free = bars + 6;
+  uint64_t *sc_full = bars + 7;                 // [4]
+  uint64_t *s_full = bars + 11;                 // [side]
+  uint64_t *p_full = bars + 13;                 // [side]
+  uint64_t *pv_done = bars + 15;                // [side]
+  uint64_t *drain = bars + 17;                  // [side] every product of an issuer has completed
+  uint64_t *q_full = bars + 19;                 // [row tile]
+  uint64_t *turn = bars + 21;                   // [side][warp]
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kBars);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -104,7 +260,8 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
   const int tiles_per_split = p.split_pages / (kQ8Tok / kQ8Page);
   const int j0 = split * tiles_per_split;
   if (p.n_split > 1 && j0 * kQ8Tok >= L) return;  // past the sequence's end: the combine skips it
-  int n[2];  // tiles of this range that each row tile visits
+  // tiles of tokens that each side takes, and that the CTA takes in all
+  int n[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r0 = row0 + 128 * i;
@@ -112,26 +269,29 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
     n[i] = max(0, min(all, j0 + tiles_per_split) - j0);
   }
   const int nmax = max(n[0], n[1]);
+  if (!kTwo) n[0] = (nmax + 1) / 2, n[1] = nmax / 2;
+  const int both = min(n[0], n[1]);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
-    mbar_init(q_full, kTwo ? 8 : 4);
-    mbar_init(k_full, 4);
-    mbar_init(k_free, 1);
-    mbar_init(v_full, 4);
-    mbar_init(v_free, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(sc_full + i, 4);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full + i, 4);
+      mbar_init(v_full + i, 4);
+      mbar_init(k_free + i, kTwo ? 2 : 1);
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 4);
       mbar_init(pv_done + i, 1);
+      mbar_init(drain + i, 1);
+      mbar_init(q_full + i, 4);
     }
-    mbar_init(drain, 1);
+    mbar_init(v_free, kTwo ? 2 : 1);
+    for (int i = 0; i < 4; ++i) mbar_init(sc_full + i, 4);
+    for (int i = 0; i < 8; ++i) mbar_init(turn + i, 1);
     *abort_flag = 0;
     if (L != p.lens[s] && p.lens[s] > 0) atomicExch(&g_device_status, 1 /* FA_ERR_INVALID_ARG */);
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == 8) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
@@ -139,8 +299,9 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  auto k_tile = [&](int j) { return (kTwo || !(j & 1)) ? sK : sQ + C::kTileBytes; };
 
-  if (warp >= 8 && warp < 12) {
+  if (warp >= 8) {
     // ------------------------------------------------------------------ codes -> 16-bit tiles
     const int w = warp - 8;              // tokens 32 w .. 32 w + 31 of a tile: pages 2 w, 2 w + 1
     constexpr int kPieces = HD / 8;      // 8-code pieces of a token
@@ -149,26 +310,28 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
     const int piece = lane % kPieces, sub = lane / kPieces;
     const int32_t *trow = p.table + static_cast<size_t>(s) * p.max_blocks;
     const int nblk = (L + kQ8Page - 1) / kQ8Page;
-    auto block_of = [&](int j) -> int {  // lanes 0-15: the warp's first page, 16-31: its second
-      const int page = (j0 + j) * (kQ8Tok / kQ8Page) + 2 * w + lane / 16;
-      if (j >= nmax || page >= nblk) return -1;
-      int b = trow[page];
-      if (b < 0 || b >= p.num_blocks) {
-        atomicExch(&g_device_status, 1 /* FA_ERR_INVALID_ARG: the page is left out */);
-        b = -1;
-      }
-      return b;
+    // lane i < 8: the table's entry for page i of tile j; not looked at before it is needed (named)
+    auto entry_of = [&](int j) -> int {
+      const int page = (j0 + j) * (kQ8Tok / kQ8Page) + lane;
+      return (lane < kQ8Tok / kQ8Page && j < nmax && page < nblk) ? trow[page] : -1;
     };
-    const uint8_t *kcodes = p.k_codes + static_cast<size_t>(kh) * kQ8Page * HD;
-    const uint8_t *vcodes = p.v_codes + static_cast<size_t>(kh) * kQ8Page * HD;
+    auto named = [&](int j, int b) -> int {  // -1 for a page that the table does not name
+      const int page = (j0 + j) * (kQ8Tok / kQ8Page) + lane;
+      if (b >= 0 && b < p.num_blocks) return b;
+      if (lane < kQ8Tok / kQ8Page && j < nmax && page < nblk)
+        atomicExch(&g_device_status, 1 /* FA_ERR_INVALID_ARG: the page is left out */);
+      return -1;
+    };
+    const uint8_t *kcodes = p.k_codes + static_cast<size_t>(kh) * kQ8Page * HD + sub * HD + 8 * piece;
+    const uint8_t *vcodes = p.v_codes + static_cast<size_t>(kh) * kQ8Page * HD + sub * HD + 8 * piece;
     const size_t block_stride = static_cast<size_t>(p.Hk) * kQ8Page * HD;
     uint2 kc[kLoads], vc[kLoads];
     // a page left out reads block 0: its tokens are not live
     auto fetch = [&](const uint8_t *codes, int blk, uint2 (&c)[kLoads]) {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int b = max(__shfl_sync(0xffffffffu, blk, 16 * half), 0);
-        const uint8_t *src = codes + static_cast<size_t>(b) * block_stride + sub * HD + 8 * piece;
+        const int b = max(__shfl_sync(0xffffffffu, blk, 2 * w + half), 0);
+        const uint8_t *src = codes + static_cast<size_t>(b) * block_stride;
 #pragma unroll
         for (int k = 0; k < kLoads / 2; ++k) {
           asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
@@ -177,148 +340,128 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
         }
       }
     };
-    const uint32_t chunk_at = static_cast<uint32_t>(piece / 8) * C::kChunkBytes;
+    const uint32_t at0 = static_cast<uint32_t>(piece / 8) * C::kChunkBytes;
     const int unit = piece % 8;
-    float ks = 0.f, vs = 0.f;
-    bool in = false;
-    auto fetch_scales = [&](int j, int blk) {  // token 32 w + lane, of the page that its half warp holds
-      in = blk >= 0 && (j0 + j) * kQ8Tok + 32 * w + lane < L;
-      ks = vs = 0.f;
-      if (in) {
-        const size_t at = (static_cast<size_t>(blk) * p.Hk + kh) * kQ8Page + lane % 16;
-        ks = p.ks[at];
-        vs = p.vs[at];
+    float ks = 0.f, vs[4];  // of token 32 w + lane, and of tokens 32 i + lane
+    uint32_t live = 0;      // of the warp's own 32 tokens
+    auto fetch_scales = [&](int j, int blk) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int b = __shfl_sync(0xffffffffu, blk, 2 * i + lane / 16);
+        const bool in = b >= 0 && (j0 + j) * kQ8Tok + 32 * i + lane < L;
+        const size_t at = (static_cast<size_t>(max(b, 0)) * p.Hk + kh) * kQ8Page + lane % 16;
+        vs[i] = in ? p.vs[at] : 0.f;
+        if (i == w) {
+          ks = in ? p.ks[at] : 0.f;
+          live = __ballot_sync(0xffffffffu, in);
+        }
       }
     };
+    float F = 0x1p-126f;  // every warp finds the same F, tile by tile
     const float score_scale = p.scale_log2 * q8_score_unit<kType>();
-    int blk = block_of(0), blk_next = block_of(1);
-    if (nmax > 0) {
-      fetch(kcodes, blk, kc);
-      fetch_scales(0, blk);
-      fetch(vcodes, blk, vc);
-    }
-    for (int j = 0; j < nmax; ++j) {
-      if (j > 0 && !__all_sync(0xffffffffu, mbar_wait(k_free, (j - 1) & 1, abort_flag))) break;
+    // K of tile j and the tile's scales; returns f of this lane's token, twice
+    auto convert_k = [&](int j) -> uint32_t {
       const int buf = j % C::kScaleBufs;
       sKs[buf * kQ8Tok + 32 * w + lane] = ks * score_scale;
-      sVs[buf * kQ8Tok + 32 * w + lane] = vs;
-      const uint32_t live = __ballot_sync(0xffffffffu, in);
-      if (lane == 0) sLive[buf * 4 + w] = live;
+      float top = 0.f;  // the tile's largest finite vs
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, vs[i] < INFINITY ? vs[i] : 0.f);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      if (top > F)  // the power of two above it
+        F = __uint_as_float(min(((__float_as_uint(top) >> 23) & 0xffu) + 1u, 254u) << 23);
+      float mine = vs[0];
+#pragma unroll
+      for (int i = 1; i < 4; ++i) mine = w == i ? vs[i] : mine;
+      const bool bad = !(fabsf(mine) < INFINITY);
+      const uint32_t badmask = __ballot_sync(0xffffffffu, bad);
+      if (lane == 0) {
+        sLive[buf * 4 + w] = live;
+        sBad[buf * 4 + w] = badmask;
+        if (w == 0) sF[buf * 4] = F;
+      }
+      uint8_t *kt = k_tile(j) + at0;
 #pragma unroll
       for (int k = 0; k < kLoads; ++k) {
         const int row = 32 * w + k * kRowsPer + sub;
         uint4 o;
         q8_key4<kType>(kc[k].x, o.x, o.y);
         q8_key4<kType>(kc[k].y, o.z, o.w);
-        *reinterpret_cast<uint4 *>(sK + chunk_at + q8_swz(row, unit)) = o;
+        *reinterpret_cast<uint4 *>(kt + q8_swz(row, unit)) = o;
       }
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(sc_full + buf);
-        mbar_arrive(k_full);
+        mbar_arrive(k_full + (j & 1));
       }
-      blk = blk_next;
-      blk_next = block_of(j + 2);
-      if (j + 1 < nmax) {
-        fetch(kcodes, blk, kc);
-        fetch_scales(j + 1, blk);
-      }
-      if (j > 0 && !__all_sync(0xffffffffu, mbar_wait(v_free, (j - 1) & 1, abort_flag))) break;
+      const float fs = bad ? 0.f : mine / F * q8_vtop<kType>();  // vs / F first: neither factor overflows
+      return pack_fp16x2(fs, fs);
+    };
+    auto convert_v = [&](int j, uint32_t f2) {
 #pragma unroll
       for (int k = 0; k < kLoads; ++k) {
         const int row = 32 * w + k * kRowsPer + sub;
         uint4 o;
+        const uint32_t f = __shfl_sync(0xffffffffu, f2, k * kRowsPer + sub);
         q8_value4<kType>(vc[k].x, o.x, o.y);
         q8_value4<kType>(vc[k].y, o.z, o.w);
-        *reinterpret_cast<uint4 *>(sV + chunk_at + q8_swz(row, unit)) = o;
+        o = make_uint4(mul_fp16x2(o.x, f), mul_fp16x2(o.y, f), mul_fp16x2(o.z, f), mul_fp16x2(o.w, f));
+        *reinterpret_cast<uint4 *>(sV + at0 + q8_swz(row, unit)) = o;
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(v_full);
-      if (j + 1 < nmax) fetch(vcodes, blk, vc);
+      if (lane == 0) mbar_arrive(v_full + (j & 1));
+    };
+    // K runs kAhead tiles before V.  With one K buffer V_j is free first (P V_{j-1} is issued before
+    // Q K_j^T), with two K_{j+1} is.
+    constexpr int kAhead = kTwo ? 0 : 1;
+    int blk_k = named(0, entry_of(0)), entry = entry_of(1), blk_v = blk_k;
+    if (nmax > 0) {
+      fetch(kcodes, blk_k, kc);
+      fetch_scales(0, blk_k);
+      fetch(vcodes, blk_v, vc);
     }
-  } else if (warp == 12) {
-    // ------------------------------------------------------------------ products (one thread)
-    if (lane == 0) {
-      const uint64_t kd = smem_desc_sw128(smem_u32(sK), 16, 1024);
-      const uint64_t vd = smem_desc_sw128(smem_u32(sV), C::kChunkBytes, 1024);
-      auto qk = [&](int tile, int slot) {
-        const uint64_t qd = smem_desc_sw128(smem_u32(sQ + tile * C::kTileBytes), 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk) {
-          const uint64_t off = static_cast<uint64_t>(((kk / 4) * C::kChunkBytes + (kk % 4) * 32) >> 4);
-          umma_ss(tmem + C::kColS + 128 * slot, qd + off, kd + off, C::kIdescQK, kk > 0 ? 1u : 0u);
+    uint32_t f2_v = 0, f2_k = 0;  // f of the next V tile, and of the tile whose K was made last
+    for (int j = -kAhead; j < nmax; ++j) {
+      const int jk = j + kAhead;
+      int blk_next = blk_k;
+      if (jk < nmax) {
+        const bool ok = kTwo ? (jk < 1 || mbar_wait(k_free, (jk - 1) & 1, abort_flag))
+                             : (jk < 2 || mbar_wait(k_free + (jk & 1), ((jk >> 1) - 1) & 1, abort_flag));
+        if (!__all_sync(0xffffffffu, ok)) break;
+        f2_v = kAhead ? f2_k : 0;
+        f2_k = convert_k(jk);
+        if (!kAhead) f2_v = f2_k;
+        blk_next = named(jk + 1, entry);
+        entry = entry_of(jk + 2);
+        if (jk + 1 < nmax) {
+          fetch(kcodes, blk_next, kc);
+          fetch_scales(jk + 1, blk_next);
         }
-        umma_commit(s_full + slot);
-      };
-      auto pv = [&](int tile, int slot, bool accumulate) {
-        const uint64_t pd = smem_desc_sw128(smem_u32(sP + slot * C::kPBytes), 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < kQ8Tok / 16; ++kk) {
-          const uint64_t off = static_cast<uint64_t>(((kk / 4) * C::kChunkBytes + (kk % 4) * 32) >> 4);
-          umma_ss(tmem + C::kColO + HD * tile, pd + off, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4),
-                  C::kIdescPV, (accumulate || kk > 0) ? 1u : 0u);
-        }
-        umma_commit(pv_done + slot);
-      };
-      bool ok = nmax > 0 && mbar_wait(q_full, 0, abort_flag) && mbar_wait(k_full, 0, abort_flag);
-      if (ok) {
-        tc_fence_after();
-#pragma unroll
-        for (int i = 0; i < (kTwo ? 2 : 1); ++i)
-          if (n[i] > 0) qk(i, i);
-        umma_commit(k_free);
+      } else if (kAhead) {
+        f2_v = f2_k;
       }
-      for (int j = 0; ok && j < nmax; ++j) {
-        if constexpr (kTwo) {
-          for (int i = 0; ok && i < 2; ++i) {
-            if (j >= n[i]) continue;
-            ok = mbar_wait(p_full + i, j & 1, abort_flag) && mbar_wait(v_full, j & 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            pv(i, i, j > 0);
-            if (j + 1 < n[i]) {  // S_i has been read: its P is here
-              ok = mbar_wait(k_full, (j + 1) & 1, abort_flag);
-              if (!ok) break;
-              tc_fence_after();
-              qk(i, i);
-            }
-          }
-          if (!ok) break;
-          umma_commit(v_free);
-          if (j + 1 < nmax) umma_commit(k_free);
-        } else {
-          if (j + 1 < nmax) {  // S of the other slot was read when P_{j-1} came
-            ok = mbar_wait(k_full, (j + 1) & 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            qk(0, (j + 1) & 1);
-            umma_commit(k_free);
-          }
-          ok = mbar_wait(p_full + (j & 1), (j >> 1) & 1, abort_flag) && mbar_wait(v_full, j & 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          pv(0, j & 1, j > 0);
-          umma_commit(v_free);
-        }
+      if (j >= 0) {
+        if (j > 0 && !__all_sync(0xffffffffu, mbar_wait(v_free, (j - 1) & 1, abort_flag))) break;
+        convert_v(j, f2_v);
+        blk_v = kAhead ? blk_k : blk_next;  // of tile j + 1
+        if (j + 1 < nmax) fetch(vcodes, blk_v, vc);
       }
-      // every product issued here completes before tensor memory is given back
-      umma_commit(drain);
-      volatile int never = 0;
-      mbar_wait(drain, 0, &never);
+      blk_k = blk_next;  // of tile jk + 1
     }
-  } else if (kTwo || warp < 4) {
-    // ------------------------------------------------------------------ softmax, epilogue
-    const int tile = warp / 4;
+  } else {
+    // ------------------------------------------------------------------ softmax, products, epilogue
+    const int side = warp / 4;
+    const int rtile = kTwo ? side : 0;
     const int lrow = threadIdx.x % 128;
-    const int row = row0 + 128 * tile + lrow;
+    const int row = row0 + 128 * rtile + lrow;
     const bool mine = row < p.R;
-    const int nt = n[tile];
+    const int cnt = n[side];
     const uint32_t lane_off = static_cast<uint32_t>((warp % 4) * 32) << 16;
-    {  // this thread's row of q, in the layout the tensor core reads
+    if (kTwo || side == 0) {  // this thread's row of q, in the layout the tensor core reads
       const uint16_t *src = p.q + (row_base + row) * HD;
-      uint8_t *dst = sQ + tile * C::kTileBytes;
+      uint8_t *dst = sQ + rtile * C::kTileBytes;
 #pragma unroll
       for (int c = 0; c < HD / 8; ++c) {
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -331,192 +474,231 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
+      if (lane == 0) mbar_arrive(q_full + rtile);
     }
+    const uint32_t tS = tmem + C::kColS + 128 * side, tO = tmem + C::kColO + HD * side;
+    uint8_t *pt = sP + side * C::kPBytes;
+    auto tile_of = [&](int i) { return kTwo ? i : 2 * i + side; };  // the side's i-th tile of tokens
+    // The first thread of the side's first warp issues its products.  With two row tiles it also
+    // arrives on k_free and v_free for the tiles of tokens that only the other one visits.
+    const bool lead = warp % 4 == 0 && lane == 0;
+    const int steps = kTwo ? nmax : cnt;
+    auto next_scores = [&](int i) -> bool {  // S of the side's tile i, or the word that K is not needed
+      if (i >= steps) return true;
+      const int j = tile_of(i);
+      if (!mbar_wait(k_full + (j & 1), (j >> 1) & 1, abort_flag)) return false;
+      if (i < cnt) {
+        tc_fence_after();
+        q8_issue_qk<HD>(tS, sQ + rtile * C::kTileBytes, k_tile(j));
+        umma_commit(s_full + side);
+        umma_commit(k_free + (kTwo ? 0 : side));
+      } else {
+        mbar_arrive(k_free);
+      }
+      return true;
+    };
+    auto products = [&](int i) -> bool {  // O += P V of the side's tile i, then the next scores
+      const int j = tile_of(i);
+      if (!mbar_wait(v_full + (j & 1), (j >> 1) & 1, abort_flag)) return false;
+      if (i < cnt) {
+        if (!mbar_wait(p_full + side, i & 1, abort_flag)) return false;
+        tc_fence_after();
+        q8_issue_pv<HD>(tO, pt, sV, i > 0);
+        umma_commit(pv_done + side);
+        umma_commit(v_free);
+      } else {
+        mbar_arrive(v_free);
+      }
+      return next_scores(i + 1);
+    };
+    // Turns: the two sides' warps of an SM sub-partition do their exponentials one after the other, so
+    // that one side's products run meanwhile; left alone they fall into step and wait together.
+    auto my_turn = [&](int i) -> bool {
+      if (i >= both || (side == 0 && i == 0)) return true;
+      return __all_sync(0xffffffffu, mbar_wait(turn + warp, (side == 0 ? i - 1 : i) & 1, abort_flag));
+    };
+    auto pass_turn = [&](int i) {
+      __syncwarp();
+      if (i < both && lane == 0) mbar_arrive(turn + (warp ^ 4));
+    };
     const int t = mine ? row % p.T : 0;
     const int first_own = L - p.T;  // the first of the queries' own tokens
     const uint64_t bits = (p.tree && mine) ? p.tree[static_cast<size_t>(s) * p.T + t] : ~0ull;
-    const bool warp_rows = row0 + 128 * tile + (warp % 4) * 32 < p.R;  // any row in this warp
-    float m = -INFINITY, l = 0.f;
-    const uint32_t tO = tmem + lane_off + C::kColO + HD * tile;
-    bool ok = true;
-    for (int j = 0; j < nt; ++j) {
-      const int slot = kTwo ? tile : (j & 1);
-      const uint32_t use = kTwo ? j : (j >> 1);  // how often the slot was used before
-      const uint32_t tS = tmem + lane_off + C::kColS + 128 * slot;
-      uint8_t *pt = sP + slot * C::kPBytes;
+    const bool warp_rows = row0 + 128 * rtile + (warp % 4) * 32 < p.R;  // any row in this warp
+    float m = -INFINITY, l = 0.f, F = 0.f;
+    bool poison = false;  // the row sees a token whose values are no numbers
+    bool ok = __all_sync(0xffffffffu,
+                         !lead || ((cnt == 0 || mbar_wait(q_full + rtile, 0, abort_flag)) && next_scores(0)));
+    for (int i = 0; ok && i < cnt; ++i) {
+      const int j = tile_of(i);
       const int buf = j % C::kScaleBufs;
-      const float *ksb = sKs + buf * kQ8Tok, *vsb = sVs + buf * kQ8Tok;
-      // warp-uniform, as the tensor-memory loads below are warp-wide
+      const float *ksb = sKs + buf * kQ8Tok;
+      // warp-uniform, as the tensor-memory loads below are warp-wide.  P V of the tile before has
+      // completed (its issue stood before these scores'), so P may be written and O rescaled.
       if (!__all_sync(0xffffffffu, mbar_wait(sc_full + buf, (j / C::kScaleBufs) & 1, abort_flag) &&
-                                       mbar_wait(s_full + slot, use & 1, abort_flag))) { ok = false; break; }
-      if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(pv_done + slot, (use - 1) & 1, abort_flag))) { ok = false; break; }
+                                       mbar_wait(s_full + side, i & 1, abort_flag) &&
+                                       (i == 0 || mbar_wait(pv_done + side, (i - 1) & 1, abort_flag))) ||
+          !my_turn(i)) { ok = false; break; }
       tc_fence_after();
       if (!warp_rows) {
-        // rows past R: whatever P holds goes to O rows that nobody reads
+        // rows past R: whatever P holds goes to O rows that nobody reads.  (The issuer's warp has
+        // rows, or the side has no tiles.)
+        pass_turn(i);
         tc_fence_before();
-        if (lane == 0) mbar_arrive(p_full + slot);
+        if (lane == 0) mbar_arrive(p_full + side);
         continue;
       }
       const int tok0 = (j0 + j) * kQ8Tok;
-      // which of the 32 tokens from tok0 + 32 c this row sees
-      auto seen = [&](int c) -> uint32_t {
-        uint32_t k = sLive[buf * 4 + c];
-        const int v0 = tok0 + 32 * c - first_own;
-        if (v0 + 31 >= 0) {
-          if (p.tree) {
-            const uint32_t b = v0 >= 64 ? 0u : v0 >= 0 ? static_cast<uint32_t>(bits >> v0)
-                                                       : (static_cast<uint32_t>(bits << -v0) | ((1u << -v0) - 1u));
-            k &= b;
-          } else if (p.causal) {
-            const int lim = t - v0 + 1;
-            k &= lim >= 32 ? ~0u : lim <= 0 ? 0u : (1u << lim) - 1u;
-          }
-        }
-        return k;
-      };
-      float sum, most;
-      auto pass = [&]() {  // p and p vs of the tile against the present reference; P to shared memory
-        const float neg = -m;
-        const uint64_t neg2 = f2_pack(neg, neg);
-        uint64_t sum2 = 0;
-        most = 0.f;
-        float sc[2][32];
-        tmem_ld32(tS, reinterpret_cast<uint32_t *>(sc[0]));
-        tmem_wait_ld();
-        q8_pin(sc[0]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c < 3) tmem_ld32(tS + 32 * (c + 1), reinterpret_cast<uint32_t *>(sc[(c + 1) & 1]));
-          const float(&x)[32] = sc[c & 1];
-          const uint32_t k = seen(c);
-          const bool some = __any_sync(0xffffffffu, k != 0xffffffffu);
-#pragma unroll
-          for (int e8 = 0; e8 < 4; ++e8) {
-            uint32_t pk[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int i = 8 * e8 + 2 * e;
-              const ulonglong2 ks4 = *reinterpret_cast<const ulonglong2 *>(ksb + 32 * c + (i & ~3));
-              const ulonglong2 vs4 = *reinterpret_cast<const ulonglong2 *>(vsb + 32 * c + (i & ~3));
-              const uint64_t ks2 = e & 1 ? ks4.y : ks4.x, vs2 = e & 1 ? vs4.y : vs4.x;
-              float y0, y1;
-              f2_unpack(f2_fma(f2_pack(x[i], x[i + 1]), ks2, neg2), y0, y1);
-              if (some) {
-                y0 = (k >> i) & 1 ? y0 : -INFINITY;
-                y1 = (k >> (i + 1)) & 1 ? y1 : -INFINITY;
-              }
-              const uint64_t w2 = f2_pack(ex2(y0), ex2(y1));
-              sum2 = f2_add(sum2, w2);
-              float v0, v1;
-              f2_unpack(f2_mul(w2, vs2), v0, v1);
-              if (some) {  // a token that is not seen may hold a scale that is not a number
-                v0 = (k >> i) & 1 ? v0 : 0.f;
-                v1 = (k >> (i + 1)) & 1 ? v1 : 0.f;
-              }
-              most = fmax3(most, v0, v1);
-              pk[e] = pack_fp16x2(v0, v1);
-            }
-            *reinterpret_cast<uint4 *>(pt + (c / 2) * C::kChunkBytes + q8_swz(lrow, 4 * (c & 1) + e8)) =
-                make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          }
-          if (c < 3) {
-            tmem_wait_ld();
-            q8_pin(sc[(c + 1) & 1]);
-          }
-        }
-        float s0, s1;
-        f2_unpack(sum2, s0, s1);
-        sum = s0 + s1;
-      };
-      bool over = true;
-      if (j > 0) {
-        pass();
-        over = sum > kQ8MostP || most > kQ8MostPv;
+      const float F_old = F;
+      F = sF[buf * 4];
+      uint32_t k[4];  // the tokens that this row sees
+      {
+        const uint4 live = *reinterpret_cast<const uint4 *>(sLive + buf * 4);
+        k[0] = live.x, k[1] = live.y, k[2] = live.z, k[3] = live.w;
       }
-      if (__any_sync(0xffffffffu, over)) {
-        float x = -INFINITY;
-#pragma unroll 1
+      if ((p.causal || p.tree) && tok0 + kQ8Tok > first_own) {
+#pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float sc[32];
-          tmem_ld32(tS + 32 * c, reinterpret_cast<uint32_t *>(sc));
-          const uint32_t k = seen(c);
-          tmem_wait_ld();
-          q8_pin(sc);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float y = sc[i] * ksb[32 * c + i];
-            if ((k >> i) & 1) x = fmaxf(x, fmaxf(y - kQ8Slack, y + lg2(vsb[32 * c + i])));
+          const int v0 = tok0 + 32 * c - first_own;  // the chunk's first token among the queries' own
+          if (p.tree) {
+            k[c] &= v0 >= 64 ? 0u : v0 >= 0 ? static_cast<uint32_t>(bits >> v0)
+                    : v0 > -32 ? (static_cast<uint32_t>(bits << -v0) | ((1u << -v0) - 1u)) : ~0u;
+          } else {
+            const int lim = t - v0 + 1;
+            k[c] &= lim >= 32 ? ~0u : lim <= 0 ? 0u : (1u << lim) - 1u;
           }
         }
-        const float a = !over ? 1.f : m == -INFINITY ? 0.f : ex2(m - x);
-        if (over) m = x;
-        l *= a;
-        if (j > 0) {
-          // the previous tile's product must be in O before it is rescaled
-          const int ps = kTwo ? tile : ((j - 1) & 1);
-          const uint32_t pu = kTwo ? j - 1 : ((j - 1) >> 1);
-          if (!__all_sync(0xffffffffu, mbar_wait(pv_done + ps, pu & 1, abort_flag))) { ok = false; break; }
-          tc_fence_after();
+      }
+      const bool all = __all_sync(0xffffffffu, (k[0] & k[1] & k[2] & k[3]) == 0xffffffffu);
+      {
+        const uint4 bad = *reinterpret_cast<const uint4 *>(sBad + buf * 4);
+        poison = poison || ((k[0] & bad.x) | (k[1] & bad.y) | (k[2] & bad.z) | (k[3] & bad.w)) != 0;
+      }
+      // one pass against the reference at hand; a second, after a look at all scores, where that
+      // has to move (at once on the first tile)
+      float sum;
+      bool over = true;
+      float a = F_old / F;  // what O is to be multiplied by
 #pragma unroll 1
-          for (int c = 0; c < HD; c += 32) {
-            float o[32];
-            tmem_ld32(tO + c, reinterpret_cast<uint32_t *>(o));
-            tmem_wait_ld();
-            q8_pin(o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= a;
-            tmem_st32(tO + c, reinterpret_cast<uint32_t *>(o));
-            tmem_wait_st();
+      for (int round = i == 0 ? 1 : 0;; ++round) {
+        if (round == 1) {
+          const float x = q8_row_max(tS + lane_off, k, ksb);
+          if (over) {  // a row that sees nothing yet keeps m = -inf
+            const float r = m == -INFINITY ? 0.f : ex2(m - (x - kQ8TileStart));
+            m = x - kQ8TileStart;
+            l *= r;
+            a *= r;
           }
         }
-        pass();
+        sum = all ? q8_weigh<HD, false>(tS + lane_off, k, ksb, m, pt, lrow)
+                  : q8_weigh<HD, true>(tS + lane_off, k, ksb, m, pt, lrow);
+        if (round == 1) break;
+        over = sum > kQ8TileMost;
+        if (!__any_sync(0xffffffffu, over)) break;
+      }
+      pass_turn(i);
+      if (i > 0 && __any_sync(0xffffffffu, a != 1.f)) {
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 32) {
+          float o[32];
+          tmem_ld32(tO + lane_off + c, reinterpret_cast<uint32_t *>(o));
+          tmem_wait_ld();
+          q8_pin(o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] *= a;
+          tmem_st32(tO + lane_off + c, reinterpret_cast<uint32_t *>(o));
+          tmem_wait_st();
+        }
       }
       l += sum;
       tc_fence_before();
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full + slot);
+      if (lane == 0) mbar_arrive(p_full + side);
+      ok = __all_sync(0xffffffffu, !lead || products(i));
     }
-    if (ok && nt > 0) {
-      const int last = nt - 1;
-      const int ps = kTwo ? tile : (last & 1);
-      const uint32_t pu = kTwo ? last : (last >> 1);
-      ok = __all_sync(0xffffffffu, mbar_wait(pv_done + ps, pu & 1, abort_flag));
-      tc_fence_after();
+    if (lead) {
+      for (int i = cnt; ok && i < steps; ++i) ok = products(i);
+      // every product issued here completes before tensor memory is given back
+      umma_commit(drain + side);
+      volatile int never = 0;
+      mbar_wait(drain + side, 0, &never);
     }
-    if (ok && warp_rows) {
-      const size_t out = row_base + row;
+    ok = __all_sync(0xffffffffu, ok && (cnt == 0 || mbar_wait(pv_done + side, (cnt - 1) & 1, abort_flag)));
+    tc_fence_after();
+    const float unit = q8_o_unit<kType>() / q8_vtop<kType>();
+    float f = F * unit;  // of this side's O
+    if constexpr (!kTwo) {
+      // join the sides: the odd tiles' sums go through shared memory (P is free: every product has
+      // completed), the even side writes.  Both are brought to the larger reference.
+      float *xo = reinterpret_cast<float *>(sP);                     // [feature][row]
+      float *xm = reinterpret_cast<float *>(sK);                     // m, l, poison of the odd side
+      q8_sides_barrier();  // neither side's products read P or K any more
+      if (side == 1 && warp_rows && ok) {
+        xm[lrow] = m;
+        xm[128 + lrow] = l;
+        xm[256 + lrow] = poison ? 1.f : 0.f;
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 32) {
+          float o[32];
+          if (cnt > 0) {
+            tmem_ld32(tO + lane_off + c, reinterpret_cast<uint32_t *>(o));
+            tmem_wait_ld();
+            q8_pin(o);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) xo[(c + e) * 128 + lrow] = cnt > 0 && l != 0.f ? o[e] * f : 0.f;
+        }
+      }
+      q8_sides_barrier();
+      if (side == 0 && warp_rows && ok) {
+        const float m1 = xm[lrow], l1 = xm[128 + lrow];
+        poison = poison || xm[256 + lrow] != 0.f;
+        const float M = l == 0.f ? m1 : l1 == 0.f ? m : fmaxf(m, m1);
+        const float a0 = l == 0.f ? 0.f : ex2(m - M), a1 = l1 == 0.f ? 0.f : ex2(m1 - M);
+        const bool none = l == 0.f;
+        l = (none ? 0.f : l * a0) + (l1 == 0.f ? 0.f : l1 * a1);
+        m = M;
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 32) {
+          float o[32];
+          if (cnt > 0) {
+            tmem_ld32(tO + lane_off + c, reinterpret_cast<uint32_t *>(o));
+            tmem_wait_ld();
+            q8_pin(o);
+          }
+          if (mine) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = (none ? 0.f : o[e] * f * a0) + (l1 == 0.f ? 0.f : xo[(c + e) * 128 + lrow] * a1);
+            q8_write32<HD>(p, row_base + row, split, c, o, m, l, poison);
+          }
+          __syncwarp();
+        }
+      }
+    } else if (ok && warp_rows) {
       const bool none = l == 0.f;
-      const float f = none ? 0.f : q8_o_unit<kType>();
 #pragma unroll 1
       for (int c = 0; c < HD; c += 32) {
         float o[32];
-        if (nt > 0) {
-          tmem_ld32(tO + c, reinterpret_cast<uint32_t *>(o));
+        if (cnt > 0) {
+          tmem_ld32(tO + lane_off + c, reinterpret_cast<uint32_t *>(o));
           tmem_wait_ld();
           q8_pin(o);
         }
         if (mine) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 v = none ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                  : make_float4(o[i] * f, o[i + 2] * f, o[i + 1] * f, o[i + 3] * f);
-            if (p.n_split > 1)
-              *reinterpret_cast<float4 *>(p.ws_o + (out * p.n_split + split) * HD + c + i) = v;
-            else
-              q8_write4<HD>(p, out, c + i, v, m, l);
-          }
+          for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * f;
+          q8_write32<HD>(p, row_base + row, split, c, o, m, l, poison);
         }
         __syncwarp();
       }
-      if (mine && p.n_split > 1) p.ws_ml[out * p.n_split + split] = make_float2(m, l);
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

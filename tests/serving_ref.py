@@ -74,7 +74,12 @@ def attention(q, k_pool, v_pool, ks, vs, table, lens, scale, causal=False, tree=
     normaliser) and by exp2's 2^-21.  p vs is rounded to fp16 against a reference that puts the row's
     largest p vs at 1 or above, or its largest p at 2^64 (values of scale 0): half a step is 2^-11 of
     it, or 2^-25 where it is below fp16's normal range, which is 2^-25 max(max w vs, 2^-64) of the
-    row's weights, and adds up over the codes.  LSE moves by the scores' error, plus the logarithm's."""
+    row's weights, and adds up over the codes.
+    With more than 16 rows per key head the value scales are folded into V instead: p, f = vs 2^a / F
+    and code * f are rounded to fp16, 2^-11 each.  The largest p is at least 2^6, so below fp16's
+    normal range it is off by 2^-31 of the largest weight.  F is at most twice the sequence's largest
+    vs; f, at most 2^14 (e4m3, codes to 1.75) or 2^8 (int8, codes to 127), and the product lose 2^-25
+    each there: below 2^-24 of that vs per unit of weight.  LSE moves by the scores' error, plus the logarithm's."""
     q = q.double().cpu()
     S, Hq, T, d = q.shape
     Hk = k_pool.shape[1]
@@ -116,9 +121,15 @@ def attention(q, k_pool, v_pool, ks, vs, table, lens, scale, causal=False, tree=
             far = torch.log2(f[f > 0]).abs().max() if bool((f > 0).any()) else 0.0
             lb[s, h] = (2.0 ** -18 * e + 2.0 ** -20 * (1.0 + lse[s, h].abs().nan_to_num(0.0, posinf=0.0))
                         + 2.0 ** -24 * (16.0 + far))
-            top = (w * f[:, 0]).amax(-1, keepdim=True).clamp(min=2.0 ** -64) if len(f) else 0.0
-            ob[s, h] = ((2.0 ** -11 + 2.0 ** -17 * e + 2.0 ** -18)[:, None] * (w @ V.abs())
-                        + 2.0 ** -25 * top * (w > 0).double() @ codes)
+            seen = (w > 0).double()
+            if Hq // Hk * T <= 16:
+                top = (w * f[:, 0]).amax(-1, keepdim=True).clamp(min=2.0 ** -64) if len(f) else 0.0
+                floor, steps = 2.0 ** -25 * top * seen @ codes, 1
+            else:
+                top = w.amax(-1, keepdim=True) if len(f) else 0.0
+                largest = vs[pages[named[::PAGE]].to(vs.device), h // (Hq // Hk)].nan_to_num(0.0).max()
+                floor, steps = 2.0 ** -31 * top * (seen @ V.abs()) + 2.0 ** -24 * float(largest), 3
+            ob[s, h] = (steps * 2.0 ** -11 + 2.0 ** -17 * e + 2.0 ** -18)[:, None] * (w @ V.abs()) + floor
     return o, lse, ob, lb
 
 
