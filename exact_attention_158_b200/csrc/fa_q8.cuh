@@ -53,23 +53,15 @@ struct Q8Params {
   float scale_log2;
 };
 
-// ---- codes to 16-bit pairs -------------------------------------------------------------------
-// Keys, against bf16 queries: e4m3 seeeemmm moved to bf16's s0000eeee mmm0000 is the value times
-// 2^-120, subnormals included; int8 c is (128 + low 7 bits) - (128, or 256 when negative), both
-// exact in bf16.  Values, against fp16 weights: e4m3 moved to fp16's s0eeeemm m000000 is the value
-// times 2^-8; int8 c is fp16's 1024 + (c + 128) less 1152.
-// lo takes bytes 0 and 2 of the word, hi bytes 1 and 3.
-__device__ __forceinline__ uint32_t q8_bf16_e4m3(uint32_t x) {  // codes in bytes 1 and 3
-  return (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
-}
-__device__ __forceinline__ uint32_t q8_bf16_int8(uint32_t x) {  // codes in bytes 0 and 2
-  const uint32_t a = (x & 0x007f007fu) | 0x43004300u, b = (x & 0x00800080u) | 0x43004300u;
+// ---- codes to fp16 pairs ---------------------------------------------------------------------
+// Both types are exact in fp16.  e4m3: the hardware's conversion, a pair at a time: lo takes bytes 0, 1
+// of the word and hi bytes 2, 3.  int8: c is fp16's 1024 + (c + 128) less 1152; lo takes bytes 0, 2
+// and hi bytes 1, 3.  kQ8Pick picks from two words what makes lo pair byte 0 (or 2) of the first with
+// that of the second, and hi byte 1 (or 3).
+__device__ __forceinline__ uint32_t q8_fp16_e4m3(uint32_t x) {  // the two codes in the low half
   uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(r) : "r"(x));
   return r;
-}
-__device__ __forceinline__ uint32_t q8_fp16_e4m3(uint32_t x) {
-  return (x & 0x80008000u) | ((x >> 1) & 0x3f803f80u);
 }
 __device__ __forceinline__ uint32_t q8_fp16_int8(uint32_t x) {
   uint32_t r;
@@ -77,43 +69,35 @@ __device__ __forceinline__ uint32_t q8_fp16_int8(uint32_t x) {
   return r;
 }
 template <int kType>
-__device__ __forceinline__ void q8_key4(uint32_t x, uint32_t &lo, uint32_t &hi) {
+__device__ __forceinline__ void q8_cvt4(uint32_t x, uint32_t &lo, uint32_t &hi) {
   if constexpr (kType == kQ8E4m3) {
-    lo = q8_bf16_e4m3(x << 8);
-    hi = q8_bf16_e4m3(x);
-  } else {
-    lo = q8_bf16_int8(x);
-    hi = q8_bf16_int8(x >> 8);
-  }
-}
-template <int kType>
-__device__ __forceinline__ void q8_value4(uint32_t x, uint32_t &lo, uint32_t &hi) {
-  if constexpr (kType == kQ8E4m3) {
-    lo = q8_fp16_e4m3(x << 8);
-    hi = q8_fp16_e4m3(x);
+    lo = q8_fp16_e4m3(x);
+    hi = q8_fp16_e4m3(x >> 16);
   } else {
     lo = q8_fp16_int8(x);
     hi = q8_fp16_int8(x >> 8);
   }
 }
-// e4m3: q is multiplied by 2^64 (exact) so that q . k stays well above fp32's smallest normal; the
-// scores then carry 2^(64 - 120), and O carries the values' 2^-8.
-template <int kType> __device__ constexpr float q8_score_unit() { return kType == kQ8E4m3 ? 0x1p56f : 1.f; }
-template <int kType> __device__ constexpr float q8_o_unit() { return kType == kQ8E4m3 ? 0x1p8f : 1.f; }
-
-__device__ __forceinline__ uint32_t q8_scale_q(uint32_t bf16x2) {
-  uint32_t r;  // times 2^64 in each half
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(bf16x2), "r"(0x5f805f80u));
-  return r;
+template <int kType>
+__device__ __forceinline__ uint32_t q8_pick(uint32_t a, uint32_t b, int half) {
+  if constexpr (kType == kQ8E4m3) return __byte_perm(a, b, half ? 0x7362 : 0x5140);
+  return __byte_perm(a, b, half ? 0x7632 : 0x5410);
 }
 
-__device__ __forceinline__ void mma_bf16_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                                 uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// Queries in fp16: a power of two, the row's own, brings its largest feature to 2^14, so that bf16's 8
+// bits stay exact over 28 binades below it (and lose 2^-39 of it beyond); scores are divided by it.
+__device__ __forceinline__ float q8_q_unit(float top) {  // of the largest finite |q|
+  const uint32_t e = min(max((__float_as_uint(top) >> 23) & 0xffu, 15u), 254u);
+  return __uint_as_float((254u + 14u - e) << 23);
 }
+__device__ __forceinline__ float q8_inverse(float u) {  // of a power of two
+  return __uint_as_float((254u << 23) - __float_as_uint(u));
+}
+__device__ __forceinline__ float q8_finite_max(float top, uint32_t bf16x2) {
+  const float a = fabsf(__uint_as_float(bf16x2 << 16)), b = fabsf(__uint_as_float(bf16x2 & 0xffff0000u));
+  return fmaxf(top, fmaxf(a < INFINITY ? a : 0.f, b < INFINITY ? b : 0.f));
+}
+
 __device__ __forceinline__ void mma_fp16_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                                  uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -217,28 +201,39 @@ __global__ void __launch_bounds__(kQ8Threads)
   __syncthreads();
 
   // q: column n = g of the score tile is row row0 + 8 nt + g; this lane holds the features that it
-  // reads of K (units kUnits c + i, words w), as (byte 0, byte 2) and (byte 1, byte 3) pairs
+  // reads of K (units kUnits c + i, words w), paired as the conversion pairs codes
   uint32_t qb[NT][4 * kUnits][2];
-  int tq[NT][2];  // query index t of the two rows (columns 2c, 2c + 1) whose scores this lane holds
+  float sc[NT][2];  // score scale of the two rows (columns 2c, 2c + 1) whose scores this lane holds
+  int tq[NT][2];    // and their query index t
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int row = row0 + 8 * nt + g;
     const uint16_t *src = p.q + (row_base + row) * HD + 16 * kUnits * c;
+    uint2 v[4 * kUnits];
+    float top = 0.f;
 #pragma unroll
     for (int k = 0; k < 4 * kUnits; ++k) {
-      uint2 v = make_uint2(0u, 0u);
-      if (row < p.R) v = *reinterpret_cast<const uint2 *>(src + 4 * k);
-      qb[nt][k][0] = __byte_perm(v.x, v.y, 0x5410);  // features 0, 2
-      qb[nt][k][1] = __byte_perm(v.x, v.y, 0x7632);  // features 1, 3
-      if constexpr (kType == kQ8E4m3) {
-        qb[nt][k][0] = q8_scale_q(qb[nt][k][0]);
-        qb[nt][k][1] = q8_scale_q(qb[nt][k][1]);
-      }
+      v[k] = make_uint2(0u, 0u);
+      if (row < p.R) v[k] = *reinterpret_cast<const uint2 *>(src + 4 * k);
+      top = q8_finite_max(q8_finite_max(top, v[k].x), v[k].y);
     }
-    tq[nt][0] = (row0 + 8 * nt + 2 * c) % p.T;
-    tq[nt][1] = (row0 + 8 * nt + 2 * c + 1) % p.T;
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const float unit = q8_q_unit(top);
+#pragma unroll
+    for (int k = 0; k < 4 * kUnits; ++k) {
+      const float f0 = __uint_as_float(v[k].x << 16) * unit, f1 = __uint_as_float(v[k].x & 0xffff0000u) * unit;
+      const float f2 = __uint_as_float(v[k].y << 16) * unit, f3 = __uint_as_float(v[k].y & 0xffff0000u) * unit;
+      qb[nt][k][0] = kType == kQ8E4m3 ? pack_fp16x2(f0, f1) : pack_fp16x2(f0, f2);
+      qb[nt][k][1] = kType == kQ8E4m3 ? pack_fp16x2(f2, f3) : pack_fp16x2(f1, f3);
+    }
+    const float inv = p.scale_log2 * q8_inverse(unit);  // of row g: lane 4 g holds it
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      sc[nt][e] = __shfl_sync(0xffffffffu, inv, 4 * (2 * c + e));
+      tq[nt][e] = (row0 + 8 * nt + 2 * c + e) % p.T;
+    }
   }
-  const float sc = p.scale_log2 * q8_score_unit<kType>();
 
   float acc[NT][kMT][4];
   float m[NT][2], l[NT][2];
@@ -322,7 +317,7 @@ __global__ void __launch_bounds__(kQ8Threads)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       in[r] = named && tok0 + g + 8 * r < L;
-      kss[r] = in[r] ? sp[g + 8 * r] * sc : 0.f;
+      kss[r] = in[r] ? sp[g + 8 * r] : 0.f;
       vss[r] = in[r] ? sp[kQ8Page + g + 8 * r] : 0.f;
     }
     float sa[NT][4];
@@ -337,11 +332,11 @@ __global__ void __launch_bounds__(kQ8Threads)
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         uint32_t a0, a1, a2, a3;
-        q8_key4<kType>(w0[w], a0, a2);
-        q8_key4<kType>(w1[w], a1, a3);
+        q8_cvt4<kType>(w0[w], a0, a2);
+        q8_cvt4<kType>(w1[w], a1, a3);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          mma_bf16_16x8x16(sa[nt], a0, a1, a2, a3, qb[nt][4 * k + w][0], qb[nt][4 * k + w][1]);
+          mma_fp16_16x8x16(sa[nt], a0, a1, a2, a3, qb[nt][4 * k + w][0], qb[nt][4 * k + w][1]);
       }
     }
     // V: tokens 2c, 2c+1, 2c+8, 2c+9, features (HD / 8) g ..
@@ -355,6 +350,15 @@ __global__ void __launch_bounds__(kQ8Threads)
       } else {
         const uint2 x = *reinterpret_cast<const uint2 *>(vp + row * HD + 16 * ((g >> 1) ^ ((row >> 1) & 3)) + 8 * (g & 1));
         vw[r][0] = x.x, vw[r][1] = x.y;
+      }
+    }
+    // a slot past the sequence's end may hold any bytes, and e4m3's NaN would pass through p = 0
+    if (kType == kQ8E4m3 && (!named || tok0 + kQ8Page > L)) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const bool keep = named && tok0 + 2 * c + (r & 1) + 8 * (r >> 1) < L;
+#pragma unroll
+        for (int w = 0; w < kVW; ++w) vw[r][w] = keep ? vw[r][w] : 0u;
       }
     }
     __syncwarp();  // every lane has read the stage: refill it
@@ -387,7 +391,7 @@ __global__ void __launch_bounds__(kQ8Threads)
               else if (p.causal) see = v <= tq[nt][e];
             }
           }
-          sa[nt][2 * r + e] = see ? sa[nt][2 * r + e] * kss[r] : -INFINITY;
+          sa[nt][2 * r + e] = see ? sa[nt][2 * r + e] * (kss[r] * sc[nt][e]) : -INFINITY;
         }
     float pw[NT][4];
     auto weigh = [&]() {  // p and p vs against the present references; true when one passes its limit
@@ -451,10 +455,9 @@ __global__ void __launch_bounds__(kQ8Threads)
     for (int w = 0; w < kVW; ++w) {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        constexpr uint32_t kPick[2] = {0x5410u, 0x7632u};  // two features of two tokens
         uint32_t a0, a1, a2, a3;
-        q8_value4<kType>(__byte_perm(vw[0][w], vw[1][w], kPick[half]), a0, a1);
-        q8_value4<kType>(__byte_perm(vw[2][w], vw[3][w], kPick[half]), a2, a3);
+        q8_cvt4<kType>(q8_pick<kType>(vw[0][w], vw[1][w], half), a0, a1);
+        q8_cvt4<kType>(q8_pick<kType>(vw[2][w], vw[3][w], half), a2, a3);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
           mma_fp16_16x8x16(acc[nt][2 * w + half], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
@@ -487,7 +490,7 @@ __global__ void __launch_bounds__(kQ8Threads)
       for (int w = 0; w < kQ8Warps; ++w) M = fmaxf(M, sm_m[w][row]);
       // a warp that saw no token has l = 0 and takes no part; a NaN stays one
       const bool none = sm_l[warp][row] == 0.f;
-      const float f = ex2(m[nt][e] - M) * q8_o_unit<kType>();
+      const float f = ex2(m[nt][e] - M);
       float *dst = part + (warp * kRows + row) * HD + (HD / 8) * g;
 #pragma unroll
       for (int j = 0; j < kMT; ++j) {

@@ -8,7 +8,7 @@
 //   warps 0-3    one side: a thread holds a row (a TMEM lane).  Scores out of TMEM, p to shared
 //                memory; one thread issues the side's products
 //   warps 4-7    the other side
-//   warps 8-11   codes: global (one tile ahead, in registers) -> bf16 K / fp16 V tiles in the
+//   warps 8-11   codes: global (one tile ahead, in registers) -> fp16 K and V tiles in the
 //                swizzled layout the tensor core reads; the tile's key scales and its live tokens
 // TMEM (512 columns): S0 [0,128)  S1 [128,256)  O0 [256,256+d)  O1 [256+d,256+2d).
 // With more than 128 rows the sides hold two row tiles; with fewer they share one row tile and take
@@ -30,8 +30,9 @@
 // only when their sum passes 2^15 (always on a row's first tile) or F has grown does the warp go back to
 // S, move the references so that the largest p is 2^6, rescale O in TMEM and do the pass again.
 //
-// The conversion leaves every four features in the order 0, 2, 1, 3; q is stored in that order too, and
-// O's columns are put back when it is written.
+// Queries go to fp16 against one power of two for all rows of the CTA (q8_q_unit; it is part of the key
+// scales).  int8's conversion leaves every four features in the order 0, 2, 1, 3; q is stored in that
+// order too, and O's columns are put back when it is written.
 //
 // Bound: per 128 x 128 scores the products take about 1020 cycles at d = 128 and the exponentials
 // 1024 (16 a cycle); the tile's 32 KB of codes take about 1400 cycles of the SM's share of HBM.
@@ -45,8 +46,8 @@ constexpr int kQ8TileThreads = 12 * 32;
 constexpr int kQ8Tok = 128;                 // tokens of a tile
 constexpr float kQ8TileMost = 0x1p15f;      // a tile's sum of p, and so any p: fp16 ends at 2^16
 constexpr float kQ8TileStart = 6.f;         // log2 of the largest p after the reference has moved
-// f at the largest vs: e4m3 codes are at most 1.75 in fp16 units (448 2^-8), int8 codes 127
-template <int kType> __device__ constexpr float q8_vtop() { return kType == kQ8E4m3 ? 0x1p14f : 0x1p8f; }
+// f at the largest vs: e4m3 codes are at most 448, int8 codes 127
+template <int kType> __device__ constexpr float q8_vtop() { return kType == kQ8E4m3 ? 0x1p6f : 0x1p8f; }
 
 template <int HD>
 struct Q8TileCfg {
@@ -57,14 +58,20 @@ struct Q8TileCfg {
   static constexpr int kScaleBufs = 4;
   static constexpr int kBars = 30;
   static constexpr size_t kSmem = 1024 + 2 * kTileBytes + 2 * kTileBytes + 2 * kPBytes +
-                                  kScaleBufs * (kQ8Tok * 4 + 48) + kBars * 8 + 16;
+                                  kScaleBufs * (kQ8Tok * 4 + 48) + kBars * 8 + 48;
   static constexpr uint32_t kColS = 0, kColO = 256;
-  static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, 0, 0);
   // fp16 operands: the type fields of A and B are 0
-  static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, HD, 0, 1) & ~((1u << 7) | (1u << 10));
+  static constexpr uint32_t kFp16 = ~((1u << 7) | (1u << 10));
+  static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, 0, 0) & kFp16;
+  static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, HD, 0, 1) & kFp16;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static_assert(kSmem > 114 * 1024, "one CTA per SM: it takes all of the tensor memory");
 };
+
+// Two bf16 features times a power of two, in fp16.
+__device__ __forceinline__ uint32_t q8_fp16_of(uint32_t bf16x2, float unit) {
+  return pack_fp16x2(__uint_as_float(bf16x2 << 16) * unit, __uint_as_float(bf16x2 & 0xffff0000u) * unit);
+}
 
 // 16-byte unit `unit` of row `row` in a 128-byte-swizzled chunk.
 __device__ __forceinline__ uint32_t q8_swz(int row, int unit) {
@@ -163,13 +170,15 @@ __device__ __forceinline__ float q8_row_max(uint32_t s_tmem, const uint32_t (&k)
 }
 
 // 32 features of a row, in the conversion's order, from its sums: to the output, or as a partial.
-template <int HD>
+template <int HD, int kType>
 __device__ __forceinline__ void q8_write32(const Q8Params &p, size_t row, int split, int c, const float (&o)[32],
                                            float m, float l, bool poison) {
   const float nan = __int_as_float(0x7fc00000);
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
-    const float4 v = poison ? make_float4(nan, nan, nan, nan) : make_float4(o[i], o[i + 2], o[i + 1], o[i + 3]);
+    const float4 v = poison ? make_float4(nan, nan, nan, nan)
+                     : kType == kQ8Int8 ? make_float4(o[i], o[i + 2], o[i + 1], o[i + 3])
+                                        : make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
     if (p.n_split > 1)
       *reinterpret_cast<float4 *>(p.ws_o + (row * p.n_split + split) * HD + c + i) = v;
     else
@@ -245,7 +254,8 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
   uint64_t *drain = bars + 17;                  // [side] every product of an issuer has completed
   uint64_t *q_full = bars + 19;                 // [row tile]
   uint64_t *turn = bars + 21;                   // [side][warp]
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kBars);
+  float *sTop = reinterpret_cast<float *>(bars + C::kBars);  // [8]: the warps' largest |q|
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sTop + 8);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
   unsigned u = blockIdx.x;
@@ -295,10 +305,29 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
+  if (warp < 8) {
+    const int row = row0 + (kTwo ? 128 * (warp / 4) : 0) + threadIdx.x % 128;
+    float top = 0.f;
+    if (row < p.R) {
+      const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (row_base + row) * HD);
+#pragma unroll
+      for (int c = 0; c < HD / 8; ++c) {
+        const uint4 v = src[c];
+        top = q8_finite_max(q8_finite_max(q8_finite_max(q8_finite_max(top, v.x), v.y), v.z), v.w);
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    if (lane == 0) sTop[warp] = top;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  float q_top = sTop[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) q_top = fmaxf(q_top, sTop[i]);
+  const float q_unit = q8_q_unit(q_top);
   auto k_tile = [&](int j) { return (kTwo || !(j & 1)) ? sK : sQ + C::kTileBytes; };
 
   if (warp >= 8) {
@@ -358,7 +387,7 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
       }
     };
     float F = 0x1p-126f;  // every warp finds the same F, tile by tile
-    const float score_scale = p.scale_log2 * q8_score_unit<kType>();
+    const float score_scale = p.scale_log2 * q8_inverse(q_unit);
     // K of tile j and the tile's scales; returns f of this lane's token, twice
     auto convert_k = [&](int j) -> uint32_t {
       const int buf = j % C::kScaleBufs;
@@ -385,8 +414,8 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
       for (int k = 0; k < kLoads; ++k) {
         const int row = 32 * w + k * kRowsPer + sub;
         uint4 o;
-        q8_key4<kType>(kc[k].x, o.x, o.y);
-        q8_key4<kType>(kc[k].y, o.z, o.w);
+        q8_cvt4<kType>(kc[k].x, o.x, o.y);
+        q8_cvt4<kType>(kc[k].y, o.z, o.w);
         *reinterpret_cast<uint4 *>(kt + q8_swz(row, unit)) = o;
       }
       fence_async_smem();
@@ -398,14 +427,17 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
       const float fs = bad ? 0.f : mine / F * q8_vtop<kType>();  // vs / F first: neither factor overflows
       return pack_fp16x2(fs, fs);
     };
-    auto convert_v = [&](int j, uint32_t f2) {
+    auto convert_v = [&](int j, uint32_t f2, uint32_t live_v) {
+      const bool all = live_v == 0xffffffffu;
 #pragma unroll
       for (int k = 0; k < kLoads; ++k) {
         const int row = 32 * w + k * kRowsPer + sub;
         uint4 o;
         const uint32_t f = __shfl_sync(0xffffffffu, f2, k * kRowsPer + sub);
-        q8_value4<kType>(vc[k].x, o.x, o.y);
-        q8_value4<kType>(vc[k].y, o.z, o.w);
+        // a slot that no token holds may have any bytes, and e4m3's NaN would pass through p = 0
+        if (kType == kQ8E4m3 && !all && !((live_v >> (k * kRowsPer + sub)) & 1)) vc[k] = make_uint2(0u, 0u);
+        q8_cvt4<kType>(vc[k].x, o.x, o.y);
+        q8_cvt4<kType>(vc[k].y, o.z, o.w);
         o = make_uint4(mul_fp16x2(o.x, f), mul_fp16x2(o.y, f), mul_fp16x2(o.z, f), mul_fp16x2(o.w, f));
         *reinterpret_cast<uint4 *>(sV + at0 + q8_swz(row, unit)) = o;
       }
@@ -422,7 +454,8 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
       fetch_scales(0, blk_k);
       fetch(vcodes, blk_v, vc);
     }
-    uint32_t f2_v = 0, f2_k = 0;  // f of the next V tile, and of the tile whose K was made last
+    // f and the live tokens of the next V tile, and of the tile whose K was made last
+    uint32_t f2_v = 0, f2_k = 0, live_v = 0, live_k = 0;
     for (int j = -kAhead; j < nmax; ++j) {
       const int jk = j + kAhead;
       int blk_next = blk_k;
@@ -430,21 +463,22 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
         const bool ok = kTwo ? (jk < 1 || mbar_wait(k_free, (jk - 1) & 1, abort_flag))
                              : (jk < 2 || mbar_wait(k_free + (jk & 1), ((jk >> 1) - 1) & 1, abort_flag));
         if (!__all_sync(0xffffffffu, ok)) break;
-        f2_v = kAhead ? f2_k : 0;
+        f2_v = f2_k, live_v = live_k;
+        live_k = live;
         f2_k = convert_k(jk);
-        if (!kAhead) f2_v = f2_k;
+        if (!kAhead) f2_v = f2_k, live_v = live_k;
         blk_next = named(jk + 1, entry);
         entry = entry_of(jk + 2);
         if (jk + 1 < nmax) {
           fetch(kcodes, blk_next, kc);
           fetch_scales(jk + 1, blk_next);
         }
-      } else if (kAhead) {
-        f2_v = f2_k;
+      } else {
+        f2_v = f2_k, live_v = live_k;
       }
       if (j >= 0) {
         if (j > 0 && !__all_sync(0xffffffffu, mbar_wait(v_free, (j - 1) & 1, abort_flag))) break;
-        convert_v(j, f2_v);
+        convert_v(j, f2_v, live_v);
         blk_v = kAhead ? blk_k : blk_next;  // of tile j + 1
         if (j + 1 < nmax) fetch(vcodes, blk_v, vc);
       }
@@ -466,10 +500,11 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
       for (int c = 0; c < HD / 8; ++c) {
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (mine) v = *reinterpret_cast<const uint4 *>(src + 8 * c);
-        v = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
-                       __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
-        if constexpr (kType == kQ8E4m3)
-          v = make_uint4(q8_scale_q(v.x), q8_scale_q(v.y), q8_scale_q(v.z), q8_scale_q(v.w));
+        if constexpr (kType == kQ8Int8)
+          v = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
+                         __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
+        v = make_uint4(q8_fp16_of(v.x, q_unit), q8_fp16_of(v.y, q_unit), q8_fp16_of(v.z, q_unit),
+                       q8_fp16_of(v.w, q_unit));
         *reinterpret_cast<uint4 *>(dst + (c / 8) * C::kChunkBytes + q8_swz(lrow, c % 8)) = v;
       }
       fence_async_smem();
@@ -626,8 +661,7 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
     }
     ok = __all_sync(0xffffffffu, ok && (cnt == 0 || mbar_wait(pv_done + side, (cnt - 1) & 1, abort_flag)));
     tc_fence_after();
-    const float unit = q8_o_unit<kType>() / q8_vtop<kType>();
-    float f = F * unit;  // of this side's O
+    const float f = F / q8_vtop<kType>();  // of this side's O
     if constexpr (!kTwo) {
       // join the sides: the odd tiles' sums go through shared memory (P is free: every product has
       // completed), the even side writes.  Both are brought to the larger reference.
@@ -671,7 +705,7 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               o[e] = (none ? 0.f : o[e] * f * a0) + (l1 == 0.f ? 0.f : xo[(c + e) * 128 + lrow] * a1);
-            q8_write32<HD>(p, row_base + row, split, c, o, m, l, poison);
+            q8_write32<HD, kType>(p, row_base + row, split, c, o, m, l, poison);
           }
           __syncwarp();
         }
@@ -689,7 +723,7 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
         if (mine) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * f;
-          q8_write32<HD>(p, row_base + row, split, c, o, m, l, poison);
+          q8_write32<HD, kType>(p, row_base + row, split, c, o, m, l, poison);
         }
         __syncwarp();
       }

@@ -384,9 +384,10 @@ size_t fa_q8_workspace_size(int S, int Hq, int Hk, int Lq, int d, int max_blocks
  *
  *   q              bf16 [S, Hq, d] (decode) or [S, Hq, Lq, d], contiguous.
  *   k_pool, v_pool   codes [num_blocks, Hk, 16, d];  k_scale, v_scale: fp32 [num_blocks, Hk, 16];
- *                  all 16-byte aligned.  type: FA_CACHE_E4M3 or FA_CACHE_INT8.  A NaN scale makes
- *                  its token NaN for the rows that see it; e4m3's own NaN codes (0x7f, 0xff), which
- *                  fa_cache_append never writes, count as +-480.
+ *                  all 16-byte aligned.  type: FA_CACHE_E4M3 or FA_CACHE_INT8.  Scales are >= 0; a
+ *                  NaN scale makes its token NaN for the rows that see it.  The tokens of a sequence
+ *                  hold no e4m3 NaN codes (0x7f, 0xff; fa_cache_append writes none); other slots of
+ *                  the pool may hold anything.
  *   block_table    int32 [S, max_blocks_per_seq], device; a page whose entry is outside
  *                  [0, num_blocks) is left out and reported (FA_ERR_INVALID_ARG).
  *   seq_lens       int32 [S], device, each in [Lq, 16 * max_blocks_per_seq], or <= 0 for an empty
@@ -399,8 +400,7 @@ size_t fa_q8_workspace_size(int S, int Hq, int Hk, int Lq, int d, int max_blocks
  *   workspace      device scratch of at least fa_q8_workspace_size(...) bytes, 16-byte aligned (may
  *                  be null when that is 0); no initialisation needed, garbage afterwards.  Two calls
  *                  in flight at once need separate workspaces.
- * |q| must stay below 2^63 for the e4m3 type (it is scaled by 2^64 on the way).  Results do not
- * depend on what else runs: there are no atomics in the sums.
+ * Results do not depend on what else runs: there are no atomics in the sums.
  * Returns FA_OK once the kernels are queued.
  */
 fa_status fa_decode_paged_q8(const void *q, const void *k_pool, const void *v_pool,

@@ -78,8 +78,9 @@ def attention(q, k_pool, v_pool, ks, vs, table, lens, scale, causal=False, tree=
     With more than 16 rows per key head the value scales are folded into V instead: p, f = vs 2^a / F
     and code * f are rounded to fp16, 2^-11 each.  The largest p is at least 2^6, so below fp16's
     normal range it is off by 2^-31 of the largest weight.  F is at most twice the sequence's largest
-    vs; f, at most 2^14 (e4m3, codes to 1.75) or 2^8 (int8, codes to 127), and the product lose 2^-25
-    each there: below 2^-24 of that vs per unit of weight.  LSE moves by the scores' error, plus the logarithm's."""
+    vs.  f is at most 2^6 (e4m3, codes to 448) or 2^8 (int8, codes to 127); where it is below fp16's
+    normal range it loses 2^-25, times a code, and so does the product: below 2^-21 of that vs per unit
+    of weight.  LSE moves by the scores' error, plus the logarithm's."""
     q = q.double().cpu()
     S, Hq, T, d = q.shape
     Hk = k_pool.shape[1]
@@ -128,7 +129,7 @@ def attention(q, k_pool, v_pool, ks, vs, table, lens, scale, causal=False, tree=
             else:
                 top = w.amax(-1, keepdim=True) if len(f) else 0.0
                 largest = vs[pages[named[::PAGE]].to(vs.device), h // (Hq // Hk)].nan_to_num(0.0).max()
-                floor, steps = 2.0 ** -31 * top * (seen @ V.abs()) + 2.0 ** -24 * float(largest), 3
+                floor, steps = 2.0 ** -31 * top * (seen @ V.abs()) + 2.0 ** -21 * float(largest), 3
             ob[s, h] = (steps * 2.0 ** -11 + 2.0 ** -17 * e + 2.0 ** -18)[:, None] * (w @ V.abs()) + floor
     return o, lse, ob, lb
 
