@@ -30,8 +30,8 @@ namespace fa {
 constexpr int kQ8Page = 16;
 constexpr int kQ8Warps = 4;
 constexpr int kQ8Threads = 32 * kQ8Warps;
-constexpr int kQ8Stages = 4;
 constexpr float kQ8MostPv = 0x1p10f, kQ8MostP = 0x1p100f;  // past these the reference moves
+constexpr uint32_t kQ8MostPvBits = 0x6400u;                // 2^10 in fp16
 constexpr float kQ8Slack = 64.f;                           // log2: p stays below 2^64 after a move
 
 enum Q8Type { kQ8E4m3 = 1, kQ8Int8 = 2 };
@@ -110,6 +110,11 @@ __device__ __forceinline__ uint32_t pack_fp16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ uint32_t max_fp16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -127,9 +132,12 @@ template <int HD>
 struct Q8Cfg {
   static constexpr int kSlab = kQ8Page * HD;              // bytes of one page of one head
   static constexpr int kStage = 2 * kSlab;
-  static constexpr int kRing = kQ8Warps * kQ8Stages * kStage;
-  static constexpr int kScales = kQ8Warps * kQ8Stages * 2 * kQ8Page * 4;
-  static constexpr int kBars = kQ8Warps * kQ8Stages * 8;
+  // d = 128: three stages let four CTAs share an SM (16 warps, 200 KB in flight); with four stages
+  // and three CTAs the same bytes are in flight but fewer warps compute (QQQQ)
+  static constexpr int kStages = HD == 128 ? 3 : 4;
+  static constexpr int kRing = kQ8Warps * kStages * kStage;
+  static constexpr int kScales = kQ8Warps * kStages * 2 * kQ8Page * 4;
+  static constexpr int kBars = kQ8Warps * kStages * 8;
   static constexpr int kSmem = kRing + kScales + kBars + 1024;  // + alignment of the ring
 };
 
@@ -160,7 +168,7 @@ __device__ __forceinline__ void q8_write4(const Q8Params &p, size_t row, int e0,
 
 // One CTA: one chunk of the context of one (sequence, key head), 8 NT query rows.
 template <int HD, int NT, int kType>
-__global__ void __launch_bounds__(kQ8Threads)
+__global__ void __launch_bounds__(kQ8Threads, (HD == 128 ? 5 : 6) - NT)
     fa_q8_stream_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                         const Q8Params p) {
   using C = Q8Cfg<HD>;
@@ -195,7 +203,7 @@ __global__ void __launch_bounds__(kQ8Threads)
   if (threadIdx.x == 0) {
     abort_flag = 0;
     if (L != p.lens[s] && p.lens[s] > 0) atomicExch(&g_device_status, 1 /* FA_ERR_INVALID_ARG */);
-    for (int i = 0; i < kQ8Warps * kQ8Stages; ++i) mbar_init(bars + i, 1);
+    for (int i = 0; i < kQ8Warps * C::kStages; ++i) mbar_init(bars + i, 1);
     fence_mbar_init();
   }
   __syncthreads();
@@ -247,9 +255,9 @@ __global__ void __launch_bounds__(kQ8Threads)
     l[nt][0] = l[nt][1] = 0.f;
   }
 
-  uint8_t *my_ring = ring + warp * kQ8Stages * C::kStage;
-  float *my_scales = scales + warp * kQ8Stages * 2 * kQ8Page;
-  uint64_t *my_bars = bars + warp * kQ8Stages;
+  uint8_t *my_ring = ring + warp * C::kStages * C::kStage;
+  float *my_scales = scales + warp * C::kStages * 2 * kQ8Page;
+  uint64_t *my_bars = bars + warp * C::kStages;
   const int32_t *trow = p.table + static_cast<size_t>(s) * p.max_blocks;
   const int n_mine = pg1 - pg0 > warp ? (pg1 - pg0 - warp + kQ8Warps - 1) / kQ8Warps : 0;
 
@@ -266,18 +274,15 @@ __global__ void __launch_bounds__(kQ8Threads)
       }
     }
   };
-  // page i's block is read from the table batch that holds it; a page left out (-1) loads block 0
-  auto issue = [&](int i, int blk) {
-    if (lane == 0) {
-      const int st = i % kQ8Stages;
+  // loads a page into a stage: lane 0 its K and key scales, lane 1 V; a page left out (-1) loads block 0
+  auto issue = [&](int st, int blk) {
+    if (lane < 2) {
       const int page = max(blk, 0) * p.Hk + kh;
-      uint8_t *dst = my_ring + st * C::kStage;
-      float *sd = my_scales + st * 2 * kQ8Page;
-      mbar_arrive_expect_tx(my_bars + st, C::kStage + 2 * kQ8Page * 4);
-      tma_load_3d(dst, &tk, my_bars + st, 0, 0, page);
-      tma_load_3d(dst + C::kSlab, &tv, my_bars + st, 0, 0, page);
-      bulk_load_1d(sd, p.ks + static_cast<size_t>(page) * kQ8Page, kQ8Page * 4, my_bars + st);
-      bulk_load_1d(sd + kQ8Page, p.vs + static_cast<size_t>(page) * kQ8Page, kQ8Page * 4, my_bars + st);
+      uint64_t *bar = my_bars + st;
+      if (lane == 0) mbar_arrive_expect_tx(bar, C::kStage + 2 * kQ8Page * 4);
+      tma_load_3d(my_ring + st * C::kStage + lane * C::kSlab, lane ? &tv : &tk, bar, 0, 0, page);
+      bulk_load_1d(my_scales + (st * 2 + lane) * kQ8Page, (lane ? p.vs : p.ks) + static_cast<size_t>(page) * kQ8Page,
+                   kQ8Page * 4, bar);
     }
   };
   // Blocks are fetched 32 pages at a time into `tab`, one batch ahead of the loads; `live` keeps a
@@ -285,7 +290,7 @@ __global__ void __launch_bounds__(kQ8Threads)
   fetch_table(0);
   uint32_t live = 0;
 #pragma unroll 1
-  for (int i = 0; i < kQ8Stages; ++i) {
+  for (int i = 0; i < C::kStages; ++i) {
     if (i < n_mine) {
       const int blk = __shfl_sync(0xffffffffu, tab, i);
       issue(i, blk);
@@ -293,10 +298,11 @@ __global__ void __launch_bounds__(kQ8Threads)
     }
   }
 
+  int st = 0;
+  uint32_t phase = 0;
 #pragma unroll 1
   for (int i = 0; i < n_mine; ++i) {
-    const int st = i % kQ8Stages;
-    if (!mbar_wait(my_bars + st, (i / kQ8Stages) & 1, &abort_flag)) break;
+    if (!mbar_wait(my_bars + st, phase, &abort_flag)) break;
     const uint8_t *kp = my_ring + st * C::kStage, *vp = kp + C::kSlab;
     const float *sp = my_scales + st * 2 * kQ8Page;
     const bool named = (live >> st) & 1;
@@ -363,52 +369,73 @@ __global__ void __launch_bounds__(kQ8Threads)
     }
     __syncwarp();  // every lane has read the stage: refill it
     {
-      const int next = i + kQ8Stages;
+      const int next = i + C::kStages;
       if ((next & 31) == 0) fetch_table(next);
       const int blk = __shfl_sync(0xffffffffu, tab, next & 31);
       live &= ~(1u << st);
       if (next < n_mine) {
-        issue(next, blk);
+        issue(st, blk);
         if (blk >= 0) live |= 1u << st;
       }
+      if (++st == C::kStages) st = 0, phase ^= 1;
     }
 
     // scores: sa[nt][2 r + e] is token g + 8 r against query row 8 nt + 2 c + e
     // the page reaches the queries' own tokens, where the masks apply
     const bool edge = (p.causal || p.tree) && tok0 + kQ8Page > L - p.T;
-    float pv[NT][4];
+    // most pages lie whole inside what every row sees: no masks
+    const bool plain = named && tok0 + kQ8Page <= L && !edge;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          bool see = in[r];
-          if (edge) {
-            const int v = tok0 + g + 8 * r - (L - p.T);  // the token's place among the queries
-            if (v >= 0 && see) {
-              if (p.tree) see = (p.tree[static_cast<size_t>(s) * p.T + tq[nt][e]] >> (v & 63)) & 1;
-              else if (p.causal) see = v <= tq[nt][e];
-            }
-          }
-          sa[nt][2 * r + e] = see ? sa[nt][2 * r + e] * (kss[r] * sc[nt][e]) : -INFINITY;
-        }
-    float pw[NT][4];
-    auto weigh = [&]() {  // p and p vs against the present references; true when one passes its limit
-      bool over = false;
+        for (int e = 0; e < 2; ++e) sa[nt][2 * r + e] *= kss[r] * sc[nt][e];
+    if (!plain) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float x = sa[nt][2 * r + e];
-            // a token that this row does not see: no part in the sums, whatever its scales are
-            const float w = x == -INFINITY ? 0.f : ex2(x - m[nt][e]);
-            pw[nt][2 * r + e] = w;
-            pv[nt][2 * r + e] = x == -INFINITY ? 0.f : w * vss[r];
-            over = over || w > kQ8MostP || pv[nt][2 * r + e] > kQ8MostPv;
+            bool see = in[r];
+            if (edge) {
+              const int v = tok0 + g + 8 * r - (L - p.T);  // the token's place among the queries
+              if (v >= 0 && see) {
+                if (p.tree) see = (p.tree[static_cast<size_t>(s) * p.T + tq[nt][e]] >> (v & 63)) & 1;
+                else if (p.causal) see = v <= tq[nt][e];
+              }
+            }
+            if (!see) sa[nt][2 * r + e] = -INFINITY;
           }
+    }
+    float pv[NT][4], pw[NT][4], ln[NT][2];
+    uint32_t pb[NT][2];
+    auto weigh = [&]() {  // p and p vs against the present references; true when one passes its limit
+      bool over = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          pw[nt][q] = ex2(sa[nt][q] - m[nt][q % 2]);
+          pv[nt][q] = pw[nt][q] * vss[q / 2];
+        }
+        if (!plain) {
+          // a token that a row does not see has no part in its sums, whatever its scales are
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (sa[nt][q] == -INFINITY) pw[nt][q] = pv[nt][q] = 0.f;
+        }
+        pb[nt][0] = pack_fp16x2(pv[nt][0], pv[nt][1]);
+        pb[nt][1] = pack_fp16x2(pv[nt][2], pv[nt][3]);
+        const uint32_t big = max_fp16x2(pb[nt][0], pb[nt][1]);
+        over = over || (big & 0xffffu) > kQ8MostPvBits || (big >> 16) > kQ8MostPvBits;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          ln[nt][e] = l[nt][e] + (pw[nt][e] + pw[nt][2 + e]);
+          over = over || ln[nt][e] > kQ8MostP;
+        }
+      }
       return over;
     };
     if (__any_sync(0xffffffffu, weigh())) {
@@ -417,8 +444,7 @@ __global__ void __launch_bounds__(kQ8Threads)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const bool mine = pw[nt][e] > kQ8MostP || pw[nt][2 + e] > kQ8MostP ||
-                            pv[nt][e] > kQ8MostPv || pv[nt][2 + e] > kQ8MostPv;
+          const bool mine = ln[nt][e] > kQ8MostP || pv[nt][e] > kQ8MostPv || pv[nt][2 + e] > kQ8MostPv;
           float x = -INFINITY;
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
@@ -432,8 +458,9 @@ __global__ void __launch_bounds__(kQ8Threads)
             go = fmaxf(go, __shfl_xor_sync(0xffffffffu, go, off));
           }
           if (go == 0.f) continue;
-          const float a = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - x);
-          m[nt][e] = x;
+          const float mn = fmaxf(m[nt][e], x);
+          const float a = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - mn);
+          m[nt][e] = mn;
           l[nt][e] *= a;
 #pragma unroll
           for (int j = 0; j < kMT; ++j) {
@@ -443,13 +470,12 @@ __global__ void __launch_bounds__(kQ8Threads)
         }
       weigh();
     }
-    uint32_t pb[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      l[nt][0] += pw[nt][0] + pw[nt][2];
-      l[nt][1] += pw[nt][1] + pw[nt][3];
-      pb[nt][0] = movmatrix_trans(pack_fp16x2(pv[nt][0], pv[nt][1]));
-      pb[nt][1] = movmatrix_trans(pack_fp16x2(pv[nt][2], pv[nt][3]));
+      l[nt][0] = ln[nt][0];
+      l[nt][1] = ln[nt][1];
+      pb[nt][0] = movmatrix_trans(pb[nt][0]);
+      pb[nt][1] = movmatrix_trans(pb[nt][1]);
     }
 #pragma unroll
     for (int w = 0; w < kVW; ++w) {
