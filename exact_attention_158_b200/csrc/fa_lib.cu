@@ -1087,8 +1087,13 @@ struct Q8Plan {
   size_t rows;      // S * Hq * Lq
 };
 
-constexpr int kQ8TargetCtas = 148 * 3 * 4;  // a few waves of the three CTAs that fit an SM
-constexpr int kQ8MinPages = 16;             // pages of a chunk: four to a warp
+// Few rows: chunks enough for two waves of the four CTAs that fit an SM, none longer than 128 pages (so
+// that ragged lengths balance: 64 sequences of 512 to 8192 tokens took 397 us in two chunks each and
+// 383 in four) and none shorter than 32 (eight to a warp: below that, joining costs more than
+// it saves).
+constexpr int kQ8TargetCtas = 148 * 4 * 2;
+constexpr int kQ8MinPages = 32, kQ8MaxPages = 128;
+constexpr int kQ8WideSplit = 4;             // more chunks than this: a CTA joins each row
 constexpr int kQ8StreamRows = 16;           // up to here fa_q8_stream_kernel, beyond fa_q8_tile_kernel
 constexpr int kQ8TileTargetCtas = 148;      // one CTA per SM
 constexpr int kQ8TileMinPages = 16;         // two token tiles to a chunk
@@ -1107,7 +1112,9 @@ bool q8_plan(int S, int Hq, int Hk, int Lq, int d, int max_blocks, Q8Plan *out) 
   p.row_tiles = (p.R + tile_rows * p.nt - 1) / (tile_rows * p.nt);
   const long long units = static_cast<long long>(S) * Hk * p.row_tiles;
   const int target = p.tile ? kQ8TileTargetCtas : kQ8TargetCtas, least = p.tile ? kQ8TileMinPages : kQ8MinPages;
-  const long long n = std::min<long long>((target + units - 1) / units, (max_blocks + least - 1) / least);
+  long long n = (target + units - 1) / units;
+  if (!p.tile) n = std::max<long long>(n, (max_blocks + kQ8MaxPages - 1) / kQ8MaxPages);
+  n = std::min<long long>({n, (max_blocks + least - 1) / least, fa::kQ8MaxSplit});
   p.split_pages = static_cast<int>((max_blocks + n - 1) / n);
   if (p.tile) p.split_pages = (p.split_pages + 7) / 8 * 8;  // whole tiles of 128 tokens
   p.n_split = (max_blocks + p.split_pages - 1) / p.split_pages;
@@ -1127,8 +1134,11 @@ fa_status q8_combine(const fa::Q8Params &p, cudaStream_t s) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return launch_failed(e);
   if (p.n_split > 1) {
-    const size_t threads = static_cast<size_t>(p.S) * p.Hk * p.R * (HD / 4);
-    fa::fa_q8_combine_kernel<HD><<<static_cast<unsigned>((threads + 127) / 128), 128, 0, s>>>(p);
+    const size_t rows = static_cast<size_t>(p.S) * p.Hk * p.R;
+    if (p.n_split > kQ8WideSplit)
+      fa::fa_q8_combine_kernel<HD, true><<<static_cast<unsigned>(rows), 256, 0, s>>>(p);
+    else
+      fa::fa_q8_combine_kernel<HD, false><<<static_cast<unsigned>((rows * (HD / 4) + 255) / 256), 256, 0, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return launch_failed(e);
   }
   return FA_OK;

@@ -549,33 +549,82 @@ __global__ void __launch_bounds__(kQ8Threads, (HD == 128 ? 5 : 6) - NT)
   }
 }
 
-// Joins the chunks of every row: M = max m_c, l = sum 2^(m_c - M) l_c, O = sum 2^(m_c - M) O_c / l.
-// HD / 4 threads per row; a chunk without a visible token has l = 0 and takes no part.
-template <int HD>
-__global__ void __launch_bounds__(128) fa_q8_combine_kernel(const Q8Params p) {
+// Joins the chunks of every row: M = max m_c, l = sum 2^(m_c - M) l_c, O = sum 2^(m_c - M) O_c / l; a
+// chunk without a visible token has l = 0 and takes no part.
+//
+// kWide: a CTA per row, for many chunks of few rows (one long context), where a thread that walked the
+// chunks one after the other would wait for each (111 chunks: 60 us of a 175 us call).  The
+// chunks' weights are made by all threads at once, then each warp sums every eighth chunk.
+// Otherwise HD / 4 threads per row, each over all chunks.
+constexpr int kQ8MaxSplit = 512;
+
+template <int HD, bool kWide>
+__global__ void __launch_bounds__(256) fa_q8_combine_kernel(const Q8Params p) {
   constexpr int kPer = HD / 4;
-  const size_t gt = static_cast<size_t>(blockIdx.x) * 128 + threadIdx.x;
-  const size_t row = gt / kPer;
-  if (row >= static_cast<size_t>(p.S) * p.Hk * p.R) return;
-  const int e0 = 4 * static_cast<int>(gt % kPer);
+  const size_t rows = static_cast<size_t>(p.S) * p.Hk * p.R;
+  const size_t row = kWide ? blockIdx.x : (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) / kPer;
+  if (row >= rows) return;
   const int s = static_cast<int>(row / (static_cast<size_t>(p.Hk) * p.R));
   const int nblk = (q8_len(p, s) + kQ8Page - 1) / kQ8Page;
   const int n = (nblk + p.split_pages - 1) / p.split_pages;
   const float2 *ml = p.ws_ml + row * p.n_split;
+  const int e0 = 4 * static_cast<int>(threadIdx.x % kPer);
   const float *po = p.ws_o + row * p.n_split * HD + e0;
-  float M = -INFINITY;
-  for (int i = 0; i < n; ++i) M = fmaxf(M, ml[i].x);
-  float sum = 0.f;
+  float M = -INFINITY, sum = 0.f;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = 0; i < n; ++i) {
-    const float2 x = ml[i];
-    if (x.y == 0.f) continue;
-    const float f = ex2(x.x - M);
-    const float4 v = *reinterpret_cast<const float4 *>(po + static_cast<size_t>(i) * HD);
-    sum = fmaf(f, x.y, sum);
+  auto add = [&](float f, const float4 &v) {
     a.x = fmaf(f, v.x, a.x), a.y = fmaf(f, v.y, a.y), a.z = fmaf(f, v.z, a.z), a.w = fmaf(f, v.w, a.w);
+  };
+  if constexpr (!kWide) {
+    for (int i = 0; i < n; ++i) M = fmaxf(M, ml[i].x);
+    for (int i = 0; i < n; ++i) {
+      const float2 x = ml[i];
+      if (x.y == 0.f) continue;
+      const float f = ex2(x.x - M);
+      sum = fmaf(f, x.y, sum);
+      add(f, *reinterpret_cast<const float4 *>(po + static_cast<size_t>(i) * HD));
+    }
+    q8_write4<HD>(p, row, e0, a, M, sum);
+  } else {
+    constexpr int kGroups = 256 / kPer;  // groups of threads, each a whole row of features
+    __shared__ float weight[kQ8MaxSplit], red[2][8];
+    __shared__ float4 part[256];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    for (int i = threadIdx.x; i < n; i += 256) M = fmaxf(M, ml[i].x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    if (lane == 0) red[0][warp] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) M = fmaxf(M, red[0][w]);
+    for (int i = threadIdx.x; i < n; i += 256) {
+      const float2 x = ml[i];
+      const float f = x.y == 0.f ? 0.f : ex2(x.x - M);
+      weight[i] = f;
+      if (x.y != 0.f) sum = fmaf(f, x.y, sum);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == 0) red[1][warp] = sum;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) sum += red[1][w];
+    // (a chunk with l = 0 wrote zeros: its weight of 0 does no harm)
+#pragma unroll 4
+    for (int i = threadIdx.x / kPer; i < n; i += kGroups)
+      add(weight[i], *reinterpret_cast<const float4 *>(po + static_cast<size_t>(i) * HD));
+    part[threadIdx.x] = a;
+    __syncthreads();
+    if (threadIdx.x < kPer) {
+#pragma unroll
+      for (int g = 1; g < kGroups; ++g) {
+        const float4 x = part[threadIdx.x + g * kPer];
+        a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+      }
+      q8_write4<HD>(p, row, e0, a, M, sum);
+    }
   }
-  q8_write4<HD>(p, row, e0, a, M, sum);
 }
 
 }  // namespace fa
