@@ -38,7 +38,7 @@ struct AppendParams {
   RopeTable table;
   int T, Hq, Hk;
   long long num_slots;
-  int log_tok;
+  int groups, heads_per_group;  // of the q, k and v heads, as in RopeParams
 };
 
 // x / s rounded to nearest, from r = 1 / s rounded to nearest: one residual step after the product
@@ -68,95 +68,98 @@ __device__ __forceinline__ uint32_t cache_code4(const float *f, float s, float r
   }
 }
 
-// grid: ceil(T / kTok).  Rows of a CTA: q heads, k heads, v heads, its tokens side by side; HD / 16
-// threads a row, 16 features each, the row maximum by shuffles among them.
+// Threads as in fa_rope_kernel: one per (head group, token, chunk), the heads of q, k and v counted in
+// that order; HD / 16 threads a row, 16 features each, the row maximum by shuffles among them.
 template <int HD, int kType>
 __global__ void __launch_bounds__(kRopeThreads) fa_cache_append_kernel(const AppendParams p) {
-  __shared__ float2 cs[kRopeMaxTok * kRopeMaxPairs];
-  __shared__ long long slot_sm[kRopeMaxTok];
-  constexpr int kChunks = HD / 16;
-  const int tok_n = 1 << p.log_tok;
-  const int m0 = blockIdx.x << p.log_tok;
-  const int live = min(tok_n, p.T - m0);
-  const int pairs = p.table.rot / 2;
-  for (int t = threadIdx.x; t < live; t += kRopeThreads) {
-    long long slot = p.slots[m0 + t];
-    if (slot >= p.num_slots) {  // caller broke the contract: report, write nothing for the token
-      atomicExch(&g_device_status, 1 /* FA_ERR_INVALID_ARG */);
-      slot = -1;
-    }
-    slot_sm[t] = slot;
+  constexpr int kChunks = HD / 16, kUnroll = 4;
+  using bf = __nv_bfloat16;
+  const unsigned long long gid = static_cast<unsigned long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
+  const int chunk = static_cast<int>(gid % kChunks);
+  const unsigned long long rest = gid / kChunks;
+  const unsigned group = static_cast<unsigned>(rest / static_cast<unsigned>(p.T));
+  // threads past the end stay for the shuffles, without rows
+  const bool live = group < static_cast<unsigned>(p.groups);
+  const long long m = live ? rest - static_cast<unsigned long long>(group) * p.T : 0;
+  const int first = live ? group * p.heads_per_group : 0;
+  const int last = live ? min(first + p.heads_per_group, p.Hq + 2 * p.Hk) : 0;
+  const int2 rcol = rope_cols(p.table, chunk), vcol = make_int2(16 * chunk, 16 * chunk + 8);
+  auto load = [&](Raw16<bf> &r, int h) {
+    if (h >= last) return;
+    const uint16_t *row = h < p.Hq ? p.q + m * p.q_s[0] + h * p.q_s[1]
+                          : h < p.Hq + p.Hk ? p.k + m * p.k_s[0] + (h - p.Hq) * p.k_s[1]
+                                            : p.v + m * p.v_s[0] + (h - p.Hq - p.Hk) * p.v_s[1];
+    raw_load(r, reinterpret_cast<const bf *>(row), h < p.Hq + p.Hk ? rcol : vcol);
+  };
+  Raw16<bf> raw[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) load(raw[u], first + u);
+  long long slot = live ? p.slots[m] : -1;
+  RopeTurn turn;
+  turn.any = false;
+  // (a thread whose heads are all values needs no angles)
+  if (first < p.Hq + p.Hk && live) rope_turn(p.table, p.positions + m, chunk, turn);
+  if (slot >= p.num_slots) {  // caller broke the contract: report, write nothing for the token
+    atomicExch(&g_device_status, 1 /* FA_ERR_INVALID_ARG */);
+    slot = -1;
   }
-  for (int i = threadIdx.x; i < live * pairs; i += kRopeThreads)
-    cs[i] = rope_cos_sin(p.table, p.positions[m0 + i / pairs], i % pairs);
-  __syncthreads();
-  const int rows = (p.Hq + 2 * p.Hk) << p.log_tok;
-  const int chunk = threadIdx.x % kChunks;
-  const int2 rcol = rope_cols(p.table, chunk);
-  constexpr int kStep = kRopeThreads / kChunks;
-  // whole warps stay in the loop together: the shuffles need every lane
-  for (int r0 = 0; r0 < rows; r0 += kStep) {
-    const int r = r0 + threadIdx.x / kChunks;
-    const int t = r & (tok_n - 1);
-    int h = r >> p.log_tok;
-    const bool is_q = h < p.Hq;
-    const bool is_v = h >= p.Hq + p.Hk;
-    if (!is_q) h -= is_v ? p.Hq + p.Hk : p.Hq;
-    const long long slot = t < live ? slot_sm[t] : -1;
-    const bool act = r < rows && t < live && (is_q || slot >= 0);
-    const int2 col = is_v ? make_int2(16 * chunk, 16 * chunk + 8) : rcol;
-    float f[16];
+  for (int i = 0; i < p.heads_per_group; i += kUnroll) {  // the same rounds for every thread
 #pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] = 0.f;
-    if (act) {
-      const long long m = m0 + t;
-      const uint16_t *src = is_q ? p.q + m * p.q_s[0] + h * p.q_s[1]
-                            : is_v ? p.v + m * p.v_s[0] + h * p.v_s[1]
-                                   : p.k + m * p.k_s[0] + h * p.k_s[1];
-      load8(reinterpret_cast<const __nv_bfloat16 *>(src + col.x), f);
-      load8(reinterpret_cast<const __nv_bfloat16 *>(src + col.y), f + 8);
-      if (!is_v) rope_apply(p.table, cs + t * pairs, chunk, f);
-    }
-    float top = 0.f, bad = 0.f;
-    if constexpr (kType != kCacheBf16) {
+    for (int u = 0; u < kUnroll; ++u) {
+      if (i + u >= p.heads_per_group) break;
+      int h = first + i + u;
+      const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hk;
+      const bool act = h < last && (is_q || slot >= 0);
+      const int2 col = is_v ? vcol : rcol;
+      float f[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        top = fmaxf(top, fabsf(f[i]));
-        bad += f[i] * 0.f;  // NaN when any feature is infinite or NaN
+      for (int e = 0; e < 16; ++e) f[e] = 0.f;
+      if (act) {
+        raw_floats(raw[u], f);
+        if (!is_v) rope_apply(p.table, turn, f);
       }
+      load(raw[u], h + kUnroll);
+      if (!is_q) h -= is_v ? p.Hq + p.Hk : p.Hq;
+      float top = 0.f, bad = 0.f;
+      if constexpr (kType != kCacheBf16) {
 #pragma unroll
-      for (int off = kChunks / 2; off > 0; off >>= 1) {
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        bad += __shfl_xor_sync(0xffffffffu, bad, off);
-      }
-    }
-    if (!act) continue;
-    if (is_q) {
-      uint16_t *dst = p.q_out + static_cast<long long>(m0 + t) * p.qo_s[0] + h * p.qo_s[1];
-      store8(reinterpret_cast<__nv_bfloat16 *>(dst + col.x), f);
-      store8(reinterpret_cast<__nv_bfloat16 *>(dst + col.y), f + 8);
-      continue;
-    }
-    const long long row = (slot / kCachePage * p.Hk + h) * kCachePage + slot % kCachePage;
-    void *pool = is_v ? p.v_pool : p.k_pool;
-    if constexpr (kType == kCacheBf16) {
-      uint16_t *dst = static_cast<uint16_t *>(pool) + row * HD;
-      store8(reinterpret_cast<__nv_bfloat16 *>(dst + col.x), f);
-      store8(reinterpret_cast<__nv_bfloat16 *>(dst + col.y), f + 8);
-    } else {
-      float scale = top >= kCacheTiny ? __fdiv_rn(top, cache_qmax<kType>()) : 0.f;
-      float rcp = scale > 0.f ? __frcp_rn(scale) : 0.f;
-      if (!(bad == 0.f)) scale = __int_as_float(0x7fc00000), rcp = 0.f;
-      const bool live_row = rcp > 0.f;
-      uint32_t w[4] = {0u, 0u, 0u, 0u};
-      if (live_row) {
+        for (int e = 0; e < 16; ++e) {
+          top = fmaxf(top, fabsf(f[e]));
+          bad = fmaf(f[e], 0.f, bad);  // NaN when any feature is infinite or NaN
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = cache_code4<kType>(f + 4 * i, scale, rcp);
+        for (int off = kChunks / 2; off > 0; off >>= 1) {
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+          bad += __shfl_xor_sync(0xffffffffu, bad, off);
+        }
       }
-      uint8_t *dst = static_cast<uint8_t *>(pool) + row * HD;
-      *reinterpret_cast<uint2 *>(dst + col.x) = make_uint2(w[0], w[1]);
-      *reinterpret_cast<uint2 *>(dst + col.y) = make_uint2(w[2], w[3]);
-      if (chunk == 0) (is_v ? p.v_scale : p.k_scale)[row] = scale;
+      if (!act) continue;
+      if (is_q) {
+        uint16_t *dst = p.q_out + m * p.qo_s[0] + h * p.qo_s[1];
+        store8(reinterpret_cast<bf *>(dst + col.x), f);
+        store8(reinterpret_cast<bf *>(dst + col.y), f + 8);
+        continue;
+      }
+      const long long row = (slot / kCachePage * p.Hk + h) * kCachePage + slot % kCachePage;
+      void *pool = is_v ? p.v_pool : p.k_pool;
+      if constexpr (kType == kCacheBf16) {
+        uint16_t *dst = static_cast<uint16_t *>(pool) + row * HD;
+        store8(reinterpret_cast<bf *>(dst + col.x), f);
+        store8(reinterpret_cast<bf *>(dst + col.y), f + 8);
+      } else {
+        float scale = top >= kCacheTiny ? __fdiv_rn(top, cache_qmax<kType>()) : 0.f;
+        float rcp = scale > 0.f ? __frcp_rn(scale) : 0.f;
+        if (!(bad == 0.f)) scale = __int_as_float(0x7fc00000), rcp = 0.f;
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        if (rcp > 0.f) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = cache_code4<kType>(f + 4 * e, scale, rcp);
+        }
+        uint8_t *dst = static_cast<uint8_t *>(pool) + row * HD;
+        *reinterpret_cast<uint2 *>(dst + col.x) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2 *>(dst + col.y) = make_uint2(w[2], w[3]);
+        if (chunk == 0) (is_v ? p.v_scale : p.k_scale)[row] = scale;
+      }
     }
   }
 }

@@ -1011,13 +1011,16 @@ fa_status check_rope(const int32_t *positions, const double *freqs, int rot, fa_
   return FA_OK;
 }
 
-// Tokens per CTA (as a power of two): about 1024 row chunks to a CTA, but no fewer than about four
-// CTAs per SM's worth of tokens, so that a decode step's few tokens spread over the GPU.
-int rope_log_tok(long long tokens, int rows_per_token, int d, int num_sms) {
-  int lg = 0;
-  const long long per_token = static_cast<long long>(rows_per_token) * (d / 16);
-  while (lg < 5 && (per_token << (lg + 1)) <= 1024 && (tokens >> (lg + 1)) >= 4LL * num_sms) ++lg;
-  return lg;
+// How the heads of a token are split over threads: not at all where the tokens alone give every SM
+// kRopeWarps warps, else into as many groups as that takes, down to one head each (a decode step).
+constexpr int kRopeWarps = 24;
+
+unsigned rope_split(long long tokens, int heads, int d, int num_sms, int *groups, int *per_group) {
+  const long long warps = std::max(1LL, tokens * (d / 16) / 32);
+  long long g = std::min<long long>(heads, (static_cast<long long>(kRopeWarps) * num_sms + warps - 1) / warps);
+  *per_group = static_cast<int>((heads + g - 1) / g);
+  *groups = (heads + *per_group - 1) / *per_group;
+  return static_cast<unsigned>((tokens * (d / 16) * *groups + fa::kRopeThreads - 1) / fa::kRopeThreads);
 }
 
 template <int HD>
@@ -1318,13 +1321,14 @@ fa_status fa_rope(const void *q, const long long *q_strides, void *q_out,
   p.positions = positions;
   p.pos_stride = pos_stride;
   p.N = N;
-  p.tokens = static_cast<long long>(B) * N;
-  if (p.tokens > INT_MAX || static_cast<long long>(Hq) + Hk > INT_MAX >> 5) return FA_ERR_INVALID_ARG;
+  const long long tokens = static_cast<long long>(B) * N;
+  // threads are counted in blocks of an unsigned grid
+  if (tokens > INT_MAX || static_cast<long long>(Hq) + Hk > INT_MAX) return FA_ERR_INVALID_ARG;
+  p.tokens = static_cast<unsigned>(tokens);
   DeviceInfo *dev = nullptr;
   int dev_id = 0;
   if ((st = current_device(&dev, &dev_id)) != FA_OK) return st;
-  p.log_tok = rope_log_tok(p.tokens, Hq + Hk, d, dev->num_sms);
-  const unsigned grid = static_cast<unsigned>((p.tokens + (1 << p.log_tok) - 1) >> p.log_tok);
+  const unsigned grid = rope_split(tokens, Hq + Hk, d, dev->num_sms, &p.groups, &p.heads_per_group);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int inf = in_dtype == FA_OUT_F32, outf = out_dtype == FA_OUT_F32;
   cudaError_t e = d == 128 ? launch_rope<128>(p, inf, outf, grid, s) : launch_rope<64>(p, inf, outf, grid, s);
@@ -1347,7 +1351,7 @@ fa_status fa_cache_append(const void *k, const long long *k_strides, const void 
   if (st != FA_OK) return st;
   if (!k || !v || !slots || !k_strides || !v_strides) return FA_ERR_INVALID_ARG;
   if (Hq > 0 && (!q || !q_out || !q_strides || !q_out_strides)) return FA_ERR_INVALID_ARG;
-  if (static_cast<long long>(Hq) + 2LL * Hk > INT_MAX >> 5) return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(Hq) + 2LL * Hk > INT_MAX) return FA_ERR_INVALID_ARG;
   if (!aligned16(k) || !aligned16(v) || !aligned(slots, 8)) return FA_ERR_ALIGNMENT;
   if (Hq > 0 && (!aligned16(q) || !aligned16(q_out))) return FA_ERR_ALIGNMENT;
   const long long *strides[4] = {k_strides, v_strides, q_strides, q_out_strides};
@@ -1391,8 +1395,7 @@ fa_status fa_cache_append(const void *k, const long long *k_strides, const void 
   DeviceInfo *dev = nullptr;
   int dev_id = 0;
   if ((st = current_device(&dev, &dev_id)) != FA_OK) return st;
-  p.log_tok = rope_log_tok(T, Hq + 2 * Hk, d, dev->num_sms);
-  const unsigned grid = static_cast<unsigned>((static_cast<long long>(T) + (1 << p.log_tok) - 1) >> p.log_tok);
+  const unsigned grid = rope_split(T, Hq + 2 * Hk, d, dev->num_sms, &p.groups, &p.heads_per_group);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = d == 128 ? launch_append<128>(p, type, grid, s) : launch_append<64>(p, type, grid, s);
   return e == cudaSuccess ? FA_OK : launch_failed(e);

@@ -7,11 +7,14 @@
 //
 // Angles.  At position 10^6 an fp32 product p * f_j is off by up to 0.06 rad, so p * f_j / (2 pi) is
 // formed in fp64 and only its fraction, in [-1/2, 1/2], goes to fp32, the rest (2^-26 turns) as a
-// first-order correction of the sine and cosine.  One sine and cosine serve every head of the token: a CTA takes kTok tokens, makes their tables in
-// shared memory once, and applies them to all heads of q and k.
+// first-order correction of the sine and cosine.
 //
-// Bound: HBM, each element read and written once.  16-byte accesses; the strided side (a
-// projection's [B, N, heads, d]) and the head-major side are both whole rows of 128 to 512 bytes.
+// Bound: HBM, each element read and written once.  A thread keeps one token and one chunk of eight
+// pairs for all the heads it takes, so the eight angles it needs are made once, in registers, and
+// nothing is shared: no table, no barrier, every warp runs by itself.  (With a table in shared memory,
+// made by the CTA behind a barrier, B8 H16+16 N2048 d128 took 57 to 78 us, QQQQ this way.)
+// 16-byte accesses, whole rows of 128 to 512 bytes by the HD / 16 threads of a row; the four or eight
+// tokens of a warp are neighbours, so the head-major side moves 1 to 2 KB at a time.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -19,9 +22,7 @@
 
 namespace fa {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeMaxTok = 32;
-constexpr int kRopeMaxPairs = 64;  // rot / 2 at d = 128
+constexpr int kRopeThreads = 128;
 
 // What turns a row: shared by fa_rope and by the cache writer.
 struct RopeTable {
@@ -54,26 +55,68 @@ __device__ __forceinline__ int2 rope_cols(const RopeTable &t, int chunk) {
   return make_int2(16 * chunk, 16 * chunk + 8);
 }
 
-// Turns a thread's 16 features by the token's table cs[rot / 2].
-__device__ __forceinline__ void rope_apply(const RopeTable &t, const float2 *cs, int chunk,
-                                           float (&f)[16]) {
-  if (16 * chunk >= t.rot) return;
+// The cosines and sines of a chunk's eight pairs at a token's position.
+struct RopeTurn {
+  float2 w[8];
+  bool any;  // a chunk of the part passed through turns nothing
+};
+__device__ __forceinline__ void rope_turn(const RopeTable &t, const int32_t *position, int chunk, RopeTurn &r) {
+  r.any = 16 * chunk < t.rot;
+  if (r.any) {
+    const int p = *position;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r.w[j] = rope_cos_sin(t, p, 8 * chunk + j);
+  }
+}
+
+__device__ __forceinline__ void rope_apply(const RopeTable &t, const RopeTurn &r, float (&f)[16]) {
+  if (!r.any) return;
   if (t.interleaved) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float2 w = cs[8 * chunk + j];
       const float a = f[2 * j], b = f[2 * j + 1];
-      f[2 * j] = fmaf(a, w.x, -b * w.y);
-      f[2 * j + 1] = fmaf(b, w.x, a * w.y);
+      f[2 * j] = fmaf(a, r.w[j].x, -b * r.w[j].y);
+      f[2 * j + 1] = fmaf(b, r.w[j].x, a * r.w[j].y);
     }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float2 w = cs[8 * chunk + j];
       const float a = f[j], b = f[8 + j];
-      f[j] = fmaf(a, w.x, -b * w.y);
-      f[8 + j] = fmaf(b, w.x, a * w.y);
+      f[j] = fmaf(a, r.w[j].x, -b * r.w[j].y);
+      f[8 + j] = fmaf(b, r.w[j].x, a * r.w[j].y);
     }
+  }
+}
+
+// Sixteen features as they lie in memory: loaded early, converted when their turn comes.
+template <class T> struct Raw16;
+template <> struct Raw16<__nv_bfloat16> { uint4 v[2]; };
+template <> struct Raw16<float> { float4 v[4]; };
+__device__ __forceinline__ void raw_load(Raw16<__nv_bfloat16> &r, const __nv_bfloat16 *row, int2 col) {
+  r.v[0] = *reinterpret_cast<const uint4 *>(row + col.x);
+  r.v[1] = *reinterpret_cast<const uint4 *>(row + col.y);
+}
+__device__ __forceinline__ void raw_load(Raw16<float> &r, const float *row, int2 col) {
+  r.v[0] = reinterpret_cast<const float4 *>(row + col.x)[0];
+  r.v[1] = reinterpret_cast<const float4 *>(row + col.x)[1];
+  r.v[2] = reinterpret_cast<const float4 *>(row + col.y)[0];
+  r.v[3] = reinterpret_cast<const float4 *>(row + col.y)[1];
+}
+__device__ __forceinline__ void raw_floats(const Raw16<__nv_bfloat16> &r, float (&f)[16]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w[4] = {r.v[i].x, r.v[i].y, r.v[i].z, r.v[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+      f[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  }
+}
+__device__ __forceinline__ void raw_floats(const Raw16<float> &r, float (&f)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[4 * i] = r.v[i].x, f[4 * i + 1] = r.v[i].y, f[4 * i + 2] = r.v[i].z, f[4 * i + 3] = r.v[i].w;
   }
 }
 
@@ -113,53 +156,52 @@ struct RopeParams {
   long long pos_stride;  // between batch rows (0: one row of positions for all)
   RopeTable table;
   int N;
-  long long tokens;  // B * N
-  int log_tok;       // tokens per CTA (a power of two)
+  unsigned tokens;  // B * N
+  int groups, heads_per_group;  // the heads are split over `groups` threads where tokens are few
 };
 
-// grid: ceil(tokens / kTok).  A CTA's rows are numbered head by head, its tokens side by side, so
-// neighbouring thread groups move neighbouring rows of the head-major side; HD / 16 threads a row.
+// One thread per (head group, token, chunk of features), the chunk fastest, then the token.
 template <int HD, class In, class Out>
 __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams p) {
-  __shared__ float2 cs[kRopeMaxTok * kRopeMaxPairs];
-  __shared__ long long base[2][2][kRopeMaxTok];  // tensor, side: the token's row of head 0
   constexpr int kChunks = HD / 16;
-  const int tok_n = 1 << p.log_tok;
-  const long long m0 = static_cast<long long>(blockIdx.x) << p.log_tok;
-  const int live = static_cast<int>(min(static_cast<long long>(tok_n), p.tokens - m0));
-  const int pairs = p.table.rot / 2;
-  for (int t = threadIdx.x; t < live; t += kRopeThreads) {
-    const long long b = (m0 + t) / p.N, n = (m0 + t) % p.N;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      base[i][0][t] = b * p.x[i].in_s[0] + n * p.x[i].in_s[2];
-      base[i][1][t] = b * p.x[i].out_s[0] + n * p.x[i].out_s[2];
-    }
-  }
-  for (int i = threadIdx.x; i < live * pairs; i += kRopeThreads) {
-    const int t = i / pairs, j = i % pairs;
-    const long long b = (m0 + t) / p.N, n = (m0 + t) % p.N;
-    cs[t * pairs + j] = rope_cos_sin(p.table, p.positions[b * p.pos_stride + n], j);
-  }
-  __syncthreads();
-  const int rows = (p.x[0].H + p.x[1].H) << p.log_tok;
-  const int chunk = threadIdx.x % kChunks;
+  constexpr int kUnroll = sizeof(In) == 4 ? 2 : 4;  // rows on their way at once
+  const unsigned long long gid = static_cast<unsigned long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
+  const int chunk = static_cast<int>(gid % kChunks);
+  const unsigned long long rest = gid / kChunks;
+  const unsigned group = static_cast<unsigned>(rest / p.tokens);
+  if (group >= static_cast<unsigned>(p.groups)) return;
+  const unsigned m = static_cast<unsigned>(rest - static_cast<unsigned long long>(group) * p.tokens);
+  const long long b = m / static_cast<unsigned>(p.N), n = m % static_cast<unsigned>(p.N);
+  const int first = group * p.heads_per_group;
+  const int last = min(first + p.heads_per_group, p.x[0].H + p.x[1].H);
   const int2 col = rope_cols(p.table, chunk);
-  for (int r = threadIdx.x / kChunks; r < rows; r += kRopeThreads / kChunks) {
-    const int t = r & (tok_n - 1);
-    int h = r >> p.log_tok;
-    if (t >= live) continue;
-    const int which = h >= p.x[0].H;
-    if (which) h -= p.x[0].H;
-    const RopeTensor &x = p.x[which];
-    const In *src = static_cast<const In *>(x.in) + base[which][0][t] + h * x.in_s[1];
-    Out *dst = static_cast<Out *>(x.out) + base[which][1][t] + h * x.out_s[1];
-    float f[16];
-    load8(src + col.x, f);
-    load8(src + col.y, f + 8);
-    rope_apply(p.table, cs + t * pairs, chunk, f);
-    store8(dst + col.x, f);
-    store8(dst + col.y, f + 8);
+  auto in_row = [&](int h) {
+    const RopeTensor &x = p.x[h >= p.x[0].H];
+    if (h >= p.x[0].H) h -= p.x[0].H;
+    return static_cast<const In *>(x.in) + b * x.in_s[0] + h * x.in_s[1] + n * x.in_s[2];
+  };
+  Raw16<In> raw[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u)
+    if (first + u < last) raw_load(raw[u], in_row(first + u), col);
+  RopeTurn turn;
+  rope_turn(p.table, p.positions + b * p.pos_stride + n, chunk, turn);
+  for (int h0 = first; h0 < last; h0 += kUnroll) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      int h = h0 + u;
+      if (h >= last) break;
+      float f[16];
+      raw_floats(raw[u], f);
+      // in place, a row is read before it is written: it has one thread per chunk of pairs
+      if (h + kUnroll < last) raw_load(raw[u], in_row(h + kUnroll), col);
+      rope_apply(p.table, turn, f);
+      const RopeTensor &x = p.x[h >= p.x[0].H];
+      if (h >= p.x[0].H) h -= p.x[0].H;
+      Out *dst = static_cast<Out *>(x.out) + b * x.out_s[0] + h * x.out_s[1] + n * x.out_s[2];
+      store8(dst + col.x, f);
+      store8(dst + col.y, f + 8);
+    }
   }
 }
 
