@@ -169,60 +169,81 @@ struct ReadParams {
   const float *k_scale, *v_scale;
   const int64_t *slots;
   uint16_t *k, *v;  // [T, H, d] contiguous
-  long long rows;   // T * H
-  int H;
+  int T, H;
   long long num_slots;
+  int groups, heads_per_group;  // of the k and v heads, as in RopeParams
 };
 
-// HD / 16 threads per row of k and of v: grid ceil(2 * rows * HD / 16 / 256).
+// Threads as in fa_rope_kernel: one per (head group, token, chunk of 16 features), the heads of k and v
+// counted in that order; four rows on their way at once.
 template <int HD, int kType>
-__global__ void __launch_bounds__(256) fa_cache_read_kernel(const ReadParams p) {
-  constexpr int kChunks = HD / 16;
-  const long long gt = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  const int chunk = static_cast<int>(gt % kChunks);
-  long long r = gt / kChunks;
-  if (r >= 2 * p.rows) return;
-  const bool is_v = r >= p.rows;
-  if (is_v) r -= p.rows;
-  const long long m = r / p.H;
-  const int h = static_cast<int>(r % p.H);
+__global__ void __launch_bounds__(kRopeThreads) fa_cache_read_kernel(const ReadParams p) {
+  constexpr int kChunks = HD / 16, kUnroll = 4;
+  const unsigned long long gid = static_cast<unsigned long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
+  const int chunk = static_cast<int>(gid % kChunks);
+  const unsigned long long rest = gid / kChunks;
+  const unsigned group = static_cast<unsigned>(rest / static_cast<unsigned>(p.T));
+  if (group >= static_cast<unsigned>(p.groups)) return;
+  const long long m = rest - static_cast<unsigned long long>(group) * p.T;
+  const int first = group * p.heads_per_group, last = min(first + p.heads_per_group, 2 * p.H);
   long long slot = p.slots[m];
   if (slot >= p.num_slots) {
-    if (chunk == 0) atomicExch(&g_device_status, 1 /* FA_ERR_INVALID_ARG */);
+    atomicExch(&g_device_status, 1 /* FA_ERR_INVALID_ARG */);
     slot = -1;
   }
-  float f[16];
+  const long long row0 = slot < 0 ? 0 : slot / kCachePage * p.H * kCachePage + slot % kCachePage;
+  struct Row { uint4 c[kType == kCacheBf16 ? 2 : 1]; float scale; } row[kUnroll];
+  for (int h0 = first; h0 < last; h0 += kUnroll) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) f[i] = 0.f;
-  if (slot >= 0) {
-    const long long row = (slot / kCachePage * p.H + h) * kCachePage + slot % kCachePage;
-    const void *pool = is_v ? p.v_pool : p.k_pool;
-    if constexpr (kType == kCacheBf16) {
-      const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(pool) + row * HD + 16 * chunk;
-      load8(src, f);
-      load8(src + 8, f + 8);
-    } else {
-      const float scale = (is_v ? p.v_scale : p.k_scale)[row];
-      const uint4 c = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(pool) + row * HD + 16 * chunk);
-      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint32_t b = (w[i / 4] >> (8 * (i % 4))) & 0xffu;
-        float y;
-        if constexpr (kType == kCacheE4m3) {
-          __nv_fp8_e4m3 e;
-          e.__x = static_cast<__nv_fp8_storage_t>(b);
-          y = static_cast<float>(e);
-        } else {
-          y = static_cast<float>(static_cast<int8_t>(b));
-        }
-        f[i] = y * scale;
+    for (int u = 0; u < kUnroll; ++u) {
+      if (h0 + u >= last || slot < 0) continue;
+      const bool is_v = h0 + u >= p.H;
+      const long long r = row0 + static_cast<long long>(h0 + u - (is_v ? p.H : 0)) * kCachePage;
+      const uint8_t *pool = static_cast<const uint8_t *>(is_v ? p.v_pool : p.k_pool);
+      if constexpr (kType == kCacheBf16) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(pool + (r * HD + 16 * chunk) * 2);
+        row[u].c[0] = src[0];
+        row[u].c[1] = src[1];
+      } else {
+        row[u].c[0] = *reinterpret_cast<const uint4 *>(pool + r * HD + 16 * chunk);
+        row[u].scale = (is_v ? p.v_scale : p.k_scale)[r];
       }
     }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (h0 + u >= last) break;
+      const bool is_v = h0 + u >= p.H;
+      uint16_t *dst = (is_v ? p.v : p.k) + (m * p.H + h0 + u - (is_v ? p.H : 0)) * HD + 16 * chunk;
+      uint4 o[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+      if (slot >= 0) {
+        if constexpr (kType == kCacheBf16) {
+          o[0] = row[u].c[0];
+          o[1] = row[u].c[1];
+        } else {
+          const uint32_t w[4] = {row[u].c[0].x, row[u].c[0].y, row[u].c[0].z, row[u].c[0].w};
+          uint32_t b[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float x, y;
+            if constexpr (kType == kCacheE4m3) {
+              const __half2 f = __half2(__nv_cvt_fp8x2_to_halfraw2(
+                  static_cast<__nv_fp8x2_storage_t>(w[i / 2] >> (16 * (i % 2))), __NV_E4M3));
+              x = __low2float(f);
+              y = __high2float(f);
+            } else {
+              x = static_cast<float>(static_cast<int8_t>(w[i / 2] >> (16 * (i % 2))));
+              y = static_cast<float>(static_cast<int8_t>(w[i / 2] >> (16 * (i % 2) + 8)));
+            }
+            b[i] = pack_bf16x2(x * row[u].scale, y * row[u].scale);
+          }
+          o[0] = make_uint4(b[0], b[1], b[2], b[3]);
+          o[1] = make_uint4(b[4], b[5], b[6], b[7]);
+        }
+      }
+      reinterpret_cast<uint4 *>(dst)[0] = o[0];
+      reinterpret_cast<uint4 *>(dst)[1] = o[1];
+    }
   }
-  uint16_t *dst = (is_v ? p.v : p.k) + r * HD + 16 * chunk;
-  store8(reinterpret_cast<__nv_bfloat16 *>(dst), f);
-  store8(reinterpret_cast<__nv_bfloat16 *>(dst + 8), f + 8);
 }
 
 }  // namespace fa

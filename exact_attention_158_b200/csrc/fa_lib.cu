@@ -1043,9 +1043,9 @@ cudaError_t launch_append(const fa::AppendParams &p, fa_cache_type type, unsigne
 
 template <int HD>
 cudaError_t launch_read(const fa::ReadParams &p, fa_cache_type type, unsigned grid, cudaStream_t s) {
-  if (type == FA_CACHE_BF16) fa::fa_cache_read_kernel<HD, fa::kCacheBf16><<<grid, 256, 0, s>>>(p);
-  else if (type == FA_CACHE_E4M3) fa::fa_cache_read_kernel<HD, fa::kCacheE4m3><<<grid, 256, 0, s>>>(p);
-  else fa::fa_cache_read_kernel<HD, fa::kCacheInt8><<<grid, 256, 0, s>>>(p);
+  if (type == FA_CACHE_BF16) fa::fa_cache_read_kernel<HD, fa::kCacheBf16><<<grid, fa::kRopeThreads, 0, s>>>(p);
+  else if (type == FA_CACHE_E4M3) fa::fa_cache_read_kernel<HD, fa::kCacheE4m3><<<grid, fa::kRopeThreads, 0, s>>>(p);
+  else fa::fa_cache_read_kernel<HD, fa::kCacheInt8><<<grid, fa::kRopeThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -1418,12 +1418,10 @@ fa_status fa_cache_read(const void *k_pool, const void *v_pool, const float *k_s
   p.slots = slots;
   p.k = static_cast<uint16_t *>(k);
   p.v = static_cast<uint16_t *>(v);
-  p.rows = static_cast<long long>(T) * H;
+  p.T = T;
   p.H = H;
   p.num_slots = static_cast<long long>(num_blocks) * fa::kCachePage;
-  const long long blocks = (2 * p.rows * (d / 16) + 255) / 256;
-  if (blocks > INT_MAX) return FA_ERR_INVALID_ARG;
-  const size_t out_bytes = static_cast<size_t>(p.rows) * d * 2;
+  const size_t out_bytes = static_cast<size_t>(T) * H * d * 2;
   const size_t rows = static_cast<size_t>(num_blocks) * H * fa::kCachePage;
   const size_t pool_bytes = rows * d * (type == FA_CACHE_BF16 ? 2 : 1);
   const void *ins[5] = {k_pool, v_pool, k_scale, v_scale, slots};
@@ -1437,7 +1435,7 @@ fa_status fa_cache_read(const void *k_pool, const void *v_pool, const float *k_s
   int dev_id = 0;
   if ((st = current_device(&dev, &dev_id)) != FA_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned grid = static_cast<unsigned>(blocks);
+  const unsigned grid = rope_split(T, 2 * H, d, dev->num_sms, &p.groups, &p.heads_per_group);
   cudaError_t e = d == 128 ? launch_read<128>(p, type, grid, s) : launch_read<64>(p, type, grid, s);
   return e == cudaSuccess ? FA_OK : launch_failed(e);
 }
