@@ -58,18 +58,25 @@ __device__ __forceinline__ uint32_t cache_code4(const float *f, float s, float r
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
     return lo | (hi << 16);
   } else {
-    uint32_t w = 0;
+    // |y| <= 127 (1 + 2^-23): adding 1.5 * 2^23 leaves the nearest integer in the low bits, and no clamp
+    // is needed (a conversion instruction runs at an eighth of the rate)
+    uint32_t b[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = max(-127, min(127, __float2int_rn(y[i])));
-      w |= static_cast<uint32_t>(c & 0xff) << (8 * i);
-    }
-    return w;
+    for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(y[i] + 12582912.f);
+    return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
   }
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN when either is one
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
 // Threads as in fa_rope_kernel: one per (head group, token, chunk), the heads of q, k and v counted in
 // that order; HD / 16 threads a row, 16 features each, the row maximum by shuffles among them.
+// Instructions, not bytes, bound the first form of this kernel (254 per four rows of a warp, 47 us for
+// 8191 tokens x 48 heads of 128; QQQQ now): a thread walks its q, k and v rows in loops of their own.
 template <int HD, int kType>
 __global__ void __launch_bounds__(kRopeThreads) fa_cache_append_kernel(const AppendParams p) {
   constexpr int kChunks = HD / 16, kUnroll = 4;
@@ -78,90 +85,82 @@ __global__ void __launch_bounds__(kRopeThreads) fa_cache_append_kernel(const App
   const int chunk = static_cast<int>(gid % kChunks);
   const unsigned long long rest = gid / kChunks;
   const unsigned group = static_cast<unsigned>(rest / static_cast<unsigned>(p.T));
-  // threads past the end stay for the shuffles, without rows
-  const bool live = group < static_cast<unsigned>(p.groups);
-  const long long m = live ? rest - static_cast<unsigned long long>(group) * p.T : 0;
-  const int first = live ? group * p.heads_per_group : 0;
-  const int last = live ? min(first + p.heads_per_group, p.Hq + 2 * p.Hk) : 0;
+  if (group >= static_cast<unsigned>(p.groups)) return;  // whole rows of threads
+  const long long m = rest - static_cast<unsigned long long>(group) * p.T;
+  const int first = group * p.heads_per_group;
+  const int last = min(first + p.heads_per_group, p.Hq + 2 * p.Hk);
   const int2 rcol = rope_cols(p.table, chunk), vcol = make_int2(16 * chunk, 16 * chunk + 8);
-  auto load = [&](Raw16<bf> &r, int h) {
-    if (h >= last) return;
-    const uint16_t *row = h < p.Hq ? p.q + m * p.q_s[0] + h * p.q_s[1]
-                          : h < p.Hq + p.Hk ? p.k + m * p.k_s[0] + (h - p.Hq) * p.k_s[1]
-                                            : p.v + m * p.v_s[0] + (h - p.Hq - p.Hk) * p.v_s[1];
-    raw_load(r, reinterpret_cast<const bf *>(row), h < p.Hq + p.Hk ? rcol : vcol);
-  };
-  Raw16<bf> raw[kUnroll];
-#pragma unroll
-  for (int u = 0; u < kUnroll; ++u) load(raw[u], first + u);
-  long long slot = live ? p.slots[m] : -1;
-  RopeTurn turn;
-  turn.any = false;
-  // (a thread whose heads are all values needs no angles)
-  if (first < p.Hq + p.Hk && live) rope_turn(p.table, p.positions + m, chunk, turn);
+  long long slot = p.slots[m];
   if (slot >= p.num_slots) {  // caller broke the contract: report, write nothing for the token
     atomicExch(&g_device_status, 1 /* FA_ERR_INVALID_ARG */);
     slot = -1;
   }
-  for (int i = 0; i < p.heads_per_group; i += kUnroll) {  // the same rounds for every thread
+  RopeTurn turn;
+  // rows [lo, hi) of one kind: four loads on their way ahead of `put`
+  auto walk = [&](const uint16_t *src, long long step, int lo, int hi, int2 col, auto put) {
+    Raw16<bf> raw[kUnroll];
+    if (lo >= hi) return;
+    const bf *row = reinterpret_cast<const bf *>(src) + lo * step;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (i + u >= p.heads_per_group) break;
-      int h = first + i + u;
-      const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hk;
-      const bool act = h < last && (is_q || slot >= 0);
-      const int2 col = is_v ? vcol : rcol;
-      float f[16];
+    for (int u = 0; u < kUnroll; ++u)
+      if (lo + u < hi) raw_load(raw[u], row + u * step, col);
+    for (int h0 = lo; h0 < hi; h0 += kUnroll) {
+      row += kUnroll * step;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) f[e] = 0.f;
-      if (act) {
+      for (int u = 0; u < kUnroll; ++u) {
+        if (h0 + u >= hi) break;
+        float f[16];
         raw_floats(raw[u], f);
-        if (!is_v) rope_apply(p.table, turn, f);
-      }
-      load(raw[u], h + kUnroll);
-      if (!is_q) h -= is_v ? p.Hq + p.Hk : p.Hq;
-      float top = 0.f, bad = 0.f;
-      if constexpr (kType != kCacheBf16) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          top = fmaxf(top, fabsf(f[e]));
-          bad = fmaf(f[e], 0.f, bad);  // NaN when any feature is infinite or NaN
-        }
-#pragma unroll
-        for (int off = kChunks / 2; off > 0; off >>= 1) {
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-          bad += __shfl_xor_sync(0xffffffffu, bad, off);
-        }
-      }
-      if (!act) continue;
-      if (is_q) {
-        uint16_t *dst = p.q_out + m * p.qo_s[0] + h * p.qo_s[1];
-        store8(reinterpret_cast<bf *>(dst + col.x), f);
-        store8(reinterpret_cast<bf *>(dst + col.y), f + 8);
-        continue;
-      }
-      const long long row = (slot / kCachePage * p.Hk + h) * kCachePage + slot % kCachePage;
-      void *pool = is_v ? p.v_pool : p.k_pool;
-      if constexpr (kType == kCacheBf16) {
-        uint16_t *dst = static_cast<uint16_t *>(pool) + row * HD;
-        store8(reinterpret_cast<bf *>(dst + col.x), f);
-        store8(reinterpret_cast<bf *>(dst + col.y), f + 8);
-      } else {
-        float scale = top >= kCacheTiny ? __fdiv_rn(top, cache_qmax<kType>()) : 0.f;
-        float rcp = scale > 0.f ? __frcp_rn(scale) : 0.f;
-        if (!(bad == 0.f)) scale = __int_as_float(0x7fc00000), rcp = 0.f;
-        uint32_t w[4] = {0u, 0u, 0u, 0u};
-        if (rcp > 0.f) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = cache_code4<kType>(f + 4 * e, scale, rcp);
-        }
-        uint8_t *dst = static_cast<uint8_t *>(pool) + row * HD;
-        *reinterpret_cast<uint2 *>(dst + col.x) = make_uint2(w[0], w[1]);
-        *reinterpret_cast<uint2 *>(dst + col.y) = make_uint2(w[2], w[3]);
-        if (chunk == 0) (is_v ? p.v_scale : p.k_scale)[row] = scale;
+        if (h0 + u + kUnroll < hi) raw_load(raw[u], row + u * step, col);
+        put(h0 + u, f);
       }
     }
-  }
+  };
+  const unsigned mates = ((1u << kChunks) - 1u) << ((threadIdx.x & 31) / kChunks * kChunks);
+  const long long row0 = slot < 0 ? 0 : slot / kCachePage * p.Hk * kCachePage + slot % kCachePage;
+  auto store = [&](void *pool, float *scales, int h, int2 col, const float (&f)[16]) {
+    const long long row = row0 + static_cast<long long>(h) * kCachePage;
+    if constexpr (kType == kCacheBf16) {
+      bf *dst = static_cast<bf *>(pool) + row * HD;
+      store8(dst + col.x, f);
+      store8(dst + col.y, f + 8);
+    } else {
+      float top = 0.f;  // NaN and infinities come through
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = max_nan(top, fabsf(f[e]));
+#pragma unroll
+      for (int off = kChunks / 2; off > 0; off >>= 1) top = max_nan(top, __shfl_xor_sync(mates, top, off));
+      float scale = top >= kCacheTiny ? __fdiv_rn(top, cache_qmax<kType>()) : 0.f;
+      float rcp = scale > 0.f ? __frcp_rn(scale) : 0.f;
+      if (!(top < INFINITY)) scale = __int_as_float(0x7fc00000), rcp = 0.f;
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+      if (rcp > 0.f) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = cache_code4<kType>(f + 4 * e, scale, rcp);
+      }
+      uint8_t *dst = static_cast<uint8_t *>(pool) + row * HD;
+      *reinterpret_cast<uint2 *>(dst + col.x) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2 *>(dst + col.y) = make_uint2(w[2], w[3]);
+      if (chunk == 0) scales[row] = scale;
+    }
+  };
+  // (a thread whose heads are all values needs no angles)
+  turn.any = false;
+  if (first < p.Hq + p.Hk) rope_turn(p.table, p.positions + m, chunk, turn);
+  walk(p.q + m * p.q_s[0], p.q_s[1], first, min(last, p.Hq), rcol, [&](int h, float (&f)[16]) {
+    rope_apply(p.table, turn, f);
+    bf *dst = reinterpret_cast<bf *>(p.q_out) + m * p.qo_s[0] + h * p.qo_s[1];
+    store8(dst + rcol.x, f);
+    store8(dst + rcol.y, f + 8);
+  });
+  if (slot < 0) return;
+  walk(p.k + m * p.k_s[0], p.k_s[1], max(first - p.Hq, 0), min(last - p.Hq, p.Hk), rcol, [&](int h, float (&f)[16]) {
+    rope_apply(p.table, turn, f);
+    store(p.k_pool, p.k_scale, h, rcol, f);
+  });
+  const int v0 = p.Hq + p.Hk;
+  walk(p.v + m * p.v_s[0], p.v_s[1], max(first - v0, 0), min(last - v0, p.Hk), vcol,
+       [&](int h, float (&f)[16]) { store(p.v_pool, p.v_scale, h, vcol, f); });
 }
 
 struct ReadParams {
