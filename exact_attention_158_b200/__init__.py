@@ -18,6 +18,7 @@ A serving step over an 8-bit cache writes its tokens and then attends to them:
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -710,6 +711,7 @@ def fa_cache_read(k_pool, v_pool, slots, k_scale=None, v_scale=None, k_out=None,
     return k_out, v_out
 
 
+@functools.lru_cache(maxsize=1024)
 def fa_q8_workspace_size(S: int, Hq: int, Hk: int, Lq: int, d: int, max_blocks_per_seq: int) -> int:
     """Bytes of workspace fa_decode_paged_q8 (Lq = 1), fa_prefill_paged_q8 and fa_tree_attention_q8
     need; 0 when none."""
@@ -737,7 +739,7 @@ def _attend_q8(where, q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens
         _require_flat(tree_mask, "tree_mask", torch.int64, (S, Lq), dev)
     code_o = _out_code(out_dtype)
     if out is None:
-        out = q.new_empty(shape, dtype=out_dtype)
+        out = torch.empty_like(q) if code_o == FA_OUT_BF16 else q.new_empty(shape, dtype=out_dtype)
     else:
         _require_flat(out, "out", out_dtype, shape, dev)
     if lse is not None:
@@ -747,7 +749,7 @@ def _attend_q8(where, q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens
     maxb = block_table.shape[1]
     ws, ws_bytes = None, 0
     if workspace is None:
-        ws_bytes = lib.fa_q8_workspace_size(S, Hq, Hk, Lq, d, maxb)
+        ws_bytes = fa_q8_workspace_size(S, Hq, Hk, Lq, d, maxb)
         if ws_bytes:
             workspace = q.new_empty(ws_bytes, dtype=torch.uint8)
             ws = workspace.data_ptr()
