@@ -1177,6 +1177,15 @@ fa_status launch_q8_tile(DeviceInfo &dev, const fa::Q8Params &p, cudaStream_t s)
                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            static_cast<int>(C::kSmem));
       if (e != cudaSuccess) return launch_failed(e);
+      // the kernel's warps hand registers to one another: a build that launches with fewer would wait
+      // for them for ever
+      cudaFuncAttributes attr;
+      if ((e = cudaFuncGetAttributes(&attr, fa::fa_q8_tile_kernel<HD, kType, kTwo>)) != cudaSuccess)
+        return launch_failed(e);
+      if (attr.numRegs < fa::kQ8LaunchRegs) {
+        t_last_error = "fa_q8_tile_kernel was built with too few registers";
+        return FA_ERR_LAUNCH;
+      }
       dev.q8_attr[slot] = true;
     }
   }

@@ -5,8 +5,8 @@
 // One CTA takes up to 256 of the R rows of one (sequence, key head) and a range of its 128-token
 // tiles.  Codes cannot feed a 16-bit product, so they are converted once per tile for all of the
 // CTA's rows:
-//   warps 0-3    one side: a thread holds a row (a TMEM lane).  Scores out of TMEM, p to shared
-//                memory; one thread issues the side's products
+//   warps 0-3    one side: a thread holds a row (a TMEM lane).  Scores out of TMEM, p back over
+//                them; one thread issues the side's products
 //   warps 4-7    the other side
 //   warps 8-11   codes: global (one tile ahead, in registers) -> fp16 K and V tiles in the
 //                swizzled layout the tensor core reads; the tile's key scales and its live tokens
@@ -27,8 +27,8 @@
 // as 0 * NaN: V is 0 there, and rows that do see it are marked and written as NaN.
 //
 // A row's softmax is one pass: p = 2^(s ks - m) against the reference it has, summed and stored;
-// only when their sum passes 2^15 (always on a row's first tile) or F has grown does the warp go back to
-// S, move the references so that the largest p is 2^6, rescale O in TMEM and do the pass again.
+// where one passes 2^15, and on a row's first tile, the reference moves so that the largest p is 2^6, and
+// O is rescaled in TMEM (as it is when F has grown).
 //
 // Queries go to fp16 against one power of two for all rows of the CTA (q8_q_unit; it is part of the key
 // scales).  int8's conversion leaves every four features in the order 0, 2, 1, 3; q is stored in that
@@ -44,8 +44,8 @@ namespace fa {
 
 constexpr int kQ8TileThreads = 12 * 32;
 constexpr int kQ8Tok = 128;                 // tokens of a tile
-constexpr float kQ8TileMost = 0x1p15f;      // a tile's sum of p, and so any p: fp16 ends at 2^16
-constexpr float kQ8TileStart = 6.f;         // log2 of the largest p after the reference has moved
+constexpr float kQ8TileMost = 15.f;         // log2 of the largest p: fp16 ends at 2^16
+constexpr float kQ8TileStart = 6.f;         // and after the reference has moved
 // f at the largest vs: e4m3 codes are at most 448, int8 codes 127
 template <int kType> __device__ constexpr float q8_vtop() { return kType == kQ8E4m3 ? 0x1p6f : 0x1p8f; }
 
@@ -54,11 +54,11 @@ struct Q8TileCfg {
   static constexpr int kChunks = HD / 64;             // 64-feature (128-byte) swizzle chunks
   static constexpr int kChunkBytes = 128 * 128;       // 128 rows x 128 bytes
   static constexpr int kTileBytes = kChunks * kChunkBytes;
-  static constexpr int kPBytes = 2 * kChunkBytes;     // 128 x 128 fp16
   static constexpr int kScaleBufs = 4;
-  static constexpr int kBars = 30;
-  static constexpr size_t kSmem = 1024 + 2 * kTileBytes + 2 * kTileBytes + 2 * kPBytes +
-                                  kScaleBufs * (kQ8Tok * 4 + 48) + kBars * 8 + 48;
+  static constexpr int kBars = 30;  // 22 + 8 turns
+  // Q (two row tiles), K and V (two tiles of tokens each)
+  static constexpr size_t kNeed = 1024 + 6 * kTileBytes + kScaleBufs * (kQ8Tok * 4 + 48) + kBars * 8 + 48;
+  static constexpr size_t kSmem = kNeed > 116 * 1024 ? kNeed : 116 * 1024;
   static constexpr uint32_t kColS = 0, kColO = 256;
   // fp16 operands: the type fields of A and B are 0
   static constexpr uint32_t kFp16 = ~((1u << 7) | (1u << 10));
@@ -84,89 +84,79 @@ __device__ __forceinline__ uint32_t mul_fp16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// Registers a thread: 168 for all at launch (384 x 168 = 64512).  The softmax keeps 128 scores at once
+// and spilled around them (reloads from L2: 800 to 2400 cycles a tile), the conversion needs fewer:
+// 8 warps x 32 x 200 + 4 x 32 x 104 = 64512.
+constexpr int kQ8LaunchRegs = 168, kQ8SoftmaxRegs = 200, kQ8ConvertRegs = 104;
+static_assert(256 * kQ8SoftmaxRegs + 128 * kQ8ConvertRegs <= kQ8TileThreads * kQ8LaunchRegs,
+              "registers of the launch");
+template <int N>
+__device__ __forceinline__ void q8_regs_acquire() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void q8_regs_release() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // Keeps uses of registers that a tcgen05.ld fills behind the wait that precedes this.
 __device__ __forceinline__ void q8_pin(float (&x)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(x[i]));
 }
 
-// 32 scores of a row -> p: added to sum, rounded to fp16 into units unit0.. of the row of P.  kMasked:
-// only the tokens in k take part.  The steps are kept apart (all loads of ks, all arguments, all
-// exponentials, then sums and stores): interleaved per few scores, each waits for the one before it,
-// and loads of ks cannot move above stores of p, which the compiler cannot tell apart.
+// A row's 128 scores (TMEM) -> p in fp16 (TMEM, over the scores: token pairs in the first 64 columns) and
+// the sum of p.  k: the tokens that the row sees (kMasked: not all of them).  m and l are the row's
+// reference and sum so far; where the reference has to move, l is brought to the new one and `a` is
+// multiplied by what O needs.  All scores are in registers at once and the steps are kept apart
+// (arguments, largest, exponentials).
 template <bool kMasked>
-__device__ __forceinline__ void q8_weigh32(float (&x)[32], uint32_t k, const float *ks, uint64_t neg2,
-                                           uint64_t (&sum)[4], uint8_t *p_chunk, int row, int unit0) {
-  uint64_t f[16];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const ulonglong2 v = reinterpret_cast<const ulonglong2 *>(ks)[i];
-    f[2 * i] = v.x;
-    f[2 * i + 1] = v.y;
-  }
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), f[i], neg2), x[2 * i], x[2 * i + 1]);
-    if (kMasked) {
-      x[2 * i] = (k >> (2 * i)) & 1 ? x[2 * i] : -INFINITY;
-      x[2 * i + 1] = (k >> (2 * i + 1)) & 1 ? x[2 * i + 1] : -INFINITY;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 32; ++i) x[i] = ex2(x[i]);
-  uint32_t pk[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    sum[i % 4] = f2_add(sum[i % 4], f2_pack(x[2 * i], x[2 * i + 1]));
-    pk[i] = pack_fp16x2(x[2 * i], x[2 * i + 1]);
-  }
-#pragma unroll
-  for (int u = 0; u < 4; ++u)
-    *reinterpret_cast<uint4 *>(p_chunk + q8_swz(row, unit0 + u)) =
-        make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
-}
-
-// A row's 128 scores (TMEM) -> P (shared memory) and the sum of p, against the reference m.  k: the
-// tokens that the row sees.
-template <int HD, bool kMasked>
-__device__ __forceinline__ float q8_weigh(uint32_t s_tmem, const uint32_t (&k)[4], const float *ks, float m,
-                                          uint8_t *pt, int row) {
+__device__ __forceinline__ float q8_weigh(uint32_t s_tmem, const uint32_t (&k)[4], const float *ks, float &m,
+                                          float &l, float &a) {
   const uint64_t neg2 = f2_pack(-m, -m);
-  uint64_t sum[4] = {0, 0, 0, 0};
-  float x[2][32];
-  tmem_ld32(s_tmem, reinterpret_cast<uint32_t *>(x[0]));
+  float x[128];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    tmem_wait_ld();
-    q8_pin(x[c & 1]);
-    if (c < 3) tmem_ld32(s_tmem + 32 * (c + 1), reinterpret_cast<uint32_t *>(x[(c + 1) & 1]));
-    q8_weigh32<kMasked>(x[c & 1], k[c], ks + 32 * c, neg2, sum,
-                        pt + (c / 2) * Q8TileCfg<HD>::kChunkBytes, row, 4 * (c & 1));
-  }
-  float a, b;
-  f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), a, b);
-  return a + b;
-}
-
-// The largest scaled score among the tokens in k.
-__device__ __forceinline__ float q8_row_max(uint32_t s_tmem, const uint32_t (&k)[4], const float *ks) {
-  float x = -INFINITY;
-#pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    float sc[32];
-    tmem_ld32(s_tmem + 32 * c, reinterpret_cast<uint32_t *>(sc));
-    const uint32_t kc = c == 0 ? k[0] : c == 1 ? k[1] : c == 2 ? k[2] : k[3];
-    tmem_wait_ld();
-    q8_pin(sc);
+  for (int c = 0; c < 4; ++c) tmem_ld32(s_tmem + 32 * c, reinterpret_cast<uint32_t *>(x) + 32 * c);
+  tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-      const float4 f = *reinterpret_cast<const float4 *>(ks + 32 * c + i);
-      const float y[4] = {sc[i] * f.x, sc[i + 1] * f.y, sc[i + 2] * f.z, sc[i + 3] * f.w};
+  for (int i = 0; i < 128; ++i) asm volatile("" : "+f"(x[i]));
+  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x = fmaxf(x, (kc >> (i + e)) & 1 ? y[e] : -INFINITY);
+  for (int i = 0; i < 32; ++i) {
+    const ulonglong2 f = reinterpret_cast<const ulonglong2 *>(ks)[i];
+    f2_unpack(f2_fma(f2_pack(x[4 * i], x[4 * i + 1]), f.x, neg2), x[4 * i], x[4 * i + 1]);
+    f2_unpack(f2_fma(f2_pack(x[4 * i + 2], x[4 * i + 3]), f.y, neg2), x[4 * i + 2], x[4 * i + 3]);
+    if (kMasked) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        x[4 * i + e] = (k[i / 8] >> (4 * (i % 8) + e)) & 1 ? x[4 * i + e] : -INFINITY;
     }
+    top[i % 4] = fmax3(top[i % 4], fmaxf(x[4 * i], x[4 * i + 1]), fmaxf(x[4 * i + 2], x[4 * i + 3]));
   }
-  return x;
+  const float t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  // (a row that has seen nothing has l = 0; an infinite score makes its row NaN through inf - inf)
+  const bool over = t > kQ8TileMost || (l == 0.f && t != -INFINITY);
+  if (__any_sync(0xffffffffu, over)) {
+    const float d = over ? t - kQ8TileStart : 0.f;
+    const float r = l == 0.f ? 1.f : ex2(-d);
+    m += d;
+    l *= r;
+    a *= r;
+    const uint64_t d2 = f2_pack(d, d);
+#pragma unroll
+    for (int i = 0; i < 64; ++i)
+      f2_unpack(f2_sub(f2_pack(x[2 * i], x[2 * i + 1]), d2), x[2 * i], x[2 * i + 1]);
+  }
+  uint64_t sum[2] = {0, 0};
+  uint32_t pk[64];
+#pragma unroll
+  for (int i = 0; i < 64; ++i) {
+    const float p0 = ex2(x[2 * i]), p1 = ex2(x[2 * i + 1]);
+    sum[i % 2] = f2_add(sum[i % 2], f2_pack(p0, p1));
+    pk[i] = pack_fp16x2(p0, p1);
+  }
+  tmem_st32(s_tmem, pk);
+  tmem_st32(s_tmem + 32, pk + 32);
+  tmem_wait_st();
+  float u, v;
+  f2_unpack(f2_add(sum[0], sum[1]), u, v);
+  return u + v;
 }
 
 // 32 features of a row, in the conversion's order, from its sums: to the output, or as a partial.
@@ -184,7 +174,7 @@ __device__ __forceinline__ void q8_write32(const Q8Params &p, size_t row, int sp
     else
       q8_write4<HD>(p, row, c + i, v, m, l);
   }
-  if (c == 0 && p.n_split > 1) p.ws_ml[row * p.n_split + split] = make_float2(m, l);
+  if (c == 0 && p.n_split > 1) p.ws_ml[row * p.n_split + split] = make_float2(l == 0.f ? -INFINITY : m, l);
 }
 
 // Token tiles that the rows [r0, r1) can see: all of them, or up to the last row's own token.
@@ -208,18 +198,17 @@ __device__ __forceinline__ void q8_issue_qk(uint32_t d_tmem, const uint8_t *q, c
   }
 }
 
-// O (TMEM) (+)= P V: P K-major over the tokens, V MN-major (chunks of 64 features, 8-token groups).
+// O (TMEM) (+)= P V: P from TMEM (8 columns per 16 tokens), V MN-major (chunks of 64 features, 8-token
+// groups).  P is not staged in shared memory: a 128 x 128 x 16 product with both operands there reads
+// the 128 bytes a cycle that shared memory has, and P's stores would come on top.
 template <int HD>
-__device__ __forceinline__ void q8_issue_pv(uint32_t d_tmem, const uint8_t *pt, const uint8_t *v, bool accumulate) {
+__device__ __forceinline__ void q8_issue_pv(uint32_t d_tmem, uint32_t p_tmem, const uint8_t *v, bool accumulate) {
   using C = Q8TileCfg<HD>;
-  const uint64_t pd = smem_desc_sw128(smem_u32(pt), 16, 1024);
   const uint64_t vd = smem_desc_sw128(smem_u32(v), C::kChunkBytes, 1024);
 #pragma unroll
-  for (int kk = 0; kk < kQ8Tok / 16; ++kk) {
-    const uint64_t off = static_cast<uint64_t>(((kk / 4) * C::kChunkBytes + (kk % 4) * 32) >> 4);
-    umma_ss(d_tmem, pd + off, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), C::kIdescPV,
+  for (int kk = 0; kk < kQ8Tok / 16; ++kk)
+    umma_ts(d_tmem, p_tmem + 8 * kk, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), C::kIdescPV,
             (accumulate || kk > 0) ? 1u : 0u);
-  }
 }
 
 // Every thread of warps 0-7 (none of them leaves before it; the waits on the way are bounded).
@@ -233,27 +222,24 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
   using C = Q8TileCfg<HD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t *sQ = smem;                     // two row tiles; with one, the other holds odd K tiles
-  uint8_t *sK = sQ + 2 * C::kTileBytes;
-  uint8_t *sV = sK + C::kTileBytes;
-  uint8_t *sP = sV + C::kTileBytes;
-  float *sKs = reinterpret_cast<float *>(sP + 2 * C::kPBytes);  // [buffer][token]: ks scale log2(e)
+  uint8_t *sQ = smem;                     // [row tile]
+  uint8_t *sK = sQ + 2 * C::kTileBytes;   // tile j of tokens is in [j & 1]
+  uint8_t *sV = sK + 2 * C::kTileBytes;
+  float *sKs = reinterpret_cast<float *>(sV + 2 * C::kTileBytes);  // [buffer][token]: ks scale log2(e)
   uint32_t *sLive = reinterpret_cast<uint32_t *>(sKs + C::kScaleBufs * kQ8Tok);  // [buffer][4]
   uint32_t *sBad = sLive + C::kScaleBufs * 4;  // [buffer][4]: live tokens whose vs is not finite
   float *sF = reinterpret_cast<float *>(sBad + C::kScaleBufs * 4);  // [buffer][4]: F of the tile
   uint64_t *bars = reinterpret_cast<uint64_t *>(sF + C::kScaleBufs * 4);
-  // Landing barriers of tile j are [j & 1], so that a side that waits for every other tile of tokens
-  // sees each phase of its own.  Buffers are freed by an arrival from each issuer that reads them.
-  uint64_t *k_full = bars, *v_full = bars + 2;  // [2]
-  uint64_t *k_free = bars + 4;                  // [2] (kTwo: [0])
-  uint64_t *v_free = bars + 6;
-  uint64_t *sc_full = bars + 7;                 // [4]
-  uint64_t *s_full = bars + 11;                 // [side]
-  uint64_t *p_full = bars + 13;                 // [side]
-  uint64_t *pv_done = bars + 15;                // [side]
-  uint64_t *drain = bars + 17;                  // [side] every product of an issuer has completed
-  uint64_t *q_full = bars + 19;                 // [row tile]
-  uint64_t *turn = bars + 21;                   // [side][warp]
+  // Barriers of tile j are [j & 1], as its buffers are, so that a side that waits for every other tile of
+  // tokens sees each phase of its own.  A buffer is freed by an arrival from each issuer that reads it.
+  uint64_t *k_full = bars, *v_full = bars + 2, *k_free = bars + 4, *v_free = bars + 6;  // [2]
+  uint64_t *sc_full = bars + 8;                 // [4]
+  uint64_t *s_full = bars + 12;                 // [side]
+  uint64_t *p_full = bars + 14;                 // [side]
+  uint64_t *pv_done = bars + 16;                // [side]
+  uint64_t *drain = bars + 18;                  // [side] every product of an issuer has completed
+  uint64_t *q_full = bars + 20;                 // [row tile]
+  uint64_t *turn = bars + 22;                   // [side][warp]
   float *sTop = reinterpret_cast<float *>(bars + C::kBars);  // [8]: the warps' largest |q|
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sTop + 8);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -288,13 +274,13 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
       mbar_init(k_full + i, 4);
       mbar_init(v_full + i, 4);
       mbar_init(k_free + i, kTwo ? 2 : 1);
+      mbar_init(v_free + i, kTwo ? 2 : 1);
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 4);
       mbar_init(pv_done + i, 1);
       mbar_init(drain + i, 1);
       mbar_init(q_full + i, 4);
     }
-    mbar_init(v_free, kTwo ? 2 : 1);
     for (int i = 0; i < 4; ++i) mbar_init(sc_full + i, 4);
     for (int i = 0; i < 8; ++i) mbar_init(turn + i, 1);
     *abort_flag = 0;
@@ -328,10 +314,10 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
 #pragma unroll
   for (int i = 1; i < 8; ++i) q_top = fmaxf(q_top, sTop[i]);
   const float q_unit = q8_q_unit(q_top);
-  auto k_tile = [&](int j) { return (kTwo || !(j & 1)) ? sK : sQ + C::kTileBytes; };
 
   if (warp >= 8) {
     // ------------------------------------------------------------------ codes -> 16-bit tiles
+    q8_regs_release<kQ8ConvertRegs>();
     const int w = warp - 8;              // tokens 32 w .. 32 w + 31 of a tile: pages 2 w, 2 w + 1
     constexpr int kPieces = HD / 8;      // 8-code pieces of a token
     constexpr int kRowsPer = 32 / kPieces;  // tokens that a warp-wide load covers
@@ -409,7 +395,7 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
         sBad[buf * 4 + w] = badmask;
         if (w == 0) sF[buf * 4] = F;
       }
-      uint8_t *kt = k_tile(j) + at0;
+      uint8_t *kt = sK + (j & 1) * C::kTileBytes + at0;
 #pragma unroll
       for (int k = 0; k < kLoads; ++k) {
         const int row = 32 * w + k * kRowsPer + sub;
@@ -429,6 +415,7 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
     };
     auto convert_v = [&](int j, uint32_t f2, uint32_t live_v) {
       const bool all = live_v == 0xffffffffu;
+      uint8_t *vt = sV + (j & 1) * C::kTileBytes + at0;
 #pragma unroll
       for (int k = 0; k < kLoads; ++k) {
         const int row = 32 * w + k * kRowsPer + sub;
@@ -439,15 +426,13 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
         q8_cvt4<kType>(vc[k].x, o.x, o.y);
         q8_cvt4<kType>(vc[k].y, o.z, o.w);
         o = make_uint4(mul_fp16x2(o.x, f), mul_fp16x2(o.y, f), mul_fp16x2(o.z, f), mul_fp16x2(o.w, f));
-        *reinterpret_cast<uint4 *>(sV + at0 + q8_swz(row, unit)) = o;
+        *reinterpret_cast<uint4 *>(vt + q8_swz(row, unit)) = o;
       }
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(v_full + (j & 1));
     };
-    // K runs kAhead tiles before V.  With one K buffer V_j is free first (P V_{j-1} is issued before
-    // Q K_j^T), with two K_{j+1} is.
-    constexpr int kAhead = kTwo ? 0 : 1;
+    // K runs one tile before V, as the products do
     int blk_k = named(0, entry_of(0)), entry = entry_of(1), blk_v = blk_k;
     if (nmax > 0) {
       fetch(kcodes, blk_k, kc);
@@ -456,36 +441,31 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
     }
     // f and the live tokens of the next V tile, and of the tile whose K was made last
     uint32_t f2_v = 0, f2_k = 0, live_v = 0, live_k = 0;
-    for (int j = -kAhead; j < nmax; ++j) {
-      const int jk = j + kAhead;
+    for (int j = -1; j < nmax; ++j) {
+      const int jk = j + 1;
       int blk_next = blk_k;
+      f2_v = f2_k, live_v = live_k;
       if (jk < nmax) {
-        const bool ok = kTwo ? (jk < 1 || mbar_wait(k_free, (jk - 1) & 1, abort_flag))
-                             : (jk < 2 || mbar_wait(k_free + (jk & 1), ((jk >> 1) - 1) & 1, abort_flag));
-        if (!__all_sync(0xffffffffu, ok)) break;
-        f2_v = f2_k, live_v = live_k;
+        if (jk >= 2 && !__all_sync(0xffffffffu, mbar_wait(k_free + (jk & 1), ((jk >> 1) - 1) & 1, abort_flag))) break;
         live_k = live;
         f2_k = convert_k(jk);
-        if (!kAhead) f2_v = f2_k, live_v = live_k;
         blk_next = named(jk + 1, entry);
         entry = entry_of(jk + 2);
         if (jk + 1 < nmax) {
           fetch(kcodes, blk_next, kc);
           fetch_scales(jk + 1, blk_next);
         }
-      } else {
-        f2_v = f2_k, live_v = live_k;
       }
       if (j >= 0) {
-        if (j > 0 && !__all_sync(0xffffffffu, mbar_wait(v_free, (j - 1) & 1, abort_flag))) break;
+        if (j >= 2 && !__all_sync(0xffffffffu, mbar_wait(v_free + (j & 1), ((j >> 1) - 1) & 1, abort_flag))) break;
         convert_v(j, f2_v, live_v);
-        blk_v = kAhead ? blk_k : blk_next;  // of tile j + 1
-        if (j + 1 < nmax) fetch(vcodes, blk_v, vc);
+        if (j + 1 < nmax) fetch(vcodes, blk_k, vc);  // (blk_k is still that of tile j + 1)
       }
-      blk_k = blk_next;  // of tile jk + 1
+      blk_k = blk_next;
     }
   } else {
     // ------------------------------------------------------------------ softmax, products, epilogue
+    q8_regs_acquire<kQ8SoftmaxRegs>();
     const int side = warp / 4;
     const int rtile = kTwo ? side : 0;
     const int lrow = threadIdx.x % 128;
@@ -512,7 +492,6 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
       if (lane == 0) mbar_arrive(q_full + rtile);
     }
     const uint32_t tS = tmem + C::kColS + 128 * side, tO = tmem + C::kColO + HD * side;
-    uint8_t *pt = sP + side * C::kPBytes;
     auto tile_of = [&](int i) { return kTwo ? i : 2 * i + side; };  // the side's i-th tile of tokens
     // The first thread of the side's first warp issues its products.  With two row tiles it also
     // arrives on k_free and v_free for the tiles of tokens that only the other one visits.
@@ -524,11 +503,11 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
       if (!mbar_wait(k_full + (j & 1), (j >> 1) & 1, abort_flag)) return false;
       if (i < cnt) {
         tc_fence_after();
-        q8_issue_qk<HD>(tS, sQ + rtile * C::kTileBytes, k_tile(j));
+        q8_issue_qk<HD>(tS, sQ + rtile * C::kTileBytes, sK + (j & 1) * C::kTileBytes);
         umma_commit(s_full + side);
-        umma_commit(k_free + (kTwo ? 0 : side));
+        umma_commit(k_free + (j & 1));
       } else {
-        mbar_arrive(k_free);
+        mbar_arrive(k_free + (j & 1));
       }
       return true;
     };
@@ -538,11 +517,13 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
       if (i < cnt) {
         if (!mbar_wait(p_full + side, i & 1, abort_flag)) return false;
         tc_fence_after();
-        q8_issue_pv<HD>(tO, pt, sV, i > 0);
+        q8_issue_pv<HD>(tO, tS, sV + (j & 1) * C::kTileBytes, i > 0);
         umma_commit(pv_done + side);
-        umma_commit(v_free);
+        umma_commit(v_free + (j & 1));
+        // P lies over S: the next scores may be written once this product has read it
+        if (!mbar_wait(pv_done + side, i & 1, abort_flag)) return false;
       } else {
-        mbar_arrive(v_free);
+        mbar_arrive(v_free + (j & 1));
       }
       return next_scores(i + 1);
     };
@@ -560,7 +541,7 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
     const int first_own = L - p.T;  // the first of the queries' own tokens
     const uint64_t bits = (p.tree && mine) ? p.tree[static_cast<size_t>(s) * p.T + t] : ~0ull;
     const bool warp_rows = row0 + 128 * rtile + (warp % 4) * 32 < p.R;  // any row in this warp
-    float m = -INFINITY, l = 0.f, F = 0.f;
+    float m = 0.f, l = 0.f, F = 0.f;
     bool poison = false;  // the row sees a token whose values are no numbers
     bool ok = __all_sync(0xffffffffu,
                          !lead || ((cnt == 0 || mbar_wait(q_full + rtile, 0, abort_flag)) && next_scores(0)));
@@ -569,10 +550,9 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
       const int buf = j % C::kScaleBufs;
       const float *ksb = sKs + buf * kQ8Tok;
       // warp-uniform, as the tensor-memory loads below are warp-wide.  P V of the tile before has
-      // completed (its issue stood before these scores'), so P may be written and O rescaled.
+      // completed (these scores are issued after it), so O may be rescaled.
       if (!__all_sync(0xffffffffu, mbar_wait(sc_full + buf, (j / C::kScaleBufs) & 1, abort_flag) &&
-                                       mbar_wait(s_full + side, i & 1, abort_flag) &&
-                                       (i == 0 || mbar_wait(pv_done + side, (i - 1) & 1, abort_flag))) ||
+                                       mbar_wait(s_full + side, i & 1, abort_flag)) ||
           !my_turn(i)) { ok = false; break; }
       tc_fence_after();
       if (!warp_rows) {
@@ -609,28 +589,9 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
         const uint4 bad = *reinterpret_cast<const uint4 *>(sBad + buf * 4);
         poison = poison || ((k[0] & bad.x) | (k[1] & bad.y) | (k[2] & bad.z) | (k[3] & bad.w)) != 0;
       }
-      // one pass against the reference at hand; a second, after a look at all scores, where that
-      // has to move (at once on the first tile)
-      float sum;
-      bool over = true;
-      float a = F_old / F;  // what O is to be multiplied by
-#pragma unroll 1
-      for (int round = i == 0 ? 1 : 0;; ++round) {
-        if (round == 1) {
-          const float x = q8_row_max(tS + lane_off, k, ksb);
-          if (over) {  // a row that sees nothing yet keeps m = -inf
-            const float r = m == -INFINITY ? 0.f : ex2(m - (x - kQ8TileStart));
-            m = x - kQ8TileStart;
-            l *= r;
-            a *= r;
-          }
-        }
-        sum = all ? q8_weigh<HD, false>(tS + lane_off, k, ksb, m, pt, lrow)
-                  : q8_weigh<HD, true>(tS + lane_off, k, ksb, m, pt, lrow);
-        if (round == 1) break;
-        over = sum > kQ8TileMost;
-        if (!__any_sync(0xffffffffu, over)) break;
-      }
+      float a = i == 0 ? 1.f : F_old / F;  // what O is to be multiplied by
+      const float sum = all ? q8_weigh<false>(tS + lane_off, k, ksb, m, l, a)
+                            : q8_weigh<true>(tS + lane_off, k, ksb, m, l, a);
       pass_turn(i);
       if (i > 0 && __any_sync(0xffffffffu, a != 1.f)) {
 #pragma unroll 1
@@ -647,7 +608,6 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
       }
       l += sum;
       tc_fence_before();
-      fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full + side);
       ok = __all_sync(0xffffffffu, !lead || products(i));
@@ -663,11 +623,11 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
     tc_fence_after();
     const float f = F / q8_vtop<kType>();  // of this side's O
     if constexpr (!kTwo) {
-      // join the sides: the odd tiles' sums go through shared memory (P is free: every product has
-      // completed), the even side writes.  Both are brought to the larger reference.
-      float *xo = reinterpret_cast<float *>(sP);                     // [feature][row]
-      float *xm = reinterpret_cast<float *>(sK);                     // m, l, poison of the odd side
-      q8_sides_barrier();  // neither side's products read P or K any more
+      // join the sides: the odd tiles' sums go through shared memory, the even side writes.  Both are
+      // brought to the larger reference.
+      float *xo = reinterpret_cast<float *>(sK);                     // [feature][row]
+      float *xm = reinterpret_cast<float *>(sV);                     // m, l, poison of the odd side
+      q8_sides_barrier();  // every product has completed: K and V are free
       if (side == 1 && warp_rows && ok) {
         xm[lrow] = m;
         xm[128 + lrow] = l;
