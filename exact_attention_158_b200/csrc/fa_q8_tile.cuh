@@ -8,7 +8,7 @@
 //   warps 0-3    one side: a thread holds a row (a TMEM lane).  Scores out of TMEM, p back over
 //                them; one thread issues the side's products
 //   warps 4-7    the other side
-//   warps 8-11   codes: global (one tile ahead, in registers) -> fp16 K and V tiles in the
+//   warps 8-11   codes: bulk copies into a staging slot, a tile ahead -> fp16 K and V tiles in the
 //                swizzled layout the tensor core reads; the tile's key scales and its live tokens
 // TMEM (512 columns): S0 [0,128)  S1 [128,256)  O0 [256,256+d)  O1 [256+d,256+2d).
 // With more than 128 rows the sides hold two row tiles; with fewer they share one row tile and take
@@ -55,9 +55,10 @@ struct Q8TileCfg {
   static constexpr int kChunkBytes = 128 * 128;       // 128 rows x 128 bytes
   static constexpr int kTileBytes = kChunks * kChunkBytes;
   static constexpr int kScaleBufs = 4;
-  static constexpr int kBars = 30;  // 22 + 8 turns
-  // Q (two row tiles), K and V (two tiles of tokens each)
-  static constexpr size_t kNeed = 1024 + 6 * kTileBytes + kScaleBufs * (kQ8Tok * 4 + 48) + kBars * 8 + 48;
+  static constexpr int kBars = 38;
+  // Q (two row tiles), K and V (two tiles of tokens each), the codes of one tile of tokens
+  static constexpr int kCodeBytes = kQ8Tok * HD;
+  static constexpr size_t kNeed = 6 * kTileBytes + 2 * kCodeBytes + kScaleBufs * (kQ8Tok * 4 + 48) + kBars * 8 + 48;
   static constexpr size_t kSmem = kNeed > 116 * 1024 ? kNeed : 116 * 1024;
   static constexpr uint32_t kColS = 0, kColO = 256;
   // fp16 operands: the type fields of A and B are 0
@@ -220,12 +221,13 @@ __device__ __forceinline__ void q8_sides_barrier() { asm volatile("bar.sync 1, 2
 template <int HD, int kType, bool kTwo>
 __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8Params p) {
   using C = Q8TileCfg<HD>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t *sQ = smem;                     // [row tile]
+  extern __shared__ __align__(1024) uint8_t q8_tile_smem[];  // no room for slack: checked below
+  uint8_t *sQ = q8_tile_smem;             // [row tile]
   uint8_t *sK = sQ + 2 * C::kTileBytes;   // tile j of tokens is in [j & 1]
   uint8_t *sV = sK + 2 * C::kTileBytes;
-  float *sKs = reinterpret_cast<float *>(sV + 2 * C::kTileBytes);  // [buffer][token]: ks scale log2(e)
+  uint8_t *sKc = sV + 2 * C::kTileBytes;  // codes of K as they land, a quarter of the tile to a warp
+  uint8_t *sVc = sKc + C::kCodeBytes;     // and of V
+  float *sKs = reinterpret_cast<float *>(sVc + C::kCodeBytes);  // [buffer][token]: ks scale log2(e)
   uint32_t *sLive = reinterpret_cast<uint32_t *>(sKs + C::kScaleBufs * kQ8Tok);  // [buffer][4]
   uint32_t *sBad = sLive + C::kScaleBufs * 4;  // [buffer][4]: live tokens whose vs is not finite
   float *sF = reinterpret_cast<float *>(sBad + C::kScaleBufs * 4);  // [buffer][4]: F of the tile
@@ -240,6 +242,7 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
   uint64_t *drain = bars + 18;                  // [side] every product of an issuer has completed
   uint64_t *q_full = bars + 20;                 // [row tile]
   uint64_t *turn = bars + 22;                   // [side][warp]
+  uint64_t *landed = bars + 30;                 // [K, V][converter warp]
   float *sTop = reinterpret_cast<float *>(bars + C::kBars);  // [8]: the warps' largest |q|
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sTop + 8);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -269,6 +272,10 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
   const int both = min(n[0], n[1]);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (smem_u32(q8_tile_smem) & 1023u) {  // the swizzled tiles need it; the launch gives it
+    if (threadIdx.x == 0) atomicExch(&g_device_status, 4 /* FA_ERR_LAUNCH */);
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + i, 4);
@@ -282,7 +289,7 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
       mbar_init(q_full + i, 4);
     }
     for (int i = 0; i < 4; ++i) mbar_init(sc_full + i, 4);
-    for (int i = 0; i < 8; ++i) mbar_init(turn + i, 1);
+    for (int i = 0; i < 8; ++i) mbar_init(turn + i, 1), mbar_init(landed + i, 1);
     *abort_flag = 0;
     if (L != p.lens[s] && p.lens[s] > 0) atomicExch(&g_device_status, 1 /* FA_ERR_INVALID_ARG */);
     fence_mbar_init();
@@ -322,6 +329,7 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
     constexpr int kPieces = HD / 8;      // 8-code pieces of a token
     constexpr int kRowsPer = 32 / kPieces;  // tokens that a warp-wide load covers
     constexpr int kLoads = 32 / kRowsPer;
+    constexpr uint32_t kSlab = kQ8Page * HD;  // a page of one head: contiguous in the pool
     const int piece = lane % kPieces, sub = lane / kPieces;
     const int32_t *trow = p.table + static_cast<size_t>(s) * p.max_blocks;
     const int nblk = (L + kQ8Page - 1) / kQ8Page;
@@ -337,131 +345,163 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
         atomicExch(&g_device_status, 1 /* FA_ERR_INVALID_ARG: the page is left out */);
       return -1;
     };
-    const uint8_t *kcodes = p.k_codes + static_cast<size_t>(kh) * kQ8Page * HD + sub * HD + 8 * piece;
-    const uint8_t *vcodes = p.v_codes + static_cast<size_t>(kh) * kQ8Page * HD + sub * HD + 8 * piece;
-    const size_t block_stride = static_cast<size_t>(p.Hk) * kQ8Page * HD;
-    uint2 kc[kLoads], vc[kLoads];
-    // a page left out reads block 0: its tokens are not live
-    auto fetch = [&](const uint8_t *codes, int blk, uint2 (&c)[kLoads]) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int b = max(__shfl_sync(0xffffffffu, blk, 2 * w + half), 0);
-        const uint8_t *src = codes + static_cast<size_t>(b) * block_stride;
-#pragma unroll
-        for (int k = 0; k < kLoads / 2; ++k) {
-          asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
-                       : "=r"(c[half * (kLoads / 2) + k].x), "=r"(c[half * (kLoads / 2) + k].y)
-                       : "l"(src + k * kRowsPer * HD));
-        }
+    uint8_t *kst = sKc + 2 * w * kSlab, *vst = sVc + 2 * w * kSlab;
+    uint64_t *k_landed = landed + w, *v_landed = landed + 4 + w;
+    // the warp's two pages of a tile into its staging slot: lanes 0 and 1, a page each; one that is left
+    // out is not loaded (its tokens are not live)
+    auto load_codes = [&](const uint8_t *codes, int blk, uint8_t *dst, uint64_t *bar) {
+      const int b = __shfl_sync(0xffffffffu, blk, 2 * w + (lane & 1));
+      const uint32_t both_named = __ballot_sync(0xffffffffu, b >= 0) & 3u;
+      if (lane == 0) {
+        if (both_named) mbar_arrive_expect_tx(bar, (both_named == 3u ? 2 : 1) * kSlab);
+        else mbar_arrive(bar);
       }
+      if (lane < 2 && b >= 0)
+        bulk_load_1d(dst + lane * kSlab, codes + (static_cast<size_t>(b) * p.Hk + kh) * kSlab, kSlab, bar);
     };
     const uint32_t at0 = static_cast<uint32_t>(piece / 8) * C::kChunkBytes;
     const int unit = piece % 8;
-    float ks = 0.f, vs[4];  // of token 32 w + lane, and of tokens 32 i + lane
-    uint32_t live = 0;      // of the warp's own 32 tokens
+    float4 ks, vs;      // of tokens 4 lane .. 4 lane + 3 of the tile (ks: the warp's own tokens only)
+    uint32_t live = 0;  // the warp's own 32 tokens
     auto fetch_scales = [&](int j, int blk) {
+      const int b = __shfl_sync(0xffffffffu, blk, lane / 4);
+      const size_t at = (static_cast<size_t>(max(b, 0)) * p.Hk + kh) * kQ8Page + 4 * (lane % 4);
+      ks = vs = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (b >= 0) vs = *reinterpret_cast<const float4 *>(p.vs + at);
+      if (b >= 0 && lane / 8 == w) ks = *reinterpret_cast<const float4 *>(p.ks + at);
+      live = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int b = __shfl_sync(0xffffffffu, blk, 2 * i + lane / 16);
-        const bool in = b >= 0 && (j0 + j) * kQ8Tok + 32 * i + lane < L;
-        const size_t at = (static_cast<size_t>(max(b, 0)) * p.Hk + kh) * kQ8Page + lane % 16;
-        vs[i] = in ? p.vs[at] : 0.f;
-        if (i == w) {
-          ks = in ? p.ks[at] : 0.f;
-          live = __ballot_sync(0xffffffffu, in);
-        }
+      for (int h = 0; h < 2; ++h) {
+        const int left = L - (j0 + j) * kQ8Tok - 32 * w - 16 * h;
+        const int bh = __shfl_sync(0xffffffffu, blk, 2 * w + h);
+        if (bh >= 0 && left > 0) live |= (left >= 16 ? 0xffffu : (1u << left) - 1u) << (16 * h);
       }
     };
     float F = 0x1p-126f;  // every warp finds the same F, tile by tile
     const float score_scale = p.scale_log2 * q8_inverse(q_unit);
-    // K of tile j and the tile's scales; returns f of this lane's token, twice
-    auto convert_k = [&](int j) -> uint32_t {
+    uint32_t f01 = 0, f23 = 0;  // f of tokens 4 lane ..
+    // the scales of tile j (fetched before): key scales, live tokens, F
+    auto publish_scales = [&](int j) {
       const int buf = j % C::kScaleBufs;
-      sKs[buf * kQ8Tok + 32 * w + lane] = ks * score_scale;
+      const int left = L - (j0 + j) * kQ8Tok - 4 * lane;  // tokens of this lane before the end
+      float v[4] = {vs.x, vs.y, vs.z, vs.w};
       float top = 0.f;  // the tile's largest finite vs
+      bool bad = false;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) top = fmaxf(top, vs[i] < INFINITY ? vs[i] : 0.f);
+      for (int c = 0; c < 4; ++c) {
+        if (c >= left) v[c] = 0.f;  // a slot past the end may hold anything
+        const bool fin = fabsf(v[c]) < INFINITY;
+        bad = bad || !fin;
+        top = fmaxf(top, fin ? v[c] : 0.f);
+      }
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
       if (top > F)  // the power of two above it
         F = __uint_as_float(min(((__float_as_uint(top) >> 23) & 0xffu) + 1u, 254u) << 23);
-      float mine = vs[0];
+      uint32_t badmask = 0;
+      if (__any_sync(0xffffffffu, bad)) {
 #pragma unroll
-      for (int i = 1; i < 4; ++i) mine = w == i ? vs[i] : mine;
-      const bool bad = !(fabsf(mine) < INFINITY);
-      const uint32_t badmask = __ballot_sync(0xffffffffu, bad);
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t m = (__ballot_sync(0xffffffffu, !(fabsf(v[c]) < INFINITY)) >> (8 * w)) & 0xffu;
+          for (int i = 0; i < 8; ++i) badmask |= ((m >> i) & 1u) << (4 * i + c);
+          if (!(fabsf(v[c]) < INFINITY)) v[c] = 0.f;
+        }
+      }
+      // (vs / F first: neither factor leaves the normal range)
+      const float inv = 1.f / F;
+      f01 = pack_fp16x2(v[0] * inv * q8_vtop<kType>(), v[1] * inv * q8_vtop<kType>());
+      f23 = pack_fp16x2(v[2] * inv * q8_vtop<kType>(), v[3] * inv * q8_vtop<kType>());
+      if (lane / 8 == w)
+        *reinterpret_cast<float4 *>(sKs + buf * kQ8Tok + 4 * lane) =
+            make_float4(ks.x * score_scale, ks.y * score_scale, ks.z * score_scale, ks.w * score_scale);
       if (lane == 0) {
         sLive[buf * 4 + w] = live;
         sBad[buf * 4 + w] = badmask;
         if (w == 0) sF[buf * 4] = F;
       }
-      uint8_t *kt = sK + (j & 1) * C::kTileBytes + at0;
-#pragma unroll
-      for (int k = 0; k < kLoads; ++k) {
-        const int row = 32 * w + k * kRowsPer + sub;
-        uint4 o;
-        q8_cvt4<kType>(kc[k].x, o.x, o.y);
-        q8_cvt4<kType>(kc[k].y, o.z, o.w);
-        *reinterpret_cast<uint4 *>(kt + q8_swz(row, unit)) = o;
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(sc_full + buf);
-        mbar_arrive(k_full + (j & 1));
-      }
-      const float fs = bad ? 0.f : mine / F * q8_vtop<kType>();  // vs / F first: neither factor overflows
-      return pack_fp16x2(fs, fs);
-    };
-    auto convert_v = [&](int j, uint32_t f2, uint32_t live_v) {
-      const bool all = live_v == 0xffffffffu;
-      uint8_t *vt = sV + (j & 1) * C::kTileBytes + at0;
-#pragma unroll
-      for (int k = 0; k < kLoads; ++k) {
-        const int row = 32 * w + k * kRowsPer + sub;
-        uint4 o;
-        const uint32_t f = __shfl_sync(0xffffffffu, f2, k * kRowsPer + sub);
-        // a slot that no token holds may have any bytes, and e4m3's NaN would pass through p = 0
-        if (kType == kQ8E4m3 && !all && !((live_v >> (k * kRowsPer + sub)) & 1)) vc[k] = make_uint2(0u, 0u);
-        q8_cvt4<kType>(vc[k].x, o.x, o.y);
-        q8_cvt4<kType>(vc[k].y, o.z, o.w);
-        o = make_uint4(mul_fp16x2(o.x, f), mul_fp16x2(o.y, f), mul_fp16x2(o.z, f), mul_fp16x2(o.w, f));
-        *reinterpret_cast<uint4 *>(vt + q8_swz(row, unit)) = o;
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(v_full + (j & 1));
     };
     // K runs one tile before V, as the products do
-    int blk_k = named(0, entry_of(0)), entry = entry_of(1), blk_v = blk_k;
+    int blk_k = named(0, entry_of(0)), entry = entry_of(1);
     if (nmax > 0) {
-      fetch(kcodes, blk_k, kc);
+      load_codes(p.k_codes, blk_k, kst, k_landed);
+      load_codes(p.v_codes, blk_k, vst, v_landed);
       fetch_scales(0, blk_k);
-      fetch(vcodes, blk_v, vc);
     }
-    // f and the live tokens of the next V tile, and of the tile whose K was made last
-    uint32_t f2_v = 0, f2_k = 0, live_v = 0, live_k = 0;
+    // f and the live tokens of the next V tile
+    uint32_t f01_v = 0, f23_v = 0, live_v = 0, live_k = 0;
     for (int j = -1; j < nmax; ++j) {
       const int jk = j + 1;
       int blk_next = blk_k;
-      f2_v = f2_k, live_v = live_k;
+      f01_v = f01, f23_v = f23, live_v = live_k;
+      uint2 c[kLoads];
       if (jk < nmax) {
-        if (jk >= 2 && !__all_sync(0xffffffffu, mbar_wait(k_free + (jk & 1), ((jk >> 1) - 1) & 1, abort_flag))) break;
-        live_k = live;
-        f2_k = convert_k(jk);
+        if (!__all_sync(0xffffffffu, mbar_wait(k_landed, jk & 1, abort_flag))) break;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+          c[i] = *reinterpret_cast<const uint2 *>(kst + (i * kRowsPer + sub) * HD + 8 * piece);
+        __syncwarp();  // the slot has been read: refill it
         blk_next = named(jk + 1, entry);
-        entry = entry_of(jk + 2);
-        if (jk + 1 < nmax) {
-          fetch(kcodes, blk_next, kc);
-          fetch_scales(jk + 1, blk_next);
+        if (jk + 1 < nmax) load_codes(p.k_codes, blk_next, kst, k_landed);
+        live_k = live;
+        if (jk >= 2 && !__all_sync(0xffffffffu, mbar_wait(k_free + (jk & 1), ((jk >> 1) - 1) & 1, abort_flag))) break;
+        publish_scales(jk);
+        uint8_t *kt = sK + (jk & 1) * C::kTileBytes + at0;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          uint4 o;
+          q8_cvt4<kType>(c[i].x, o.x, o.y);
+          q8_cvt4<kType>(c[i].y, o.z, o.w);
+          *reinterpret_cast<uint4 *>(kt + q8_swz(32 * w + i * kRowsPer + sub, unit)) = o;
         }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(sc_full + jk % C::kScaleBufs);
+          mbar_arrive(k_full + (jk & 1));
+        }
+        entry = entry_of(jk + 2);
+        if (jk + 1 < nmax) fetch_scales(jk + 1, blk_next);
       }
       if (j >= 0) {
+        if (!__all_sync(0xffffffffu, mbar_wait(v_landed, j & 1, abort_flag))) break;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+          c[i] = *reinterpret_cast<const uint2 *>(vst + (i * kRowsPer + sub) * HD + 8 * piece);
+        __syncwarp();
+        if (j + 1 < nmax) load_codes(p.v_codes, blk_k, vst, v_landed);  // (blk_k: still of tile j + 1)
         if (j >= 2 && !__all_sync(0xffffffffu, mbar_wait(v_free + (j & 1), ((j >> 1) - 1) & 1, abort_flag))) break;
-        convert_v(j, f2_v, live_v);
-        if (j + 1 < nmax) fetch(vcodes, blk_k, vc);  // (blk_k is still that of tile j + 1)
+        uint8_t *vt = sV + (j & 1) * C::kTileBytes + at0;
+        const bool all = live_v == 0xffffffffu;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int tok = i * kRowsPer + sub;  // of the warp's 32: f is with lane 8 w + tok / 4
+          const uint32_t pair = __shfl_sync(0xffffffffu, (i * kRowsPer) & 2 ? f23_v : f01_v, 8 * w + (i * kRowsPer) / 4);
+          // (four tokens to a load at d = 64: the upper two are the other pair's)
+          uint32_t fp = pair;
+          if (kRowsPer == 4) {
+            const uint32_t hi = __shfl_sync(0xffffffffu, f23_v, 8 * w + i);
+            fp = sub >= 2 ? hi : pair;
+          }
+          const uint32_t f = __byte_perm(fp, fp, (sub & 1) ? 0x3232 : 0x1010);
+          // a slot that no token holds may have any bytes, and e4m3's NaN would pass through p = 0
+          if (kType == kQ8E4m3 && !all && !((live_v >> tok) & 1)) c[i] = make_uint2(0u, 0u);
+          uint4 o;
+          q8_cvt4<kType>(c[i].x, o.x, o.y);
+          q8_cvt4<kType>(c[i].y, o.z, o.w);
+          o = make_uint4(mul_fp16x2(o.x, f), mul_fp16x2(o.y, f), mul_fp16x2(o.z, f), mul_fp16x2(o.w, f));
+          *reinterpret_cast<uint4 *>(vt + q8_swz(32 * w + tok, unit)) = o;
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_full + (j & 1));
       }
       blk_k = blk_next;
+    }
+    // abandoned: a copy still on its way lands before the CTA's shared memory goes away
+    if (*abort_flag) {
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 1000000) {
+      }
     }
   } else {
     // ------------------------------------------------------------------ softmax, products, epilogue
