@@ -1098,8 +1098,10 @@ constexpr int kQ8TargetCtas = 148 * 4 * 2;
 constexpr int kQ8MinPages = 32, kQ8MaxPages = 128;
 constexpr int kQ8WideSplit = 4;             // more chunks than this: a CTA joins each row
 constexpr int kQ8StreamRows = 16;           // up to here fa_q8_stream_kernel, beyond fa_q8_tile_kernel
-constexpr int kQ8TileTargetCtas = 148;      // one CTA per SM
-constexpr int kQ8TileMinPages = 16;         // two token tiles to a chunk
+// Many rows: chunks only as far as one CTA per SM goes (64 units of 4096 tokens took 111 us in three chunks
+// each, more than one round of CTAs, and 79 in two).
+constexpr int kQ8TileTargetCtas = 148;
+constexpr int kQ8TileMinPages = 16;         // four token tiles to a chunk
 
 bool q8_plan(int S, int Hq, int Hk, int Lq, int d, int max_blocks, Q8Plan *out) {
   if (S < 1 || Hq < 1 || Hk < 1 || Hq % Hk != 0 || Lq < 1 || max_blocks < 1) return false;
@@ -1115,11 +1117,11 @@ bool q8_plan(int S, int Hq, int Hk, int Lq, int d, int max_blocks, Q8Plan *out) 
   p.row_tiles = (p.R + tile_rows * p.nt - 1) / (tile_rows * p.nt);
   const long long units = static_cast<long long>(S) * Hk * p.row_tiles;
   const int target = p.tile ? kQ8TileTargetCtas : kQ8TargetCtas, least = p.tile ? kQ8TileMinPages : kQ8MinPages;
-  long long n = (target + units - 1) / units;
+  long long n = p.tile ? std::max(1LL, target / units) : (target + units - 1) / units;
   if (!p.tile) n = std::max<long long>(n, (max_blocks + kQ8MaxPages - 1) / kQ8MaxPages);
   n = std::min<long long>({n, (max_blocks + least - 1) / least, fa::kQ8MaxSplit});
   p.split_pages = static_cast<int>((max_blocks + n - 1) / n);
-  if (p.tile) p.split_pages = (p.split_pages + 7) / 8 * 8;  // whole tiles of 128 tokens
+  if (p.tile) p.split_pages = (p.split_pages + fa::kQ8TilePages - 1) / fa::kQ8TilePages * fa::kQ8TilePages;
   p.n_split = (max_blocks + p.split_pages - 1) / p.split_pages;
   p.rows = static_cast<size_t>(S) * Hq * Lq;
   if (units * p.n_split > INT_MAX) return false;
@@ -1177,15 +1179,6 @@ fa_status launch_q8_tile(DeviceInfo &dev, const fa::Q8Params &p, cudaStream_t s)
                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            static_cast<int>(C::kSmem));
       if (e != cudaSuccess) return launch_failed(e);
-      // the kernel's warps hand registers to one another: a build that launches with fewer would wait
-      // for them for ever
-      cudaFuncAttributes attr;
-      if ((e = cudaFuncGetAttributes(&attr, fa::fa_q8_tile_kernel<HD, kType, kTwo>)) != cudaSuccess)
-        return launch_failed(e);
-      if (attr.numRegs < fa::kQ8LaunchRegs) {
-        t_last_error = "fa_q8_tile_kernel was built with too few registers";
-        return FA_ERR_LAUNCH;
-      }
       dev.q8_attr[slot] = true;
     }
   }
@@ -1277,6 +1270,8 @@ fa_status q8_attention(const void *q, const void *k_pool, const void *v_pool, co
   p.n_split = plan.n_split;
   p.split_pages = plan.split_pages;
   p.causal = causal;
+  p.longest_first = plan.tile && S > 1 && S <= fa::kQ8SortSeqs &&
+                    static_cast<long long>(S) * Hk * plan.row_tiles * plan.n_split > dev->num_sms;
   p.o_f32 = o_dtype == FA_OUT_F32;
   p.scale_log2 = sc * 1.4426950408889634f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -50,6 +50,7 @@ struct Q8Params {
   int max_blocks, num_blocks;
   int row_tiles, n_split, split_pages;
   int causal, o_f32;
+  int longest_first;  // the tile kernel's CTAs take the sequences by length
   float scale_log2;
 };
 
@@ -58,10 +59,10 @@ struct Q8Params {
 // of the word and hi bytes 2, 3.  int8: c is fp16's 1024 + (c + 128) less 1152; lo takes bytes 0, 2
 // and hi bytes 1, 3.  kQ8Pick picks from two words what makes lo pair byte 0 (or 2) of the first with
 // that of the second, and hi byte 1 (or 3).
-__device__ __forceinline__ uint32_t q8_fp16_e4m3(uint32_t x) {  // the two codes in the low half
-  uint32_t r;
-  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(r) : "r"(x));
-  return r;
+__device__ __forceinline__ void q8_fp16_e4m3(uint32_t x, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
 }
 __device__ __forceinline__ uint32_t q8_fp16_int8(uint32_t x) {
   uint32_t r;
@@ -71,8 +72,7 @@ __device__ __forceinline__ uint32_t q8_fp16_int8(uint32_t x) {
 template <int kType>
 __device__ __forceinline__ void q8_cvt4(uint32_t x, uint32_t &lo, uint32_t &hi) {
   if constexpr (kType == kQ8E4m3) {
-    lo = q8_fp16_e4m3(x);
-    hi = q8_fp16_e4m3(x >> 16);
+    q8_fp16_e4m3(x, lo, hi);
   } else {
     lo = q8_fp16_int8(x);
     hi = q8_fp16_int8(x >> 8);

@@ -2,19 +2,20 @@
 // paged cache on the tcgen05 tensor cores.  The mathematics is that of fa_q8.cuh; only the values'
 // scales sit elsewhere.
 //
-// One CTA takes up to 256 of the R rows of one (sequence, key head) and a range of its 128-token
+// One CTA takes up to 256 of the R rows of one (sequence, key head) and a range of its 64-token
 // tiles.  Codes cannot feed a 16-bit product, so they are converted once per tile for all of the
 // CTA's rows:
-//   warps 0-3    one side: a thread holds a row (a TMEM lane).  Scores out of TMEM, p back over
-//                them; one thread issues the side's products
+//   warps 0-3    one side: a thread holds a row (a TMEM lane).  Scores out of TMEM, p back over them
 //   warps 4-7    the other side
-//   warps 8-11   codes: bulk copies into a staging slot, a tile ahead -> fp16 K and V tiles in the
-//                swizzled layout the tensor core reads; the tile's key scales and its live tokens
-// TMEM (512 columns): S0 [0,128)  S1 [128,256)  O0 [256,256+d)  O1 [256+d,256+2d).
-// With more than 128 rows the sides hold two row tiles; with fewer they share one row tile and take
-// the tiles of tokens in turn.  Either way one side's products run while the other's softmax does.
-// An issuer needs no warp of its own, since its side waits for what it issues; a thirteenth warp
-// would leave a thread 128 registers instead of 168.
+//   warps 8-11   codes -> fp16 K and V tiles in the swizzled layout the tensor core reads
+//   warps 12-13  products: one thread issues for each side
+//   warp  14     codes out of the pool by bulk copies, three tiles ahead
+//   warp  15     a tile's scales, live tokens and F
+// TMEM (512 columns): S [side][2] x 64, then O [side] x d.  With more than 128 rows the sides hold two
+// row tiles; with fewer they share one row tile and take the tiles of tokens in turn.  A side's S is
+// double, so Q K^T of the next tile and P V of the last run during its softmax.  (With 128-token tiles S
+// fills the same columns once: softmax, P V and Q K^T of a side then follow one another, 5800 cycles
+// per 128 tokens and two row tiles, QQQQ here.)
 //
 // Scales.  A key's scale multiplies its column of scores in fp32, read from shared memory by every
 // row: 32 broadcast 16-byte loads per row and tile, which cost the SM about half as much as the
@@ -42,8 +43,12 @@
 
 namespace fa {
 
-constexpr int kQ8TileThreads = 12 * 32;
-constexpr int kQ8Tok = 128;                 // tokens of a tile
+constexpr int kQ8TileThreads = 16 * 32;
+constexpr int kQ8Tok = 64;                  // tokens of a tile
+constexpr int kQ8TilePages = kQ8Tok / kQ8Page;
+constexpr int kQ8KBufs = 4;                 // K tiles in shared memory; V: 2, or 4 with one row tile
+constexpr int kQ8MostVBufs = 4;
+constexpr int kQ8CodeBufs = 3;              // tiles of codes on their way
 constexpr float kQ8TileMost = 15.f;         // log2 of the largest p: fp16 ends at 2^16
 constexpr float kQ8TileStart = 6.f;         // and after the reference has moved
 // f at the largest vs: e4m3 codes are at most 448, int8 codes 127
@@ -52,22 +57,29 @@ template <int kType> __device__ constexpr float q8_vtop() { return kType == kQ8E
 template <int HD>
 struct Q8TileCfg {
   static constexpr int kChunks = HD / 64;             // 64-feature (128-byte) swizzle chunks
-  static constexpr int kChunkBytes = 128 * 128;       // 128 rows x 128 bytes
-  static constexpr int kTileBytes = kChunks * kChunkBytes;
-  static constexpr int kScaleBufs = 4;
-  static constexpr int kBars = 38;
-  // Q (two row tiles), K and V (two tiles of tokens each), the codes of one tile of tokens
-  static constexpr int kCodeBytes = kQ8Tok * HD;
-  static constexpr size_t kNeed = 6 * kTileBytes + 2 * kCodeBytes + kScaleBufs * (kQ8Tok * 4 + 48) + kBars * 8 + 48;
+  static constexpr int kQChunk = 128 * 128;           // 128 rows x 128 bytes
+  static constexpr int kChunk = kQ8Tok * 128;         // 64 tokens x 128 bytes
+  static constexpr int kQBytes = kChunks * kQChunk;
+  static constexpr int kTileBytes = kChunks * kChunk;
+  static constexpr int kCodeBytes = kQ8Tok * HD;      // of K or V of one tile
+  static constexpr int kScaleBufs = 8;
+  static constexpr int kBars = 2 * kQ8KBufs + 2 * kQ8MostVBufs + 2 * kQ8CodeBufs + 2 * kScaleBufs + 4 + 4 + 4 + 2 + 2;
+  // Q (two row tiles, or one and two more V tiles in its place), K and V tiles, codes, scales (ks, f, live
+  // and bad tokens, F)
+  static_assert(kQBytes == 2 * kTileBytes, "two V tiles in the place of a row tile's Q");
+  static constexpr size_t kNeed = 1024 + 2 * kQBytes + (kQ8KBufs + 2) * kTileBytes +
+                                  2 * kQ8CodeBufs * kCodeBytes + kScaleBufs * (kQ8Tok * 8 + 32) + kBars * 8 + 48;
   static constexpr size_t kSmem = kNeed > 116 * 1024 ? kNeed : 116 * 1024;
-  static constexpr uint32_t kColS = 0, kColO = 256;
+  static constexpr uint32_t kColO = 256;  // S: [side][2] x 64 columns before it
   // fp16 operands: the type fields of A and B are 0
   static constexpr uint32_t kFp16 = ~((1u << 7) | (1u << 10));
-  static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, 0, 0) & kFp16;
+  static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, kQ8Tok, 0, 0) & kFp16;
   static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, HD, 0, 1) & kFp16;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static_assert(kSmem > 114 * 1024, "one CTA per SM: it takes all of the tensor memory");
 };
+
+constexpr int kQ8SortSeqs = 128;  // up to here every CTA ranks the sequences itself
 
 // Two bf16 features times a power of two, in fp16.
 __device__ __forceinline__ uint32_t q8_fp16_of(uint32_t bf16x2, float unit) {
@@ -85,41 +97,30 @@ __device__ __forceinline__ uint32_t mul_fp16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Registers a thread: 168 for all at launch (384 x 168 = 64512).  The softmax keeps 128 scores at once
-// and spilled around them (reloads from L2: 800 to 2400 cycles a tile), the conversion needs fewer:
-// 8 warps x 32 x 200 + 4 x 32 x 104 = 64512.
-constexpr int kQ8LaunchRegs = 168, kQ8SoftmaxRegs = 200, kQ8ConvertRegs = 104;
-static_assert(256 * kQ8SoftmaxRegs + 128 * kQ8ConvertRegs <= kQ8TileThreads * kQ8LaunchRegs,
-              "registers of the launch");
-template <int N>
-__device__ __forceinline__ void q8_regs_acquire() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void q8_regs_release() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
 // Keeps uses of registers that a tcgen05.ld fills behind the wait that precedes this.
 __device__ __forceinline__ void q8_pin(float (&x)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(x[i]));
 }
 
-// A row's 128 scores (TMEM) -> p in fp16 (TMEM, over the scores: token pairs in the first 64 columns) and
+// A row's 64 scores (TMEM) -> p in fp16 (TMEM, over the scores: token pairs in the first 32 columns) and
 // the sum of p.  k: the tokens that the row sees (kMasked: not all of them).  m and l are the row's
 // reference and sum so far; where the reference has to move, l is brought to the new one and `a` is
 // multiplied by what O needs.  All scores are in registers at once and the steps are kept apart
-// (arguments, largest, exponentials).
+// (arguments, largest, exponentials): taken a few at a time, each few wait for their loads of ks.
 template <bool kMasked>
-__device__ __forceinline__ float q8_weigh(uint32_t s_tmem, const uint32_t (&k)[4], const float *ks, float &m,
+__device__ __forceinline__ float q8_weigh(uint32_t s_tmem, const uint32_t (&k)[2], const float *ks, float &m,
                                           float &l, float &a) {
   const uint64_t neg2 = f2_pack(-m, -m);
-  float x[128];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) tmem_ld32(s_tmem + 32 * c, reinterpret_cast<uint32_t *>(x) + 32 * c);
+  float x[64];
+  tmem_ld32(s_tmem, reinterpret_cast<uint32_t *>(x));
+  tmem_ld32(s_tmem + 32, reinterpret_cast<uint32_t *>(x) + 32);
   tmem_wait_ld();
 #pragma unroll
-  for (int i = 0; i < 128; ++i) asm volatile("" : "+f"(x[i]));
+  for (int i = 0; i < 64; ++i) asm volatile("" : "+f"(x[i]));
   float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
+  for (int i = 0; i < 16; ++i) {
     const ulonglong2 f = reinterpret_cast<const ulonglong2 *>(ks)[i];
     f2_unpack(f2_fma(f2_pack(x[4 * i], x[4 * i + 1]), f.x, neg2), x[4 * i], x[4 * i + 1]);
     f2_unpack(f2_fma(f2_pack(x[4 * i + 2], x[4 * i + 3]), f.y, neg2), x[4 * i + 2], x[4 * i + 3]);
@@ -128,7 +129,8 @@ __device__ __forceinline__ float q8_weigh(uint32_t s_tmem, const uint32_t (&k)[4
       for (int e = 0; e < 4; ++e)
         x[4 * i + e] = (k[i / 8] >> (4 * (i % 8) + e)) & 1 ? x[4 * i + e] : -INFINITY;
     }
-    top[i % 4] = fmax3(top[i % 4], fmaxf(x[4 * i], x[4 * i + 1]), fmaxf(x[4 * i + 2], x[4 * i + 3]));
+    top[(2 * i) % 4] = fmax3(top[(2 * i) % 4], x[4 * i], x[4 * i + 1]);
+    top[(2 * i + 1) % 4] = fmax3(top[(2 * i + 1) % 4], x[4 * i + 2], x[4 * i + 3]);
   }
   const float t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
   // (a row that has seen nothing has l = 0; an infinite score makes its row NaN through inf - inf)
@@ -141,19 +143,18 @@ __device__ __forceinline__ float q8_weigh(uint32_t s_tmem, const uint32_t (&k)[4
     a *= r;
     const uint64_t d2 = f2_pack(d, d);
 #pragma unroll
-    for (int i = 0; i < 64; ++i)
+    for (int i = 0; i < 32; ++i)
       f2_unpack(f2_sub(f2_pack(x[2 * i], x[2 * i + 1]), d2), x[2 * i], x[2 * i + 1]);
   }
   uint64_t sum[2] = {0, 0};
-  uint32_t pk[64];
+  uint32_t pk[32];
 #pragma unroll
-  for (int i = 0; i < 64; ++i) {
+  for (int i = 0; i < 32; ++i) {
     const float p0 = ex2(x[2 * i]), p1 = ex2(x[2 * i + 1]);
     sum[i % 2] = f2_add(sum[i % 2], f2_pack(p0, p1));
     pk[i] = pack_fp16x2(p0, p1);
   }
   tmem_st32(s_tmem, pk);
-  tmem_st32(s_tmem + 32, pk + 32);
   tmem_wait_st();
   float u, v;
   f2_unpack(f2_add(sum[0], sum[1]), u, v);
@@ -187,25 +188,24 @@ __device__ __forceinline__ int q8_tiles(const Q8Params &p, int L, int r0, int r1
   return (L - p.T + t) / kQ8Tok + 1;
 }
 
-// S (TMEM) = Q K^T: both K-major in 64-feature swizzled chunks.
+// S (TMEM, 64 columns) = Q K^T: both K-major in 64-feature swizzled chunks.
 template <int HD>
 __device__ __forceinline__ void q8_issue_qk(uint32_t d_tmem, const uint8_t *q, const uint8_t *k) {
   using C = Q8TileCfg<HD>;
   const uint64_t qd = smem_desc_sw128(smem_u32(q), 16, 1024), kd = smem_desc_sw128(smem_u32(k), 16, 1024);
 #pragma unroll
-  for (int kk = 0; kk < HD / 16; ++kk) {
-    const uint64_t off = static_cast<uint64_t>(((kk / 4) * C::kChunkBytes + (kk % 4) * 32) >> 4);
-    umma_ss(d_tmem, qd + off, kd + off, C::kIdescQK, kk > 0 ? 1u : 0u);
-  }
+  for (int kk = 0; kk < HD / 16; ++kk)
+    umma_ss(d_tmem, qd + static_cast<uint64_t>(((kk / 4) * C::kQChunk + (kk % 4) * 32) >> 4),
+            kd + static_cast<uint64_t>(((kk / 4) * C::kChunk + (kk % 4) * 32) >> 4), C::kIdescQK, kk > 0 ? 1u : 0u);
 }
 
 // O (TMEM) (+)= P V: P from TMEM (8 columns per 16 tokens), V MN-major (chunks of 64 features, 8-token
-// groups).  P is not staged in shared memory: a 128 x 128 x 16 product with both operands there reads
-// the 128 bytes a cycle that shared memory has, and P's stores would come on top.
+// groups).  P is not staged in shared memory: a product with both operands there reads the 128
+// bytes a cycle that shared memory has, and P's stores would come on top.
 template <int HD>
 __device__ __forceinline__ void q8_issue_pv(uint32_t d_tmem, uint32_t p_tmem, const uint8_t *v, bool accumulate) {
   using C = Q8TileCfg<HD>;
-  const uint64_t vd = smem_desc_sw128(smem_u32(v), C::kChunkBytes, 1024);
+  const uint64_t vd = smem_desc_sw128(smem_u32(v), C::kChunk, 1024);
 #pragma unroll
   for (int kk = 0; kk < kQ8Tok / 16; ++kk)
     umma_ts(d_tmem, p_tmem + 8 * kk, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), C::kIdescPV,
@@ -221,28 +221,30 @@ __device__ __forceinline__ void q8_sides_barrier() { asm volatile("bar.sync 1, 2
 template <int HD, int kType, bool kTwo>
 __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8Params p) {
   using C = Q8TileCfg<HD>;
-  extern __shared__ __align__(1024) uint8_t q8_tile_smem[];  // no room for slack: checked below
-  uint8_t *sQ = q8_tile_smem;             // [row tile]
-  uint8_t *sK = sQ + 2 * C::kTileBytes;   // tile j of tokens is in [j & 1]
-  uint8_t *sV = sK + 2 * C::kTileBytes;
-  uint8_t *sKc = sV + 2 * C::kTileBytes;  // codes of K as they land, a quarter of the tile to a warp
-  uint8_t *sVc = sKc + C::kCodeBytes;     // and of V
-  float *sKs = reinterpret_cast<float *>(sVc + C::kCodeBytes);  // [buffer][token]: ks scale log2(e)
-  uint32_t *sLive = reinterpret_cast<uint32_t *>(sKs + C::kScaleBufs * kQ8Tok);  // [buffer][4]
-  uint32_t *sBad = sLive + C::kScaleBufs * 4;  // [buffer][4]: live tokens whose vs is not finite
-  float *sF = reinterpret_cast<float *>(sBad + C::kScaleBufs * 4);  // [buffer][4]: F of the tile
-  uint64_t *bars = reinterpret_cast<uint64_t *>(sF + C::kScaleBufs * 4);
-  // Barriers of tile j are [j & 1], as its buffers are, so that a side that waits for every other tile of
-  // tokens sees each phase of its own.  A buffer is freed by an arrival from each issuer that reads it.
-  uint64_t *k_full = bars, *v_full = bars + 2, *k_free = bars + 4, *v_free = bars + 6;  // [2]
-  uint64_t *sc_full = bars + 8;                 // [4]
-  uint64_t *s_full = bars + 12;                 // [side]
-  uint64_t *p_full = bars + 14;                 // [side]
-  uint64_t *pv_done = bars + 16;                // [side]
-  uint64_t *drain = bars + 18;                  // [side] every product of an issuer has completed
-  uint64_t *q_full = bars + 20;                 // [row tile]
-  uint64_t *turn = bars + 22;                   // [side][warp]
-  uint64_t *landed = bars + 30;                 // [K, V][converter warp]
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  constexpr int NK = kQ8KBufs, NV = kTwo ? 2 : kQ8MostVBufs, NC = kQ8CodeBufs, NS = C::kScaleBufs;
+  uint8_t *sQ = smem;                          // [row tile]
+  uint8_t *sK = sQ + (kTwo ? 2 : 1) * C::kQBytes;  // tile j of tokens is in [j % NK]
+  uint8_t *sV = sK + NK * C::kTileBytes;       // [j % NV]
+  uint8_t *sC = sV + NV * C::kTileBytes;       // [j % NC]: its codes, K then V, as they lie in the pool
+  float *sKs = reinterpret_cast<float *>(sC + 2 * NC * C::kCodeBytes);  // [j % NS][token]: ks scale log2(e)
+  uint32_t *sFt = reinterpret_cast<uint32_t *>(sKs + NS * kQ8Tok);      // [j % NS][token]: f in fp16, twice
+  uint16_t *sLive = reinterpret_cast<uint16_t *>(sFt + NS * kQ8Tok);    // [j % NS][page]
+  uint16_t *sBad = sLive + NS * 4;             // [j % NS][page]: live tokens whose vs is not finite
+  float *sF = reinterpret_cast<float *>(sBad + NS * 4);  // [j % NS][4]: F of the tile
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sF + NS * 4);
+  // Barriers are indexed as the buffers they guard; the counts are even (or every reader takes every
+  // tile), so that a side that waits for every other tile of tokens sees each phase of its own.  A
+  // buffer is freed by an arrival from each issuer (or converter warp) that reads it.
+  uint64_t *k_full = bars, *k_free = k_full + NK, *v_full = k_free + NK, *v_free = v_full + NV;
+  uint64_t *code_full = v_free + NV, *code_free = code_full + NC;
+  uint64_t *sc_full = code_free + NC, *sc_free = sc_full + NS;
+  uint64_t *s_full = sc_free + NS;              // [side][2]: the side's tile i uses [i & 1]
+  uint64_t *p_full = s_full + 4;                // [side][2]
+  uint64_t *pv_done = p_full + 4;               // [side][2]
+  uint64_t *drain = pv_done + 4;                // [side] every product of an issuer has completed
+  uint64_t *q_full = drain + 2;                 // [row tile]
   float *sTop = reinterpret_cast<float *>(bars + C::kBars);  // [8]: the warps' largest |q|
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sTop + 8);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -252,11 +254,28 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
   u /= p.n_split;
   const int group = u % p.row_tiles;
   u /= p.row_tiles;
-  const int kh = u % p.Hk, s = u / p.Hk;
+  const int kh = u % p.Hk;
+  int s = u / p.Hk;
+  if (p.longest_first) {
+    // More than one round of CTAs, which start in the order of their index: the s-th longest sequence
+    // (ties by index) instead of the s-th, so that the last round is short (32 sequences of 512 to 4096
+    // tokens, 8 heads: 175 us in the batch's order, QQQQ so)
+    __shared__ int lens[kQ8SortSeqs], found;
+    if (threadIdx.x < p.S) lens[threadIdx.x] = q8_len(p, threadIdx.x);
+    __syncthreads();
+    if (threadIdx.x < p.S) {
+      const int mine = lens[threadIdx.x];
+      int rank = 0;
+      for (int i = 0; i < p.S; ++i) rank += lens[i] > mine || (lens[i] == mine && i < static_cast<int>(threadIdx.x));
+      if (rank == s) found = threadIdx.x;
+    }
+    __syncthreads();
+    s = found;
+  }
   const int row0 = group * (kTwo ? 256 : 128);
   const size_t row_base = (static_cast<size_t>(s) * p.Hk + kh) * p.R;
   const int L = q8_len(p, s);
-  const int tiles_per_split = p.split_pages / (kQ8Tok / kQ8Page);
+  const int tiles_per_split = p.split_pages / kQ8TilePages;
   const int j0 = split * tiles_per_split;
   if (p.n_split > 1 && j0 * kQ8Tok >= L) return;  // past the sequence's end: the combine skips it
   // tiles of tokens that each side takes, and that the CTA takes in all
@@ -269,27 +288,23 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
   }
   const int nmax = max(n[0], n[1]);
   if (!kTwo) n[0] = (nmax + 1) / 2, n[1] = nmax / 2;
-  const int both = min(n[0], n[1]);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (smem_u32(q8_tile_smem) & 1023u) {  // the swizzled tiles need it; the launch gives it
-    if (threadIdx.x == 0) atomicExch(&g_device_status, 4 /* FA_ERR_LAUNCH */);
-    return;
-  }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(k_full + i, 4);
-      mbar_init(v_full + i, 4);
-      mbar_init(k_free + i, kTwo ? 2 : 1);
-      mbar_init(v_free + i, kTwo ? 2 : 1);
+    for (int i = 0; i < NK; ++i) mbar_init(k_full + i, 4), mbar_init(k_free + i, kTwo ? 2 : 1);
+    for (int i = 0; i < NV; ++i) mbar_init(v_full + i, 4), mbar_init(v_free + i, kTwo ? 2 : 1);
+    for (int i = 0; i < NC; ++i) mbar_init(code_full + i, 1), mbar_init(code_free + i, 4);
+    // read by the four converter warps and by the softmax warps of each side
+    for (int i = 0; i < NS; ++i) mbar_init(sc_full + i, 1), mbar_init(sc_free + i, kTwo ? 12 : 8);
+    for (int i = 0; i < 4; ++i) {
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 4);
       mbar_init(pv_done + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(drain + i, 1);
       mbar_init(q_full + i, 4);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(sc_full + i, 4);
-    for (int i = 0; i < 8; ++i) mbar_init(turn + i, 1), mbar_init(landed + i, 1);
     *abort_flag = 0;
     if (L != p.lens[s] && p.lens[s] > 0) atomicExch(&g_device_status, 1 /* FA_ERR_INVALID_ARG */);
     fence_mbar_init();
@@ -322,190 +337,237 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
   for (int i = 1; i < 8; ++i) q_top = fmaxf(q_top, sTop[i]);
   const float q_unit = q8_q_unit(q_top);
 
-  if (warp >= 8) {
-    // ------------------------------------------------------------------ codes -> 16-bit tiles
-    q8_regs_release<kQ8ConvertRegs>();
-    const int w = warp - 8;              // tokens 32 w .. 32 w + 31 of a tile: pages 2 w, 2 w + 1
+  if (warp >= 8 && warp < 12) {
+    // ------------------------------------------------------------------ codes -> fp16 tiles
+    const int w = warp - 8;              // page w of a tile: tokens 16 w .. 16 w + 15
     constexpr int kPieces = HD / 8;      // 8-code pieces of a token
     constexpr int kRowsPer = 32 / kPieces;  // tokens that a warp-wide load covers
-    constexpr int kLoads = 32 / kRowsPer;
-    constexpr uint32_t kSlab = kQ8Page * HD;  // a page of one head: contiguous in the pool
+    constexpr int kLoads = kQ8Page / kRowsPer;
+    constexpr int kSlab = kQ8Page * HD;
     const int piece = lane % kPieces, sub = lane / kPieces;
-    const int32_t *trow = p.table + static_cast<size_t>(s) * p.max_blocks;
-    const int nblk = (L + kQ8Page - 1) / kQ8Page;
-    // lane i < 8: the table's entry for page i of tile j; not looked at before it is needed (named)
-    auto entry_of = [&](int j) -> int {
-      const int page = (j0 + j) * (kQ8Tok / kQ8Page) + lane;
-      return (lane < kQ8Tok / kQ8Page && j < nmax && page < nblk) ? trow[page] : -1;
-    };
-    auto named = [&](int j, int b) -> int {  // -1 for a page that the table does not name
-      const int page = (j0 + j) * (kQ8Tok / kQ8Page) + lane;
-      if (b >= 0 && b < p.num_blocks) return b;
-      if (lane < kQ8Tok / kQ8Page && j < nmax && page < nblk)
-        atomicExch(&g_device_status, 1 /* FA_ERR_INVALID_ARG: the page is left out */);
-      return -1;
-    };
-    uint8_t *kst = sKc + 2 * w * kSlab, *vst = sVc + 2 * w * kSlab;
-    uint64_t *k_landed = landed + w, *v_landed = landed + 4 + w;
-    // the warp's two pages of a tile into its staging slot: lanes 0 and 1, a page each; one that is left
-    // out is not loaded (its tokens are not live)
-    auto load_codes = [&](const uint8_t *codes, int blk, uint8_t *dst, uint64_t *bar) {
-      const int b = __shfl_sync(0xffffffffu, blk, 2 * w + (lane & 1));
-      const uint32_t both_named = __ballot_sync(0xffffffffu, b >= 0) & 3u;
-      if (lane == 0) {
-        if (both_named) mbar_arrive_expect_tx(bar, (both_named == 3u ? 2 : 1) * kSlab);
-        else mbar_arrive(bar);
-      }
-      if (lane < 2 && b >= 0)
-        bulk_load_1d(dst + lane * kSlab, codes + (static_cast<size_t>(b) * p.Hk + kh) * kSlab, kSlab, bar);
-    };
-    const uint32_t at0 = static_cast<uint32_t>(piece / 8) * C::kChunkBytes;
+    const uint32_t at0 = static_cast<uint32_t>(piece / 8) * C::kChunk;
     const int unit = piece % 8;
-    float4 ks, vs;      // of tokens 4 lane .. 4 lane + 3 of the tile (ks: the warp's own tokens only)
-    uint32_t live = 0;  // the warp's own 32 tokens
-    auto fetch_scales = [&](int j, int blk) {
-      const int b = __shfl_sync(0xffffffffu, blk, lane / 4);
-      const size_t at = (static_cast<size_t>(max(b, 0)) * p.Hk + kh) * kQ8Page + 4 * (lane % 4);
-      ks = vs = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (b >= 0) vs = *reinterpret_cast<const float4 *>(p.vs + at);
-      if (b >= 0 && lane / 8 == w) ks = *reinterpret_cast<const float4 *>(p.ks + at);
-      live = 0;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int left = L - (j0 + j) * kQ8Tok - 32 * w - 16 * h;
-        const int bh = __shfl_sync(0xffffffffu, blk, 2 * w + h);
-        if (bh >= 0 && left > 0) live |= (left >= 16 ? 0xffffu : (1u << left) - 1u) << (16 * h);
-      }
-    };
-    float F = 0x1p-126f;  // every warp finds the same F, tile by tile
-    const float score_scale = p.scale_log2 * q8_inverse(q_unit);
-    uint32_t f01 = 0, f23 = 0;  // f of tokens 4 lane ..
-    // the scales of tile j (fetched before): key scales, live tokens, F
-    auto publish_scales = [&](int j) {
-      const int buf = j % C::kScaleBufs;
-      const int left = L - (j0 + j) * kQ8Tok - 4 * lane;  // tokens of this lane before the end
-      float v[4] = {vs.x, vs.y, vs.z, vs.w};
-      float top = 0.f;  // the tile's largest finite vs
-      bool bad = false;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (c >= left) v[c] = 0.f;  // a slot past the end may hold anything
-        const bool fin = fabsf(v[c]) < INFINITY;
-        bad = bad || !fin;
-        top = fmaxf(top, fin ? v[c] : 0.f);
-      }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-      if (top > F)  // the power of two above it
-        F = __uint_as_float(min(((__float_as_uint(top) >> 23) & 0xffu) + 1u, 254u) << 23);
-      uint32_t badmask = 0;
-      if (__any_sync(0xffffffffu, bad)) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t m = (__ballot_sync(0xffffffffu, !(fabsf(v[c]) < INFINITY)) >> (8 * w)) & 0xffu;
-          for (int i = 0; i < 8; ++i) badmask |= ((m >> i) & 1u) << (4 * i + c);
-          if (!(fabsf(v[c]) < INFINITY)) v[c] = 0.f;
-        }
-      }
-      // (vs / F first: neither factor leaves the normal range)
-      const float inv = 1.f / F;
-      f01 = pack_fp16x2(v[0] * inv * q8_vtop<kType>(), v[1] * inv * q8_vtop<kType>());
-      f23 = pack_fp16x2(v[2] * inv * q8_vtop<kType>(), v[3] * inv * q8_vtop<kType>());
-      if (lane / 8 == w)
-        *reinterpret_cast<float4 *>(sKs + buf * kQ8Tok + 4 * lane) =
-            make_float4(ks.x * score_scale, ks.y * score_scale, ks.z * score_scale, ks.w * score_scale);
-      if (lane == 0) {
-        sLive[buf * 4 + w] = live;
-        sBad[buf * 4 + w] = badmask;
-        if (w == 0) sF[buf * 4] = F;
-      }
-    };
+    const uint8_t *mine_c = sC + w * kSlab + sub * HD + 8 * piece;
     // K runs one tile before V, as the products do
-    int blk_k = named(0, entry_of(0)), entry = entry_of(1);
-    if (nmax > 0) {
-      load_codes(p.k_codes, blk_k, kst, k_landed);
-      load_codes(p.v_codes, blk_k, vst, v_landed);
-      fetch_scales(0, blk_k);
-    }
-    // f and the live tokens of the next V tile
-    uint32_t f01_v = 0, f23_v = 0, live_v = 0, live_k = 0;
     for (int j = -1; j < nmax; ++j) {
       const int jk = j + 1;
-      int blk_next = blk_k;
-      f01_v = f01, f23_v = f23, live_v = live_k;
       uint2 c[kLoads];
       if (jk < nmax) {
-        if (!__all_sync(0xffffffffu, mbar_wait(k_landed, jk & 1, abort_flag))) break;
+        if (!__all_sync(0xffffffffu, mbar_wait(code_full + jk % NC, (jk / NC) & 1, abort_flag) &&
+                                         (jk < NK || mbar_wait(k_free + jk % NK, (jk / NK - 1) & 1, abort_flag)))) break;
+        const uint8_t *src = mine_c + 2 * (jk % NC) * C::kCodeBytes;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-          c[i] = *reinterpret_cast<const uint2 *>(kst + (i * kRowsPer + sub) * HD + 8 * piece);
-        __syncwarp();  // the slot has been read: refill it
-        blk_next = named(jk + 1, entry);
-        if (jk + 1 < nmax) load_codes(p.k_codes, blk_next, kst, k_landed);
-        live_k = live;
-        if (jk >= 2 && !__all_sync(0xffffffffu, mbar_wait(k_free + (jk & 1), ((jk >> 1) - 1) & 1, abort_flag))) break;
-        publish_scales(jk);
-        uint8_t *kt = sK + (jk & 1) * C::kTileBytes + at0;
+        for (int i = 0; i < kLoads; ++i) c[i] = *reinterpret_cast<const uint2 *>(src + i * kRowsPer * HD);
+        uint8_t *kt = sK + (jk % NK) * C::kTileBytes + at0;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
           uint4 o;
           q8_cvt4<kType>(c[i].x, o.x, o.y);
           q8_cvt4<kType>(c[i].y, o.z, o.w);
-          *reinterpret_cast<uint4 *>(kt + q8_swz(32 * w + i * kRowsPer + sub, unit)) = o;
+          *reinterpret_cast<uint4 *>(kt + q8_swz(16 * w + i * kRowsPer + sub, unit)) = o;
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(sc_full + jk % C::kScaleBufs);
-          mbar_arrive(k_full + (jk & 1));
-        }
-        entry = entry_of(jk + 2);
-        if (jk + 1 < nmax) fetch_scales(jk + 1, blk_next);
+        if (lane == 0) mbar_arrive(k_full + jk % NK);
       }
       if (j >= 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait(v_landed, j & 1, abort_flag))) break;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-          c[i] = *reinterpret_cast<const uint2 *>(vst + (i * kRowsPer + sub) * HD + 8 * piece);
-        __syncwarp();
-        if (j + 1 < nmax) load_codes(p.v_codes, blk_k, vst, v_landed);  // (blk_k: still of tile j + 1)
-        if (j >= 2 && !__all_sync(0xffffffffu, mbar_wait(v_free + (j & 1), ((j >> 1) - 1) & 1, abort_flag))) break;
-        uint8_t *vt = sV + (j & 1) * C::kTileBytes + at0;
-        const bool all = live_v == 0xffffffffu;
+        const int buf = j % NS;
+        if (!__all_sync(0xffffffffu, mbar_wait(sc_full + buf, (j / NS) & 1, abort_flag) &&
+                                         (j < NV || mbar_wait(v_free + j % NV, (j / NV - 1) & 1, abort_flag)))) break;
+        const uint8_t *src = mine_c + (2 * (j % NC) + 1) * C::kCodeBytes;
+        uint32_t f[kLoads];
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-          const int tok = i * kRowsPer + sub;  // of the warp's 32: f is with lane 8 w + tok / 4
-          const uint32_t pair = __shfl_sync(0xffffffffu, (i * kRowsPer) & 2 ? f23_v : f01_v, 8 * w + (i * kRowsPer) / 4);
-          // (four tokens to a load at d = 64: the upper two are the other pair's)
-          uint32_t fp = pair;
-          if (kRowsPer == 4) {
-            const uint32_t hi = __shfl_sync(0xffffffffu, f23_v, 8 * w + i);
-            fp = sub >= 2 ? hi : pair;
-          }
-          const uint32_t f = __byte_perm(fp, fp, (sub & 1) ? 0x3232 : 0x1010);
-          // a slot that no token holds may have any bytes, and e4m3's NaN would pass through p = 0
-          if (kType == kQ8E4m3 && !all && !((live_v >> tok) & 1)) c[i] = make_uint2(0u, 0u);
+          c[i] = *reinterpret_cast<const uint2 *>(src + i * kRowsPer * HD);
+          f[i] = sFt[buf * kQ8Tok + 16 * w + i * kRowsPer + sub];
+        }
+        const uint32_t live = sLive[buf * 4 + w];
+        __syncwarp();  // the tile's codes and scales have been read
+        if (lane == 0) mbar_arrive(code_free + j % NC), mbar_arrive(sc_free + buf);
+        // a slot that no token holds may have any bytes, and e4m3's NaN would pass through p = 0
+        if (kType == kQ8E4m3 && live != 0xffffu) {
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i)
+            if (!((live >> (i * kRowsPer + sub)) & 1)) c[i] = make_uint2(0u, 0u);
+        }
+        uint8_t *vt = sV + (j % NV) * C::kTileBytes + at0;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
           uint4 o;
           q8_cvt4<kType>(c[i].x, o.x, o.y);
           q8_cvt4<kType>(c[i].y, o.z, o.w);
-          o = make_uint4(mul_fp16x2(o.x, f), mul_fp16x2(o.y, f), mul_fp16x2(o.z, f), mul_fp16x2(o.w, f));
-          *reinterpret_cast<uint4 *>(vt + q8_swz(32 * w + tok, unit)) = o;
+          o = make_uint4(mul_fp16x2(o.x, f[i]), mul_fp16x2(o.y, f[i]), mul_fp16x2(o.z, f[i]), mul_fp16x2(o.w, f[i]));
+          *reinterpret_cast<uint4 *>(vt + q8_swz(16 * w + i * kRowsPer + sub, unit)) = o;
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(v_full + (j & 1));
+        if (lane == 0) mbar_arrive(v_full + j % NV);
       }
-      blk_k = blk_next;
     }
-    // abandoned: a copy still on its way lands before the CTA's shared memory goes away
-    if (*abort_flag) {
-      const uint64_t t0 = globaltimer_ns();
-      while (globaltimer_ns() - t0 < 1000000) {
+  } else if (warp >= 14) {
+    // ------------------------------------------------------------------ codes and scales of the tiles
+    const int32_t *trow = p.table + static_cast<size_t>(s) * p.max_blocks;
+    const int nblk = (L + kQ8Page - 1) / kQ8Page;
+    // lane i < 4: the table's entry for page i of tile j; not looked at before it is needed (named)
+    auto has_page = [&](int j) {
+      return lane < kQ8TilePages && j < nmax && (j0 + j) * kQ8TilePages + lane < nblk;
+    };
+    auto entry_of = [&](int j) -> int { return has_page(j) ? trow[(j0 + j) * kQ8TilePages + lane] : -1; };
+    auto named = [&](int j, int b) -> int {  // -1 for a page that the table does not name
+      if (b >= 0 && b < p.num_blocks) return b;
+      if (has_page(j)) atomicExch(&g_device_status, 1 /* FA_ERR_INVALID_ARG: the page is left out */);
+      return -1;
+    };
+    if (warp == 14) {
+      // codes: lanes 0-3 a page of K each, lanes 4-7 of V; a page left out is not loaded (its tokens are
+      // not live)
+      constexpr uint32_t kSlab = kQ8Page * HD;  // a page of one head: contiguous in the pool
+      int entry = entry_of(0);
+      for (int j = 0; j < nmax; ++j) {
+        const int blk = named(j, entry);
+        entry = entry_of(j + 1);
+        if (j >= NC && !__all_sync(0xffffffffu, mbar_wait(code_free + j % NC, (j / NC - 1) & 1, abort_flag))) break;
+        const int pages = __popc(__ballot_sync(0xffffffffu, blk >= 0) & 0xfu);
+        if (lane == 0) {
+          if (pages > 0) mbar_arrive_expect_tx(code_full + j % NC, 2 * pages * kSlab);
+          else mbar_arrive(code_full + j % NC);
+        }
+        __syncwarp();
+        const int b = __shfl_sync(0xffffffffu, blk, lane & 3), is_v = (lane >> 2) & 1;
+        if (lane < 8 && b >= 0)
+          bulk_load_1d(sC + (2 * (j % NC) + is_v) * C::kCodeBytes + (lane & 3) * kSlab,
+                       (is_v ? p.v_codes : p.k_codes) + (static_cast<size_t>(b) * p.Hk + kh) * kSlab, kSlab,
+                       code_full + j % NC);
       }
+      // abandoned: a copy still on its way lands before the CTA's shared memory goes away
+      if (*abort_flag) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000) {
+        }
+      }
+    } else {
+      // scales: lane i < 16 has tokens 4 i .. 4 i + 3 of the tile
+      const float score_scale = p.scale_log2 * q8_inverse(q_unit);
+      float F = 0x1p-126f;
+      float4 ks, vs;
+      int blk = named(0, entry_of(0)), entry = entry_of(1);
+      auto fetch = [&](int b4) {
+        const int b = __shfl_sync(0xffffffffu, b4, (lane / 4) & 3);
+        const size_t at = (static_cast<size_t>(max(b, 0)) * p.Hk + kh) * kQ8Page + 4 * (lane % 4);
+        ks = vs = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (b >= 0 && lane < 16) {
+          ks = *reinterpret_cast<const float4 *>(p.ks + at);
+          vs = *reinterpret_cast<const float4 *>(p.vs + at);
+        }
+      };
+      fetch(blk);
+      for (int j = 0; j < nmax; ++j) {
+        const int buf = j % NS;
+        const int left4 = L - (j0 + j) * kQ8Tok - 4 * lane;  // tokens from this lane's on, before the end
+        float v[4] = {vs.x, vs.y, vs.z, vs.w};
+        const float4 k4 = make_float4(ks.x * score_scale, ks.y * score_scale, ks.z * score_scale, ks.w * score_scale);
+        const int left = L - (j0 + j) * kQ8Tok - kQ8Page * lane;  // and for lane i < 4, of page i
+        const uint32_t live = blk < 0 || left <= 0 ? 0u : left >= 16 ? 0xffffu : (1u << left) - 1u;
+        float top = 0.f;  // the tile's largest finite vs
+        bool bad = false;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c >= left4) v[c] = 0.f;  // a slot past the end may hold anything
+          const bool fin = fabsf(v[c]) < INFINITY;
+          bad = bad || !fin;
+          top = fmaxf(top, fin ? v[c] : 0.f);
+        }
+        blk = named(j + 1, entry);
+        entry = entry_of(j + 2);
+        fetch(blk);  // of tile j + 1
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        top = __shfl_sync(0xffffffffu, top, 0);
+        if (top > F)  // the power of two above it
+          F = __uint_as_float(min(((__float_as_uint(top) >> 23) & 0xffu) + 1u, 254u) << 23);
+        uint32_t badmask = 0;  // of page `lane`
+        if (__any_sync(0xffffffffu, bad)) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t m = (__ballot_sync(0xffffffffu, !(fabsf(v[c]) < INFINITY)) >> (4 * (lane & 3))) & 0xfu;
+            for (int i = 0; i < 4; ++i) badmask |= ((m >> i) & 1u) << (4 * i + c);
+            if (!(fabsf(v[c]) < INFINITY)) v[c] = 0.f;
+          }
+        }
+        // (vs / F first: neither factor leaves the normal range)
+        const float inv = q8_inverse(F);
+        uint32_t f[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float x = v[c] * inv * q8_vtop<kType>();
+          f[c] = pack_fp16x2(x, x);
+        }
+        // A wait by parity must not be overtaken by a phase: the barrier's next one needs these scales.
+        // (k_free of tile j - 4 would say as much, but Q K^T of tile j can complete before this wait.)
+        if (j >= NS && !__all_sync(0xffffffffu, mbar_wait(sc_free + buf, (j / NS - 1) & 1, abort_flag))) break;
+        if (lane < 16) {
+          *reinterpret_cast<float4 *>(sKs + buf * kQ8Tok + 4 * lane) = k4;
+          *reinterpret_cast<uint4 *>(sFt + buf * kQ8Tok + 4 * lane) = make_uint4(f[0], f[1], f[2], f[3]);
+        }
+        if (lane < kQ8TilePages) {
+          sLive[buf * 4 + lane] = static_cast<uint16_t>(live);
+          sBad[buf * 4 + lane] = static_cast<uint16_t>(badmask);
+        }
+        if (lane == 0) sF[buf * 4] = F;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sc_full + buf);
+      }
+    }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------------ products: a thread per side
+    const int side = warp - 12;
+    if (side < 2 && lane == 0) {
+      const int cnt = n[side], steps = kTwo ? nmax : cnt, rtile = kTwo ? side : 0;
+      const uint32_t tS = tmem + 128 * side, tO = tmem + C::kColO + HD * side;
+      // S of the side's tile i; with two row tiles an issuer also takes part for the tiles of tokens
+      // that only the other one visits, by freeing them
+      auto scores = [&](int i) -> bool {
+        if (i >= steps) return true;
+        const int j = kTwo ? i : 2 * i + side;
+        if (!mbar_wait(k_full + j % NK, (j / NK) & 1, abort_flag)) return false;
+        if (i < cnt) {
+          tc_fence_after();
+          q8_issue_qk<HD>(tS + 64 * (i & 1), sQ + rtile * C::kQBytes, sK + (j % NK) * C::kTileBytes);
+          umma_commit(s_full + 2 * side + (i & 1));
+          umma_commit(k_free + j % NK);
+        } else {
+          mbar_arrive(k_free + j % NK);
+        }
+        return true;
+      };
+      bool ok = (cnt == 0 || mbar_wait(q_full + rtile, 0, abort_flag)) && scores(0) && scores(1);
+      for (int i = 0; ok && i < steps; ++i) {
+        const int j = kTwo ? i : 2 * i + side;
+        ok = mbar_wait(v_full + j % NV, (j / NV) & 1, abort_flag);
+        if (!ok) break;
+        if (i < cnt) {
+          const int b = 2 * side + (i & 1);
+          ok = mbar_wait(p_full + b, (i >> 1) & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          q8_issue_pv<HD>(tO, tS + 64 * (i & 1), sV + (j % NV) * C::kTileBytes, i > 0);
+          umma_commit(pv_done + b);
+          umma_commit(v_free + j % NV);
+          // P lies over S: tile i + 2's scores may be written once this product has read it
+          ok = i + 2 >= cnt || mbar_wait(pv_done + b, (i >> 1) & 1, abort_flag);
+        } else {
+          mbar_arrive(v_free + j % NV);
+          for (int w = 0; w < 4; ++w) mbar_arrive(sc_free + j % NS);  // for the side's softmax warps
+        }
+        ok = ok && scores(i + 2);
+      }
+      // every product issued here completes before tensor memory is given back
+      umma_commit(drain + side);
+      volatile int never = 0;
+      mbar_wait(drain + side, 0, &never);
     }
   } else {
-    // ------------------------------------------------------------------ softmax, products, epilogue
-    q8_regs_acquire<kQ8SoftmaxRegs>();
+    // ------------------------------------------------------------------ softmax, epilogue
     const int side = warp / 4;
     const int rtile = kTwo ? side : 0;
     const int lrow = threadIdx.x % 128;
@@ -515,7 +577,7 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
     const uint32_t lane_off = static_cast<uint32_t>((warp % 4) * 32) << 16;
     if (kTwo || side == 0) {  // this thread's row of q, in the layout the tensor core reads
       const uint16_t *src = p.q + (row_base + row) * HD;
-      uint8_t *dst = sQ + rtile * C::kTileBytes;
+      uint8_t *dst = sQ + rtile * C::kQBytes;
 #pragma unroll
       for (int c = 0; c < HD / 8; ++c) {
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -525,96 +587,46 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
                          __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
         v = make_uint4(q8_fp16_of(v.x, q_unit), q8_fp16_of(v.y, q_unit), q8_fp16_of(v.z, q_unit),
                        q8_fp16_of(v.w, q_unit));
-        *reinterpret_cast<uint4 *>(dst + (c / 8) * C::kChunkBytes + q8_swz(lrow, c % 8)) = v;
+        *reinterpret_cast<uint4 *>(dst + (c / 8) * C::kQChunk + q8_swz(lrow, c % 8)) = v;
       }
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full + rtile);
     }
-    const uint32_t tS = tmem + C::kColS + 128 * side, tO = tmem + C::kColO + HD * side;
-    auto tile_of = [&](int i) { return kTwo ? i : 2 * i + side; };  // the side's i-th tile of tokens
-    // The first thread of the side's first warp issues its products.  With two row tiles it also
-    // arrives on k_free and v_free for the tiles of tokens that only the other one visits.
-    const bool lead = warp % 4 == 0 && lane == 0;
-    const int steps = kTwo ? nmax : cnt;
-    auto next_scores = [&](int i) -> bool {  // S of the side's tile i, or the word that K is not needed
-      if (i >= steps) return true;
-      const int j = tile_of(i);
-      if (!mbar_wait(k_full + (j & 1), (j >> 1) & 1, abort_flag)) return false;
-      if (i < cnt) {
-        tc_fence_after();
-        q8_issue_qk<HD>(tS, sQ + rtile * C::kTileBytes, sK + (j & 1) * C::kTileBytes);
-        umma_commit(s_full + side);
-        umma_commit(k_free + (j & 1));
-      } else {
-        mbar_arrive(k_free + (j & 1));
-      }
-      return true;
-    };
-    auto products = [&](int i) -> bool {  // O += P V of the side's tile i, then the next scores
-      const int j = tile_of(i);
-      if (!mbar_wait(v_full + (j & 1), (j >> 1) & 1, abort_flag)) return false;
-      if (i < cnt) {
-        if (!mbar_wait(p_full + side, i & 1, abort_flag)) return false;
-        tc_fence_after();
-        q8_issue_pv<HD>(tO, tS, sV + (j & 1) * C::kTileBytes, i > 0);
-        umma_commit(pv_done + side);
-        umma_commit(v_free + (j & 1));
-        // P lies over S: the next scores may be written once this product has read it
-        if (!mbar_wait(pv_done + side, i & 1, abort_flag)) return false;
-      } else {
-        mbar_arrive(v_free + (j & 1));
-      }
-      return next_scores(i + 1);
-    };
-    // Turns: the two sides' warps of an SM sub-partition do their exponentials one after the other, so
-    // that one side's products run meanwhile; left alone they fall into step and wait together.
-    auto my_turn = [&](int i) -> bool {
-      if (i >= both || (side == 0 && i == 0)) return true;
-      return __all_sync(0xffffffffu, mbar_wait(turn + warp, (side == 0 ? i - 1 : i) & 1, abort_flag));
-    };
-    auto pass_turn = [&](int i) {
-      __syncwarp();
-      if (i < both && lane == 0) mbar_arrive(turn + (warp ^ 4));
-    };
+    const uint32_t tS = tmem + 128 * side, tO = tmem + C::kColO + HD * side;
     const int t = mine ? row % p.T : 0;
     const int first_own = L - p.T;  // the first of the queries' own tokens
     const uint64_t bits = (p.tree && mine) ? p.tree[static_cast<size_t>(s) * p.T + t] : ~0ull;
     const bool warp_rows = row0 + 128 * rtile + (warp % 4) * 32 < p.R;  // any row in this warp
     float m = 0.f, l = 0.f, F = 0.f;
     bool poison = false;  // the row sees a token whose values are no numbers
-    bool ok = __all_sync(0xffffffffu,
-                         !lead || ((cnt == 0 || mbar_wait(q_full + rtile, 0, abort_flag)) && next_scores(0)));
-    for (int i = 0; ok && i < cnt; ++i) {
-      const int j = tile_of(i);
-      const int buf = j % C::kScaleBufs;
+    bool ok = true;
+    for (int i = 0; i < cnt; ++i) {
+      const int j = kTwo ? i : 2 * i + side;  // the side's i-th tile of tokens
+      const int buf = j % C::kScaleBufs, b = 2 * side + (i & 1);
       const float *ksb = sKs + buf * kQ8Tok;
-      // warp-uniform, as the tensor-memory loads below are warp-wide.  P V of the tile before has
-      // completed (these scores are issued after it), so O may be rescaled.
+      // warp-uniform, as the tensor-memory loads below are warp-wide
       if (!__all_sync(0xffffffffu, mbar_wait(sc_full + buf, (j / C::kScaleBufs) & 1, abort_flag) &&
-                                       mbar_wait(s_full + side, i & 1, abort_flag)) ||
-          !my_turn(i)) { ok = false; break; }
+                                       mbar_wait(s_full + b, (i >> 1) & 1, abort_flag))) { ok = false; break; }
       tc_fence_after();
       if (!warp_rows) {
-        // rows past R: whatever P holds goes to O rows that nobody reads.  (The issuer's warp has
-        // rows, or the side has no tiles.)
-        pass_turn(i);
+        // rows past R: whatever P holds goes to O rows that nobody reads
         tc_fence_before();
-        if (lane == 0) mbar_arrive(p_full + side);
+        if (lane == 0) mbar_arrive(p_full + b), mbar_arrive(sc_free + buf);
         continue;
       }
       const int tok0 = (j0 + j) * kQ8Tok;
       const float F_old = F;
       F = sF[buf * 4];
-      uint32_t k[4];  // the tokens that this row sees
+      uint32_t k[2];  // the tokens that this row sees
       {
-        const uint4 live = *reinterpret_cast<const uint4 *>(sLive + buf * 4);
-        k[0] = live.x, k[1] = live.y, k[2] = live.z, k[3] = live.w;
+        const uint2 live = *reinterpret_cast<const uint2 *>(sLive + buf * 4);
+        k[0] = live.x, k[1] = live.y;
       }
       if ((p.causal || p.tree) && tok0 + kQ8Tok > first_own) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int v0 = tok0 + 32 * c - first_own;  // the chunk's first token among the queries' own
+        for (int c = 0; c < 2; ++c) {
+          const int v0 = tok0 + 32 * c - first_own;  // the 32 tokens' first among the queries' own
           if (p.tree) {
             k[c] &= v0 >= 64 ? 0u : v0 >= 0 ? static_cast<uint32_t>(bits >> v0)
                     : v0 > -32 ? (static_cast<uint32_t>(bits << -v0) | ((1u << -v0) - 1u)) : ~0u;
@@ -624,16 +636,19 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
           }
         }
       }
-      const bool all = __all_sync(0xffffffffu, (k[0] & k[1] & k[2] & k[3]) == 0xffffffffu);
+      const bool all = __all_sync(0xffffffffu, (k[0] & k[1]) == 0xffffffffu);
       {
-        const uint4 bad = *reinterpret_cast<const uint4 *>(sBad + buf * 4);
-        poison = poison || ((k[0] & bad.x) | (k[1] & bad.y) | (k[2] & bad.z) | (k[3] & bad.w)) != 0;
+        const uint2 bad = *reinterpret_cast<const uint2 *>(sBad + buf * 4);
+        poison = poison || ((k[0] & bad.x) | (k[1] & bad.y)) != 0;
       }
-      float a = i == 0 ? 1.f : F_old / F;  // what O is to be multiplied by
-      const float sum = all ? q8_weigh<false>(tS + lane_off, k, ksb, m, l, a)
-                            : q8_weigh<true>(tS + lane_off, k, ksb, m, l, a);
-      pass_turn(i);
+      float a = F == F_old ? 1.f : F_old * q8_inverse(F);  // what O is to be multiplied by
+      const uint32_t ts = tS + lane_off + 64 * (i & 1);
+      const float sum = all ? q8_weigh<false>(ts, k, ksb, m, l, a) : q8_weigh<true>(ts, k, ksb, m, l, a);
       if (i > 0 && __any_sync(0xffffffffu, a != 1.f)) {
+        // the side's previous product must be in O before it is rescaled
+        const int pb = 2 * side + ((i - 1) & 1);
+        if (!__all_sync(0xffffffffu, mbar_wait(pv_done + pb, ((i - 1) >> 1) & 1, abort_flag))) { ok = false; break; }
+        tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < HD; c += 32) {
           float o[32];
@@ -649,17 +664,11 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
       l += sum;
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full + side);
-      ok = __all_sync(0xffffffffu, !lead || products(i));
+      if (lane == 0) mbar_arrive(p_full + b), mbar_arrive(sc_free + buf);
     }
-    if (lead) {
-      for (int i = cnt; ok && i < steps; ++i) ok = products(i);
-      // every product issued here completes before tensor memory is given back
-      umma_commit(drain + side);
-      volatile int never = 0;
-      mbar_wait(drain + side, 0, &never);
-    }
-    ok = __all_sync(0xffffffffu, ok && (cnt == 0 || mbar_wait(pv_done + side, (cnt - 1) & 1, abort_flag)));
+    const int last = cnt - 1;
+    ok = __all_sync(0xffffffffu, ok && (cnt == 0 || mbar_wait(pv_done + 2 * side + (last & 1), (last >> 1) & 1,
+                                                              abort_flag)));
     tc_fence_after();
     const float f = F / q8_vtop<kType>();  // of this side's O
     if constexpr (!kTwo) {

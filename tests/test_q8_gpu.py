@@ -104,6 +104,19 @@ def test_chunk_long(Lq, lens, causal):
     verify(a, o, lse, causal=causal, what="long chunk")
 
 
+@pytest.mark.parametrize("dtype", [E4M3, INT8])
+@pytest.mark.parametrize("Hq,T", [(2, 10), (2, 64), (4, 50)])  # 20, 128 and 200 rows: one and two row tiles
+def test_many_tiles_of_tokens_in_one_range(dtype, Hq, T):
+    # enough (sequence, head) pairs that contexts are not split: dozens of tiles follow one another,
+    # of ragged numbers, and the roles of a CTA run at their own pace
+    lens = [T + (37 * s) % 1900 for s in range(150)]
+    lens[7] = 3000
+    a = make(60 + T, 150, Hq, 1, 64, lens, dtype, T)
+    for _ in range(3):
+        o, lse = call("fa_prefill_paged_q8", a)
+    verify(a, o, lse, causal=True, what="many tiles")
+
+
 def masks(seed, S, T, dev="cuda"):
     import workloads as W
     rows = [W.tree_visibility(p) for p in W.random_tree_parents(seed, S, T)]
