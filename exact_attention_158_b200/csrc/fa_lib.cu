@@ -1013,6 +1013,8 @@ fa_status check_rope(const int32_t *positions, const double *freqs, int rot, fa_
 
 // How the heads of a token are split over threads: not at all where the tokens alone give every SM
 // kRopeWarps warps, else into as many groups as that takes, down to one head each (a decode step).
+// 12, 24, 48 and 96 warps measured alike (8198 tokens of fp32 gradients, 40 heads of 64: 35, 39, 35 and
+// 37 us, on a clock that steps by 2 us); 6 left SMs short of loads in flight, 43.
 constexpr int kRopeWarps = 24;
 
 unsigned rope_split(long long tokens, int heads, int d, int num_sms, int *groups, int *per_group) {
@@ -1090,18 +1092,27 @@ struct Q8Plan {
   size_t rows;      // S * Hq * Lq
 };
 
+// Up to kQ8StreamRows rows fa_q8_stream_kernel, beyond it fa_q8_tile_kernel.  32 sequences of 2048
+// tokens, 8 heads of 128: 16 rows per head take the former 58 us and the latter 96; 17 rows 91 and 96;
+// 32 rows 93 and 96; 64 rows 140 and 94.  One such sequence: 32 rows 24 and 26, 64 rows 24 and 25.
+constexpr int kQ8StreamRows = 32;
 // Few rows: chunks enough for two waves of the four CTAs that fit an SM, none longer than 128 pages (so
 // that ragged lengths balance: 64 sequences of 512 to 8192 tokens took 397 us in two chunks each and
-// 383 in four) and none shorter than 32 (eight to a warp: below that, joining costs more than
-// it saves).
+// 383 in four) and none shorter than 32 (eight to a warp; 4 sequences of 2048 tokens took 18 us at
+// least 16 or 32 long and 23 at 64, 8 of 4096 took 31, 27 and 29).
 constexpr int kQ8TargetCtas = 148 * 4 * 2;
 constexpr int kQ8MinPages = 32, kQ8MaxPages = 128;
-constexpr int kQ8WideSplit = 4;             // more chunks than this: a CTA joins each row
-constexpr int kQ8StreamRows = 16;           // up to here fa_q8_stream_kernel, beyond fa_q8_tile_kernel
 // Many rows: chunks only as far as one CTA per SM goes (64 units of 4096 tokens took 111 us in three chunks
-// each, more than one round of CTAs, and 79 in two).
+// each, more than one round of CTAs, and 79 in two), two token tiles each at least (one sequence of 2048
+// tokens, 64 rows per head: 25 us at least one or two long, 27 at four, 31 at eight).
 constexpr int kQ8TileTargetCtas = 148;
-constexpr int kQ8TileMinPages = 16;         // four token tiles to a chunk
+constexpr int kQ8TileMinPages = 8;
+// How the chunks are joined: with a CTA to each row while one round of CTAs covers the rows (128 rows of
+// 4 chunks: a call of 18 us, 20 with HD / 4 threads to a row), and always past four chunks (there
+// the threads of a row would wait for one chunk after the other).  With more rows of few chunks the CTAs
+// come in rounds: 16384 rows of 2 chunks took 104 us that way, 78 with HD / 4 threads to a row.
+constexpr int kQ8WideSplit = 4;
+constexpr size_t kQ8WideRows = 148 * 8;
 
 bool q8_plan(int S, int Hq, int Hk, int Lq, int d, int max_blocks, Q8Plan *out) {
   if (S < 1 || Hq < 1 || Hk < 1 || Hq % Hk != 0 || Lq < 1 || max_blocks < 1) return false;
@@ -1140,7 +1151,7 @@ fa_status q8_combine(const fa::Q8Params &p, cudaStream_t s) {
   if (e != cudaSuccess) return launch_failed(e);
   if (p.n_split > 1) {
     const size_t rows = static_cast<size_t>(p.S) * p.Hk * p.R;
-    if (p.n_split > kQ8WideSplit)
+    if (p.n_split > kQ8WideSplit || rows <= kQ8WideRows)
       fa::fa_q8_combine_kernel<HD, true><<<static_cast<unsigned>(rows), 256, 0, s>>>(p);
     else
       fa::fa_q8_combine_kernel<HD, false><<<static_cast<unsigned>((rows * (HD / 4) + 255) / 256), 256, 0, s>>>(p);

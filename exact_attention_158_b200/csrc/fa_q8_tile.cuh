@@ -15,29 +15,31 @@
 // row tiles; with fewer they share one row tile and take the tiles of tokens in turn.  A side's S is
 // double, so Q K^T of the next tile and P V of the last run during its softmax.  (With 128-token tiles S
 // fills the same columns once: softmax, P V and Q K^T of a side then follow one another, 5800 cycles
-// per 128 tokens and two row tiles, QQQQ here.)
+// per 128 tokens and two row tiles against 5300 here, and 4500 against 3600 with one row tile.)
 //
 // Scales.  A key's scale multiplies its column of scores in fp32, read from shared memory by every
-// row: 32 broadcast 16-byte loads per row and tile, which cost the SM about half as much as the
-// exponentials.  A value's scale is folded into V instead (a second set of such loads measured
-// 5900 cycles per tile of tokens where this form takes QQQQ): V = code * f in fp16, f = vs 2^a / F
-// with F a power of two no smaller than any vs so far; O is rescaled when F has to grow.  f and the
-// product are rounded to fp16 (2^-11 each, like p).  V uses fp16 from its top (2^15) down and p from
-// 2^6 to 2^15, so a token whose values are 2^20 times the others' and whose weight is 2^-20 takes
-// nothing from either.  A value scale that is not finite would reach rows that do not see its token
-// as 0 * NaN: V is 0 there, and rows that do see it are marked and written as NaN.
+// row (16 broadcast 16-byte loads per row and tile).  A value's scale is folded into V instead, which
+// saves as many loads and a multiplication per score: V = code * f in fp16, f = vs 2^a / F with F a
+// power of two no smaller than any vs so far; O is rescaled when F has to grow.  f and the product
+// are rounded to fp16 (2^-11 each, like p).  V uses fp16 from its top (2^15) down and p from 2^6 to
+// 2^15, so a token whose values are 2^20 times the others' and whose weight is 2^-20 takes nothing from
+// either.  A value scale that is not finite would reach rows that do not see its token as 0 * NaN: V is
+// 0 there, and rows that do see it are marked and written as NaN.
 //
-// A row's softmax is one pass: p = 2^(s ks - m) against the reference it has, summed and stored;
-// where one passes 2^15, and on a row's first tile, the reference moves so that the largest p is 2^6, and
-// O is rescaled in TMEM (as it is when F has grown).
+// A row's softmax is one pass over its scores in registers: p = 2^(s ks - m) against the reference it
+// has; where one passes 2^15, and on a row's first tile, the reference moves so that the largest p is
+// 2^6, and O is rescaled in TMEM (as it is when F has grown).
 //
 // Queries go to fp16 against one power of two for all rows of the CTA (q8_q_unit; it is part of the key
 // scales).  int8's conversion leaves every four features in the order 0, 2, 1, 3; q is stored in that
 // order too, and O's columns are put back when it is written.
 //
-// Bound: per 128 x 128 scores the products take about 1020 cycles at d = 128 and the exponentials
-// 1024 (16 a cycle); the tile's 32 KB of codes take about 1400 cycles of the SM's share of HBM.
-// Few rows are bound by HBM, many by the tensor cores and the exponentials together.
+// Bound: per 128 rows x 64 tokens the products take about 510 cycles at d = 128 and the exponentials
+// 512 (16 a cycle); the 16 KB of codes take about 700 cycles of the SM's share of HBM.  Measured, two
+// row tiles take 2650 cycles a tile of tokens, 2100 of them the two sides' softmax warps side by side:
+// two warps to a scheduler issue an instruction every three cycles or so, which the exponential unit
+// (1024 of the 2100) does not hide.  512-token chunks of 4 sequences: 304 us, 620 TFLOP/s; trees of 48
+// nodes, 32 sequences: 125 us (DRAM's floor 28 us, the products' 35).
 #pragma once
 #include "fa_q8.cuh"
 
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
   if (p.longest_first) {
     // More than one round of CTAs, which start in the order of their index: the s-th longest sequence
     // (ties by index) instead of the s-th, so that the last round is short (32 sequences of 512 to 4096
-    // tokens, 8 heads: 175 us in the batch's order, QQQQ so)
+    // tokens, 8 heads: 175 us in the batch's order, 125 so)
     __shared__ int lens[kQ8SortSeqs], found;
     if (threadIdx.x < p.S) lens[threadIdx.x] = q8_len(p, threadIdx.x);
     __syncthreads();

@@ -75,7 +75,7 @@ def attention(q, k_pool, v_pool, ks, vs, table, lens, scale, causal=False, tree=
     largest p vs at 1 or above, or its largest p at 2^64 (values of scale 0): half a step is 2^-11 of
     it, or 2^-25 where it is below fp16's normal range, which is 2^-25 max(max w vs, 2^-64) of the
     row's weights, and adds up over the codes.
-    With more than 16 rows per key head the value scales are folded into V instead: p, f = vs 2^a / F
+    With more than 32 rows per key head the value scales are folded into V instead: p, f = vs 2^a / F
     and code * f are rounded to fp16, 2^-11 each.  The largest p is at least 2^6, so below fp16's
     normal range it is off by 2^-31 of the largest weight.  F is at most twice the sequence's largest
     vs.  f is at most 2^6 (e4m3, codes to 448) or 2^8 (int8, codes to 127); where it is below fp16's
@@ -123,7 +123,7 @@ def attention(q, k_pool, v_pool, ks, vs, table, lens, scale, causal=False, tree=
             lb[s, h] = (2.0 ** -18 * e + 2.0 ** -20 * (1.0 + lse[s, h].abs().nan_to_num(0.0, posinf=0.0))
                         + 2.0 ** -24 * (16.0 + far))
             seen = (w > 0).double()
-            if Hq // Hk * T <= 16:
+            if Hq // Hk * T <= 32:
                 top = (w * f[:, 0]).amax(-1, keepdim=True).clamp(min=2.0 ** -64) if len(f) else 0.0
                 floor, steps = 2.0 ** -25 * top * seen @ codes, 1
             else:

@@ -105,7 +105,7 @@ def test_chunk_long(Lq, lens, causal):
 
 
 @pytest.mark.parametrize("dtype", [E4M3, INT8])
-@pytest.mark.parametrize("Hq,T", [(2, 10), (2, 64), (4, 50)])  # 20, 128 and 200 rows: one and two row tiles
+@pytest.mark.parametrize("Hq,T", [(2, 10), (2, 17), (2, 64), (4, 50)])  # 20, 34, 128 and 200 rows
 def test_many_tiles_of_tokens_in_one_range(dtype, Hq, T):
     # enough (sequence, head) pairs that contexts are not split: dozens of tiles follow one another,
     # of ragged numbers, and the roles of a CTA run at their own pace
