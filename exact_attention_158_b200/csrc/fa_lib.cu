@@ -1011,6 +1011,19 @@ fa_status check_rope(const int32_t *positions, const double *freqs, int rot, fa_
   return FA_OK;
 }
 
+// The memory from the first to the last element of bf16 rows [T, H, d] with these strides.
+struct Span {
+  const void *p;
+  size_t bytes;
+};
+
+Span row_span(const void *x, const long long *strides, int T, int H, int d) {
+  const long long n[2] = {T, H};
+  long long lo = 0, hi = d;
+  for (int a = 0; a < 2; ++a) (strides[a] < 0 ? lo : hi) += (n[a] - 1) * strides[a];
+  return Span{static_cast<const char *>(x) + 2 * lo, static_cast<size_t>(hi - lo) * 2};
+}
+
 // How the heads of a token are split over threads: not at all where the tokens alone give every SM
 // kRopeWarps warps, else into as many groups as that takes, down to one head each (a decode step).
 // 12, 24, 48 and 96 warps measured alike (8198 tokens of fp32 gradients, 40 heads of 64: 35, 39, 35 and
@@ -1319,6 +1332,12 @@ fa_status fa_rope(const void *q, const long long *q_strides, void *q_out,
     if (heads[i] == 0) continue;
     if (!in[i] || !out[i] || !is[i] || !os[i]) return FA_ERR_INVALID_ARG;
     if (!aligned16(in[i]) || !aligned16(out[i])) return FA_ERR_ALIGNMENT;
+    // in place is the same tensor: a row written elsewhere or wider than it was read meets others
+    if (in[i] == out[i]) {
+      if (in_dtype != out_dtype) return FA_ERR_INVALID_ARG;
+      for (int a = 0; a < 3; ++a)
+        if ((a == 1 ? heads[i] : extent[a]) > 1 && is[i][a] != os[i][a]) return FA_ERR_INVALID_ARG;
+    }
     p.x[i].in = in[i];
     p.x[i].out = out[i];
     p.x[i].H = heads[i];
@@ -1391,22 +1410,32 @@ fa_status fa_cache_append(const void *k, const long long *k_strides, const void 
   p.Hq = Hq;
   p.Hk = Hk;
   p.num_slots = static_cast<long long>(num_blocks) * fa::kCachePage;
-  // the pools and scales are written: they may lie neither on one another nor on the inputs
+  if (Hq > 0 && q == q_out)  // in place is the same tensor
+    for (int a = 0; a < 2; ++a)
+      if ((a == 0 ? T : Hq) > 1 && q_strides[a] != q_out_strides[a]) return FA_ERR_INVALID_ARG;
+  // the pools and scales are written: they may lie neither on one another nor on the rows read or
+  // written beside them (a strided tensor counts from its first to its last element); q_out in turn
+  // not on the slots and positions
   const size_t rows = static_cast<size_t>(num_blocks) * Hk * fa::kCachePage;
   const size_t pool_bytes = rows * d * (type == FA_CACHE_BF16 ? 2 : 1);
   const size_t scale_bytes = type == FA_CACHE_BF16 ? 0 : rows * 4;
   const void *outs[4] = {k_pool, v_pool, k_scale, v_scale};
   const size_t out_bytes[4] = {pool_bytes, pool_bytes, scale_bytes, scale_bytes};
-  const void *ins[4] = {slots, positions, k, v};
-  const size_t in_bytes[4] = {static_cast<size_t>(T) * 8, rot ? static_cast<size_t>(T) * 4 : 0,
-                              static_cast<size_t>(d) * 2, static_cast<size_t>(d) * 2};
+  const Span kx = row_span(k, k_strides, T, Hk, d), vx = row_span(v, v_strides, T, Hk, d);
+  const Span qx = Hq > 0 ? row_span(q, q_strides, T, Hq, d) : Span{nullptr, 0};
+  const Span qox = Hq > 0 ? row_span(q_out, q_out_strides, T, Hq, d) : Span{nullptr, 0};
+  const void *ins[6] = {slots, positions, kx.p, vx.p, qx.p, qox.p};
+  const size_t in_bytes[6] = {static_cast<size_t>(T) * 8, rot ? static_cast<size_t>(T) * 4 : 0,
+                              kx.bytes, vx.bytes, qx.bytes, qox.bytes};
   for (int a = 0; a < 4; ++a) {
     if (out_bytes[a] == 0) continue;
-    for (int b = 0; b < 4; ++b)
+    for (int b = 0; b < 6; ++b)
       if (in_bytes[b] && overlaps(outs[a], out_bytes[a], ins[b], in_bytes[b])) return FA_ERR_INVALID_ARG;
     for (int b = a + 1; b < 4; ++b)
       if (out_bytes[b] && overlaps(outs[a], out_bytes[a], outs[b], out_bytes[b])) return FA_ERR_INVALID_ARG;
   }
+  for (int b = 0; b < 2; ++b)
+    if (Hq > 0 && in_bytes[b] && overlaps(qox.p, qox.bytes, ins[b], in_bytes[b])) return FA_ERR_INVALID_ARG;
   DeviceInfo *dev = nullptr;
   int dev_id = 0;
   if ((st = current_device(&dev, &dev_id)) != FA_OK) return st;

@@ -336,11 +336,12 @@ fa_status fa_rope(const void *q, const long long *q_strides, void *q_out,
  *   k_scale, v_scale   as above for FA_CACHE_E4M3 and FA_CACHE_INT8; ignored (may be null) for
  *                  FA_CACHE_BF16.
  *   q, q_out       bf16 [T, Hq, d] with strides as k (Hq = 0: none, pointers ignored); every token's
- *                  q is rotated, padding too.  May be the same tensor.
+ *                  q is rotated, padding too.  May be the same tensor (same pointer and strides).
  *   positions      int32 [T], device;  freqs, rot, layout, amplitude as for fa_rope (rot = 0: no
  *                  rotation, positions and freqs may be null).
  *   T >= 0 (nothing is launched for 0), Hk >= 1, Hq >= 0;  d: 64 or 128;  (num_blocks + 1) * Hk <=
- *   INT_MAX.  Slots that no token names are left as they are.
+ *   INT_MAX.  Slots that no token names are left as they are.  k, v, q and q_out, from their first
+ *   element to their last, must not overlap the pools or scales.
  * Returns FA_OK once the kernel is queued.
  */
 typedef enum {

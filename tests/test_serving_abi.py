@@ -45,6 +45,13 @@ def test_rope_refusals(lib):
     assert rope(lib, N=0) == 0 and rope(lib, B=0) == 0  # nothing to do
 
 
+def test_rope_in_place_is_the_same_tensor(lib):
+    assert rope(lib, qo=A, odt=1) == 1                       # written wider than read
+    assert rope(lib, qo=A, qos=(4096, 64, 512)) == 1         # written elsewhere
+    assert rope(lib, ko=3 * A, qos=(8192, 512, 64)) == 1
+    assert rope(lib, qo=A, ko=3 * A, N=0) == 0
+
+
 def append(lib, k=A, ks=(512, 64), v=2 * A, kp=16 * A, vp=18 * A, ksc=20 * A, vsc=22 * A, ty=1, slots=3 * A,
            P=8, q=4 * A, qo=5 * A, qos=(512, 64), pos=6 * A, fr=7 * A, rot=64, layout=0, amp=1.0, T=4, Hq=8,
            Hk=8, d=64):
@@ -71,6 +78,16 @@ def test_append_refusals(lib):
 
 def read(lib, kp=16 * A, vp=18 * A, ksc=20 * A, vsc=22 * A, ty=1, slots=3 * A, P=8, k=A, v=2 * A, T=4, H=8, d=64):
     return lib.fa_cache_read(kp, vp, ksc, vsc, ty, slots, P, k, v, T, H, d, None)
+
+
+def test_append_overlaps(lib):
+    far = A // 64  # T = 4 rows of 64 features this far apart (in elements) span 3 A / 32 bytes
+    for over in (16 * A - A // 16, 18 * A - A // 16):
+        assert append(lib, k=over, ks=(far, 64)) == 1 and append(lib, v=over, ks=(far, 64)) == 1
+        assert append(lib, qo=over, qos=(far, 64)) == 1 and append(lib, q=over, ks=(far, 64)) == 1
+    assert append(lib, k=22 * A + A // 16, ks=(-far, 64)) == 1  # backwards into a scale
+    assert append(lib, qo=20 * A) == 1 and append(lib, qo=3 * A) == 1 and append(lib, qo=6 * A) == 1
+    assert append(lib, qo=4 * A, qos=(512, 128)) == 1           # in place with other strides
 
 
 def test_read_refusals(lib):
