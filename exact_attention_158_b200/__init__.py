@@ -515,6 +515,15 @@ def _stream_on(index, stream):
     return int(torch.cuda.current_stream(index).cuda_stream)
 
 
+def _new(like, shape, dtype, stream):
+    """Memory for a call on `stream`, on like's device: it comes from that stream's pool, so whatever
+    the current stream still does to freed memory, or does with it next, cannot meet the kernel."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def _on_device(index, where, fn, *args):
     if torch.cuda.current_device() == index:
         st = fn(*args)
@@ -588,7 +597,7 @@ def fa_rope(q, k, positions, freqs, layout: str = "half", amplitude: float = 1.0
         out_dtype = q_out.dtype if q_out is not None else q.dtype
     out_code = _out_code(out_dtype)
     if q_out is None:
-        q_out = q.new_empty((B, Hq, N, d), dtype=out_dtype)
+        q_out = _new(q, (B, Hq, N, d), out_dtype, stream)
     else:
         _require_rows(q_out, "q_out", 4, (out_dtype,), dev)
         if q_out.shape != q.shape:
@@ -600,7 +609,7 @@ def fa_rope(q, k, positions, freqs, layout: str = "half", amplitude: float = 1.0
         if k.shape != (B, Hk, N, d):
             raise ValueError("k must be [B, Hk, N, d] with q's B, N, d")
         if k_out is None:
-            k_out = q.new_empty((B, Hk, N, d), dtype=out_dtype)
+            k_out = _new(q, (B, Hk, N, d), out_dtype, stream)
         else:
             _require_rows(k_out, "k_out", 4, (out_dtype,), dev)
             if k_out.shape != k.shape:
@@ -671,7 +680,7 @@ def fa_cache_append(k, v, k_pool, v_pool, slots, k_scale=None, v_scale=None, pos
         if q.shape != (T, Hq, d):
             raise ValueError("q must be [T, Hq, d]")
         if q_out is None:
-            q_out = q.new_empty((T, Hq, d))
+            q_out = _new(q, (T, Hq, d), q.dtype, stream)
         else:
             _require_rows(q_out, "q_out", 3, _BF16, dev)
             if q_out.shape != q.shape:
@@ -698,11 +707,11 @@ def fa_cache_read(k_pool, v_pool, slots, k_scale=None, v_scale=None, k_out=None,
         raise ValueError("slots must be [T]")
     T = slots.shape[0]
     if k_out is None:
-        k_out = k_pool.new_empty((T, H, d), dtype=torch.bfloat16)
+        k_out = _new(k_pool, (T, H, d), torch.bfloat16, stream)
     else:
         _require_flat(k_out, "k_out", torch.bfloat16, (T, H, d), dev)
     if v_out is None:
-        v_out = k_pool.new_empty((T, H, d), dtype=torch.bfloat16)
+        v_out = _new(k_pool, (T, H, d), torch.bfloat16, stream)
     else:
         _require_flat(v_out, "v_out", torch.bfloat16, (T, H, d), dev)
     _on_device(dev, "fa_cache_read", lib.fa_cache_read, k_pool.data_ptr(), v_pool.data_ptr(), ksp, vsp,
@@ -739,19 +748,19 @@ def _attend_q8(where, q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens
         _require_flat(tree_mask, "tree_mask", torch.int64, (S, Lq), dev)
     code_o = _out_code(out_dtype)
     if out is None:
-        out = torch.empty_like(q) if code_o == FA_OUT_BF16 else q.new_empty(shape, dtype=out_dtype)
+        out = _new(q, shape, out_dtype, stream)
     else:
         _require_flat(out, "out", out_dtype, shape, dev)
     if lse is not None:
         _require_flat(lse, "lse", torch.float32, shape[:-1], dev)
     elif return_lse:
-        lse = q.new_empty(shape[:-1], dtype=torch.float32)
+        lse = _new(q, shape[:-1], torch.float32, stream)
     maxb = block_table.shape[1]
     ws, ws_bytes = None, 0
     if workspace is None:
         ws_bytes = fa_q8_workspace_size(S, Hq, Hk, Lq, d, maxb)
         if ws_bytes:
-            workspace = q.new_empty(ws_bytes, dtype=torch.uint8)
+            workspace = _new(q, (ws_bytes,), torch.uint8, stream)
             ws = workspace.data_ptr()
     else:
         _require_flat(workspace, "workspace", workspace.dtype, None, dev)

@@ -328,3 +328,34 @@ def test_a_serving_step(dtype):
         for t in range(T):
             see[t, -T:] = torch.tensor([(int(m[s, t]) >> u) & 1 == 1 for u in range(T)])
         compare(o[s], s, q[s], see, "tree")
+
+
+def test_new_tensors_belong_to_the_given_stream():
+    # the current stream has freed memory that it still writes to; a call on another stream whose
+    # results or workspace lay there would lose them
+    import exact_attention_158_b200 as fa
+    a = make(70, 2, 8, 2, 128, [3000, 700], E4M3)
+    kp, vp, ks, vs = a[1:5]
+    slots = (a[5][0, :4].long()[:, None] * 16 + torch.arange(16, device="cuda")).flatten()
+    x = torch.randn((2, 8, 32, 128), device="cuda").to(torch.bfloat16)
+    pos = torch.arange(32, dtype=torch.int32, device="cuda")
+    freqs = fa.rope_frequencies(128)[0].cuda()
+    side = torch.cuda.Stream()
+    calls = [lambda **kw: fa.fa_decode_paged_q8(*a, **kw),
+             lambda **kw: fa.fa_rope(x, x, pos, freqs, **kw),
+             lambda **kw: fa.fa_cache_read(kp, vp, slots, ks, vs, **kw)]
+    for f in calls:
+        want = f()
+        torch.cuda.synchronize()
+        late = [torch.empty_like(t) for t in want for _ in range(2)]
+        if f is calls[0]:
+            need = fa.fa_q8_workspace_size(2, 8, 2, 1, 128, a[5].shape[1])
+            assert need > 0
+            late.append(torch.empty(need, dtype=torch.uint8, device="cuda"))
+        torch.cuda._sleep(40_000_000)
+        for t in late:
+            t.fill_(7)
+        del late, t
+        got = f(stream=side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
