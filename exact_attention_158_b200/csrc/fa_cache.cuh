@@ -15,6 +15,8 @@
 #pragma once
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "fa_rope.cuh"
 
 namespace fa {
@@ -89,15 +91,15 @@ __global__ void __launch_bounds__(kRopeThreads) fa_cache_append_kernel(const App
   const long long m = rest - static_cast<unsigned long long>(group) * p.T;
   const int first = group * p.heads_per_group;
   const int last = min(first + p.heads_per_group, p.Hq + 2 * p.Hk);
-  const int2 rcol = rope_cols(p.table, chunk), vcol = make_int2(16 * chunk, 16 * chunk + 8);
+  const RopeCols<8> rcol = rope_cols<HD, 8>(p.table, chunk), vcol{{8 * chunk, HD / 2 + 8 * chunk}};
   long long slot = p.slots[m];
   if (slot >= p.num_slots) {  // caller broke the contract: report, write nothing for the token
     atomicExch(&g_device_status, 1 /* FA_ERR_INVALID_ARG */);
     slot = -1;
   }
-  RopeTurn turn;
+  RopeTurn<8> turn;
   // rows [lo, hi) of one kind: four loads on their way ahead of `put`
-  auto walk = [&](const uint16_t *src, long long step, int lo, int hi, int2 col, auto put) {
+  auto walk = [&](const uint16_t *src, long long step, int lo, int hi, const RopeCols<8> &col, auto put) {
     Raw16<bf> raw[kUnroll];
     if (lo >= hi) return;
     const bf *row = reinterpret_cast<const bf *>(src) + lo * step;
@@ -118,12 +120,10 @@ __global__ void __launch_bounds__(kRopeThreads) fa_cache_append_kernel(const App
   };
   const unsigned mates = ((1u << kChunks) - 1u) << ((threadIdx.x & 31) / kChunks * kChunks);
   const long long row0 = slot < 0 ? 0 : slot / kCachePage * p.Hk * kCachePage + slot % kCachePage;
-  auto store = [&](void *pool, float *scales, int h, int2 col, const float (&f)[16]) {
+  auto store = [&](void *pool, float *scales, int h, const RopeCols<8> &col, const float (&f)[16]) {
     const long long row = row0 + static_cast<long long>(h) * kCachePage;
     if constexpr (kType == kCacheBf16) {
-      bf *dst = static_cast<bf *>(pool) + row * HD;
-      store8(dst + col.x, f);
-      store8(dst + col.y, f + 8);
+      store_pieces(static_cast<bf *>(pool) + row * HD, col, f);
     } else {
       float top = 0.f;  // NaN and infinities come through
 #pragma unroll
@@ -139,19 +139,17 @@ __global__ void __launch_bounds__(kRopeThreads) fa_cache_append_kernel(const App
         for (int e = 0; e < 4; ++e) w[e] = cache_code4<kType>(f + 4 * e, scale, rcp);
       }
       uint8_t *dst = static_cast<uint8_t *>(pool) + row * HD;
-      *reinterpret_cast<uint2 *>(dst + col.x) = make_uint2(w[0], w[1]);
-      *reinterpret_cast<uint2 *>(dst + col.y) = make_uint2(w[2], w[3]);
+      *reinterpret_cast<uint2 *>(dst + col.col[0]) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2 *>(dst + col.col[1]) = make_uint2(w[2], w[3]);
       if (chunk == 0) scales[row] = scale;
     }
   };
   // (a thread whose heads are all values needs no angles)
-  turn.any = false;
-  if (first < p.Hq + p.Hk) rope_turn(p.table, p.positions + m, chunk, turn);
+  turn.on[0] = turn.on[1] = false;
+  if (first < p.Hq + p.Hk) rope_turn(p.table, p.positions + m, rcol, turn);
   walk(p.q + m * p.q_s[0], p.q_s[1], first, min(last, p.Hq), rcol, [&](int h, float (&f)[16]) {
     rope_apply(p.table, turn, f);
-    bf *dst = reinterpret_cast<bf *>(p.q_out) + m * p.qo_s[0] + h * p.qo_s[1];
-    store8(dst + rcol.x, f);
-    store8(dst + rcol.y, f + 8);
+    store_pieces(reinterpret_cast<bf *>(p.q_out) + m * p.qo_s[0] + h * p.qo_s[1], rcol, f);
   });
   if (slot < 0) return;
   walk(p.k + m * p.k_s[0], p.k_s[1], max(first - p.Hq, 0), min(last - p.Hq, p.Hk), rcol, [&](int h, float (&f)[16]) {
@@ -173,8 +171,8 @@ struct ReadParams {
   int groups, heads_per_group;  // of the k and v heads, as in RopeParams
 };
 
-// Threads as in fa_rope_kernel: one per (head group, token, chunk of 16 features), the heads of k and v
-// counted in that order; four rows on their way at once.
+// Threads as in fa_rope_kernel: one per (head group, token, chunk: features 8 c.. and HD/2 + 8 c..), the
+// heads of k and v counted in that order; four rows on their way at once.
 template <int HD, int kType>
 __global__ void __launch_bounds__(kRopeThreads) fa_cache_read_kernel(const ReadParams p) {
   constexpr int kChunks = HD / 16, kUnroll = 4;
@@ -191,7 +189,9 @@ __global__ void __launch_bounds__(kRopeThreads) fa_cache_read_kernel(const ReadP
     slot = -1;
   }
   const long long row0 = slot < 0 ? 0 : slot / kCachePage * p.H * kCachePage + slot % kCachePage;
-  struct Row { uint4 c[kType == kCacheBf16 ? 2 : 1]; float scale; } row[kUnroll];
+  using Piece = std::conditional_t<kType == kCacheBf16, uint4, uint2>;  // eight features
+  struct Row { Piece c[2]; float scale; } row[kUnroll];
+  constexpr int kSize = kType == kCacheBf16 ? 2 : 1;
   for (int h0 = first; h0 < last; h0 += kUnroll) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -199,27 +199,23 @@ __global__ void __launch_bounds__(kRopeThreads) fa_cache_read_kernel(const ReadP
       const bool is_v = h0 + u >= p.H;
       const long long r = row0 + static_cast<long long>(h0 + u - (is_v ? p.H : 0)) * kCachePage;
       const uint8_t *pool = static_cast<const uint8_t *>(is_v ? p.v_pool : p.k_pool);
-      if constexpr (kType == kCacheBf16) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(pool + (r * HD + 16 * chunk) * 2);
-        row[u].c[0] = src[0];
-        row[u].c[1] = src[1];
-      } else {
-        row[u].c[0] = *reinterpret_cast<const uint4 *>(pool + r * HD + 16 * chunk);
-        row[u].scale = (is_v ? p.v_scale : p.k_scale)[r];
-      }
+      const uint8_t *src = pool + (r * HD + 8 * chunk) * kSize;
+      row[u].c[0] = *reinterpret_cast<const Piece *>(src);
+      row[u].c[1] = *reinterpret_cast<const Piece *>(src + HD / 2 * kSize);
+      if constexpr (kType != kCacheBf16) row[u].scale = (is_v ? p.v_scale : p.k_scale)[r];
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       if (h0 + u >= last) break;
       const bool is_v = h0 + u >= p.H;
-      uint16_t *dst = (is_v ? p.v : p.k) + (m * p.H + h0 + u - (is_v ? p.H : 0)) * HD + 16 * chunk;
+      uint16_t *dst = (is_v ? p.v : p.k) + (m * p.H + h0 + u - (is_v ? p.H : 0)) * HD + 8 * chunk;
       uint4 o[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
       if (slot >= 0) {
         if constexpr (kType == kCacheBf16) {
           o[0] = row[u].c[0];
           o[1] = row[u].c[1];
         } else {
-          const uint32_t w[4] = {row[u].c[0].x, row[u].c[0].y, row[u].c[0].z, row[u].c[0].w};
+          const uint32_t w[4] = {row[u].c[0].x, row[u].c[0].y, row[u].c[1].x, row[u].c[1].y};
           uint32_t b[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -239,8 +235,8 @@ __global__ void __launch_bounds__(kRopeThreads) fa_cache_read_kernel(const ReadP
           o[1] = make_uint4(b[4], b[5], b[6], b[7]);
         }
       }
-      reinterpret_cast<uint4 *>(dst)[0] = o[0];
-      reinterpret_cast<uint4 *>(dst)[1] = o[1];
+      *reinterpret_cast<uint4 *>(dst) = o[0];
+      *reinterpret_cast<uint4 *>(dst + HD / 2) = o[1];
     }
   }
 }

@@ -48,44 +48,84 @@ __device__ __forceinline__ float2 rope_cos_sin(const RopeTable &t, int position,
   return make_float2(t.amplitude * c, t.amplitude * t.sign * s);
 }
 
-// A thread's 16 features of one row: f[0..7] and f[8..15] start at columns rope_cols().  In the
-// half layout chunk c of the rotated part is features 8c.. and rot/2 + 8c.. (eight whole pairs);
-// every other chunk is 16 features in a row (eight interleaved pairs, or the part passed through).
-__device__ __forceinline__ int2 rope_cols(const RopeTable &t, int chunk) {
-  if (!t.interleaved && 16 * chunk < t.rot) return make_int2(8 * chunk, t.rot / 2 + 8 * chunk);
-  return make_int2(16 * chunk, 16 * chunk + 8);
-}
-
-// The cosines and sines of a chunk's eight pairs at a token's position.
-struct RopeTurn {
-  float2 w[8];
-  bool any;  // a chunk of the part passed through turns nothing
+// A thread's 16 features of one row, f[0..15], are 16 / P pieces of P features, 16 bytes each as they are
+// read: P = 8 in bf16, 4 in fp32.  The HD / 16 threads of a row take neighbouring pieces, so each of
+// their accesses is whole sectors (32 contiguous bytes to a thread instead, two accesses to a sector:
+// 55 us where this takes 45, B8 H16+16 N2048 d128 bf16 interleaved).  In the half layout
+// the pieces come in twos, those of pairs j in features j.. and rot/2 + j.., and the part passed
+// through is split in the same way.
+template <int P> struct RopeCols {
+  int col[16 / P];
 };
-__device__ __forceinline__ void rope_turn(const RopeTable &t, const int32_t *position, int chunk, RopeTurn &r) {
-  r.any = 16 * chunk < t.rot;
-  if (r.any) {
-    const int p = *position;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) r.w[j] = rope_cos_sin(t, p, 8 * chunk + j);
-  }
-}
-
-__device__ __forceinline__ void rope_apply(const RopeTable &t, const RopeTurn &r, float (&f)[16]) {
-  if (!r.any) return;
+template <int HD, int P>
+__device__ __forceinline__ RopeCols<P> rope_cols(const RopeTable &t, int chunk) {
+  constexpr int kMates = HD / 16;
+  RopeCols<P> r;
   if (t.interleaved) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = f[2 * j], b = f[2 * j + 1];
-      f[2 * j] = fmaf(a, r.w[j].x, -b * r.w[j].y);
-      f[2 * j + 1] = fmaf(b, r.w[j].x, a * r.w[j].y);
-    }
+    for (int i = 0; i < 16 / P; ++i) r.col[i] = P * (chunk + i * kMates);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = f[j], b = f[8 + j];
-      f[j] = fmaf(a, r.w[j].x, -b * r.w[j].y);
-      f[8 + j] = fmaf(b, r.w[j].x, a * r.w[j].y);
+    for (int k = 0; k < 8 / P; ++k) {
+      const int x = P * (chunk + k * kMates), over = x - t.rot / 2;
+      r.col[2 * k] = over < 0 ? x : t.rot + over;
+      r.col[2 * k + 1] = over < 0 ? t.rot / 2 + x : t.rot + (HD - t.rot) / 2 + over;
     }
+  }
+  return r;
+}
+
+// The cosines and sines of a thread's eight pairs at a token's position: of f[2i], f[2i + 1] in the
+// interleaved layout, of features i of the two pieces in the half one.
+template <int P> struct RopeTurn {
+  float2 w[8];
+  bool on[16 / P];  // piece i is turned (in the half layout, pieces 2k and 2k + 1 alike), not passed through
+};
+template <int P>
+__device__ __forceinline__ void rope_turn(const RopeTable &t, const int32_t *position, const RopeCols<P> &c,
+                                          RopeTurn<P> &r) {
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 16 / P; ++i) {
+    r.on[i] = (t.interleaved ? c.col[i] : c.col[i / 2 * 2]) < t.rot;
+    any = any || r.on[i];
+  }
+  if (!any) return;
+  // all eight in one go (a piece passed through makes pair 0's and drops them): the sines of one pair
+  // run in the latency of the others'
+  const int p = *position;
+  int pair[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int i = j / (P / 2), e = j % (P / 2);
+    pair[j] = !r.on[i] ? 0 : e + (t.interleaved ? c.col[i] / 2 : c.col[i / 2 * 2] + i % 2 * (P / 2));
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) r.w[j] = rope_cos_sin(t, p, pair[j]);
+}
+
+__device__ __forceinline__ void rope_pair(float2 w, float &a, float &b) {
+  const float x = a;
+  a = fmaf(x, w.x, -b * w.y);
+  b = fmaf(b, w.x, x * w.y);
+}
+
+template <int P>
+__device__ __forceinline__ void rope_apply(const RopeTable &t, const RopeTurn<P> &r, float (&f)[16]) {
+  if (t.interleaved) {
+#pragma unroll
+    for (int i = 0; i < 16 / P; ++i)
+      if (r.on[i]) {
+#pragma unroll
+        for (int j = i * (P / 2); j < (i + 1) * (P / 2); ++j) rope_pair(r.w[j], f[2 * j], f[2 * j + 1]);
+      }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8 / P; ++k)
+      if (r.on[2 * k]) {
+#pragma unroll
+        for (int e = 0; e < P; ++e) rope_pair(r.w[P * k + e], f[2 * P * k + e], f[2 * P * k + P + e]);
+      }
   }
 }
 
@@ -93,15 +133,14 @@ __device__ __forceinline__ void rope_apply(const RopeTable &t, const RopeTurn &r
 template <class T> struct Raw16;
 template <> struct Raw16<__nv_bfloat16> { uint4 v[2]; };
 template <> struct Raw16<float> { float4 v[4]; };
-__device__ __forceinline__ void raw_load(Raw16<__nv_bfloat16> &r, const __nv_bfloat16 *row, int2 col) {
-  r.v[0] = *reinterpret_cast<const uint4 *>(row + col.x);
-  r.v[1] = *reinterpret_cast<const uint4 *>(row + col.y);
+template <class T> constexpr int kRopePiece = 16 / sizeof(T);  // features
+__device__ __forceinline__ void raw_load(Raw16<__nv_bfloat16> &r, const __nv_bfloat16 *row, const RopeCols<8> &c) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) r.v[i] = *reinterpret_cast<const uint4 *>(row + c.col[i]);
 }
-__device__ __forceinline__ void raw_load(Raw16<float> &r, const float *row, int2 col) {
-  r.v[0] = reinterpret_cast<const float4 *>(row + col.x)[0];
-  r.v[1] = reinterpret_cast<const float4 *>(row + col.x)[1];
-  r.v[2] = reinterpret_cast<const float4 *>(row + col.y)[0];
-  r.v[3] = reinterpret_cast<const float4 *>(row + col.y)[1];
+__device__ __forceinline__ void raw_load(Raw16<float> &r, const float *row, const RopeCols<4> &c) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = *reinterpret_cast<const float4 *>(row + c.col[i]);
 }
 __device__ __forceinline__ void raw_floats(const Raw16<__nv_bfloat16> &r, float (&f)[16]) {
 #pragma unroll
@@ -121,19 +160,6 @@ __device__ __forceinline__ void raw_floats(const Raw16<float> &r, float (&f)[16]
   }
 }
 
-__device__ __forceinline__ void load8(const float *src, float *f) {
-  const float4 a = reinterpret_cast<const float4 *>(src)[0], b = reinterpret_cast<const float4 *>(src)[1];
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16 *src, float *f) {
-  const uint4 v = *reinterpret_cast<const uint4 *>(src);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
 __device__ __forceinline__ void store8(float *dst, const float *f) {
   reinterpret_cast<float4 *>(dst)[0] = make_float4(f[0], f[1], f[2], f[3]);
   reinterpret_cast<float4 *>(dst)[1] = make_float4(f[4], f[5], f[6], f[7]);
@@ -141,6 +167,21 @@ __device__ __forceinline__ void store8(float *dst, const float *f) {
 __device__ __forceinline__ void store8(__nv_bfloat16 *dst, const float *f) {
   *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
                                                pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+
+__device__ __forceinline__ void store4(float *dst, const float *f) {
+  *reinterpret_cast<float4 *>(dst) = make_float4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16 *dst, const float *f) {
+  *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+}
+template <class T, int P>
+__device__ __forceinline__ void store_pieces(T *row, const RopeCols<P> &c, const float (&f)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16 / P; ++i) {
+    if constexpr (P == 8) store8(row + c.col[i], f + 8 * i);
+    else store4(row + c.col[i], f + 4 * i);
+  }
 }
 
 // One tensor [B, H, N, d] of the call: element strides of b, h and n on both sides.
@@ -164,7 +205,7 @@ struct RopeParams {
 // One thread per (head group, token, chunk of features), the chunk fastest, then the token.
 template <int HD, class In, class Out>
 __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams p) {
-  constexpr int kChunks = HD / 16;
+  constexpr int kChunks = HD / 16, P = kRopePiece<In>;
   constexpr int kUnroll = sizeof(In) == 4 ? 2 : 4;  // rows on their way at once
   const unsigned long long gid = static_cast<unsigned long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
   const int chunk = static_cast<int>(gid % kChunks);
@@ -175,7 +216,7 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
   const long long b = m / static_cast<unsigned>(p.N), n = m % static_cast<unsigned>(p.N);
   const int first = group * p.heads_per_group;
   const int last = min(first + p.heads_per_group, p.x[0].H + p.x[1].H);
-  const int2 col = rope_cols(p.table, chunk);
+  const RopeCols<P> col = rope_cols<HD, P>(p.table, chunk);
   auto in_row = [&](int h) {
     const RopeTensor &x = p.x[h >= p.x[0].H];
     if (h >= p.x[0].H) h -= p.x[0].H;
@@ -185,8 +226,8 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u)
     if (first + u < last) raw_load(raw[u], in_row(first + u), col);
-  RopeTurn turn;
-  rope_turn(p.table, p.positions + b * p.pos_stride + n, chunk, turn);
+  RopeTurn<P> turn;
+  rope_turn(p.table, p.positions + b * p.pos_stride + n, col, turn);
   for (int h0 = first; h0 < last; h0 += kUnroll) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -194,14 +235,13 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
       if (h >= last) break;
       float f[16];
       raw_floats(raw[u], f);
-      // in place, a row is read before it is written: it has one thread per chunk of pairs
+      // in place, a row is read before it is written: a thread writes the features it has read
       if (h + kUnroll < last) raw_load(raw[u], in_row(h + kUnroll), col);
       rope_apply(p.table, turn, f);
       const RopeTensor &x = p.x[h >= p.x[0].H];
       if (h >= p.x[0].H) h -= p.x[0].H;
       Out *dst = static_cast<Out *>(x.out) + b * x.out_s[0] + h * x.out_s[1] + n * x.out_s[2];
-      store8(dst + col.x, f);
-      store8(dst + col.y, f + 8);
+      store_pieces(dst, col, f);
     }
   }
 }
