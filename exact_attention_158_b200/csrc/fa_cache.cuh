@@ -78,7 +78,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN when either
 // Threads as in fa_rope_kernel: one per (head group, token, chunk), the heads of q, k and v counted in
 // that order; HD / 16 threads a row, 16 features each, the row maximum by shuffles among them.
 // Instructions, not bytes, bound the first form of this kernel (254 per four rows of a warp, 47 us for
-// 8191 tokens x 48 heads of 128; 39 now): a thread walks its q, k and v rows in loops of their own.
+// 8191 tokens x 48 heads of 128; 39 with the q, k and v rows walked in loops of their own).  Four rows are
+// on their way (with two, written and read back: 52 us for 48).
 template <int HD, int kType>
 __global__ void __launch_bounds__(kRopeThreads) fa_cache_append_kernel(const AppendParams p) {
   constexpr int kChunks = HD / 16, kUnroll = 4;

@@ -1026,9 +1026,10 @@ Span row_span(const void *x, const long long *strides, int T, int H, int d) {
 
 // How the heads of a token are split over threads: not at all where the tokens alone give every SM
 // kRopeWarps warps, else into as many groups as that takes, down to one head each (a decode step).
-// 12, 24, 48 and 96 warps measured alike (8198 tokens of fp32 gradients, 40 heads of 64: 35, 39, 35 and
-// 37 us, on a clock that steps by 2 us); 6 left SMs short of loads in flight, 43.
-constexpr int kRopeWarps = 24;
+// (8191 tokens written as int8 and read back, 48 heads of 128: 45 us with 6 or 12 warps, 47 with 24, 49
+// with 48: more threads make the same angles again.  8198 tokens of fp32 gradients, 40 heads of 64: 41 us
+// with 6, 31 from 12 on: fewer leave SMs short of loads in flight.)
+constexpr int kRopeWarps = 12;
 
 unsigned rope_split(long long tokens, int heads, int d, int num_sms, int *groups, int *per_group) {
   const long long warps = std::max(1LL, tokens * (d / 16) / 32);

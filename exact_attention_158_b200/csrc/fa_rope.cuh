@@ -9,11 +9,11 @@
 // formed in fp64 and only its fraction, in [-1/2, 1/2], goes to fp32, the rest (2^-26 turns) as a
 // first-order correction of the sine and cosine.
 //
-// Bound: HBM, each element read and written once.  A thread keeps one token and one chunk of eight
-// pairs for all the heads it takes, so the eight angles it needs are made once, in registers, and
+// Bound: HBM, each element read and written once.  A thread keeps one token and eight pairs
+// for all the heads it takes, so the eight angles it needs are made once, in registers, and
 // nothing is shared: no table, no barrier, every warp runs by itself.  (With a table in shared memory,
 // made by the CTA behind a barrier, B8 H16+16 N2048 d128 took 57 to 78 us, 45 this
-// way: 5960 GB/s.)
+// way: 6000 GB/s.)
 // 16-byte accesses, whole rows of 128 to 512 bytes by the HD / 16 threads of a row; the four or eight
 // tokens of a warp are neighbours, so the head-major side moves 1 to 2 KB at a time.
 #pragma once
@@ -206,7 +206,9 @@ struct RopeParams {
 template <int HD, class In, class Out>
 __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams p) {
   constexpr int kChunks = HD / 16, P = kRopePiece<In>;
-  constexpr int kUnroll = sizeof(In) == 4 ? 2 : 4;  // rows on their way at once
+  // rows on their way at once: four of fp32 cost registers, so warps (8198 tokens, 40 heads of 64: 35 us
+  // where two take 31); of bf16 they hide more (B8 H16+16 N2048 d128 back to back: 49 us, two 51)
+  constexpr int kUnroll = sizeof(In) == 4 ? 2 : 4;
   const unsigned long long gid = static_cast<unsigned long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
   const int chunk = static_cast<int>(gid % kChunks);
   const unsigned long long rest = gid / kChunks;
