@@ -154,6 +154,12 @@ __device__ __forceinline__ float q8_lse(float M, float l) {
   return ((M + static_cast<float>(k)) + lg2(f)) * 0.6931471805599453f;
 }
 
+// (m, l) of a chunk whose CTA gave up a wait: it makes the rows that it is joined into NaN.
+__device__ __forceinline__ float2 q8_no_partial() {
+  const float nan = __int_as_float(0x7fc00000);
+  return make_float2(nan, nan);
+}
+
 // Four features of an output row from its sums: O = a / l, LSE = ln 2 (M + log2 l); a row that saw
 // no token has l = 0 and gets O = 0, LSE = -inf.
 template <int HD>
@@ -305,7 +311,17 @@ __global__ void __launch_bounds__(kQ8Threads, (HD == 128 ? 5 : 6) - NT)
   uint32_t phase = 0;
 #pragma unroll 1
   for (int i = 0; i < n_mine; ++i) {
-    if (!mbar_wait(my_bars + st, phase, &abort_flag)) break;
+    if (!__all_sync(0xffffffffu, mbar_wait(my_bars + st, phase, &abort_flag))) {
+      // given up: the pages asked for land (or this gives up too) before their memory is used again
+      if (lane == 0) {
+        volatile int never = 0;
+        for (int k = i; k < min(i + C::kStages, n_mine); ++k) {
+          mbar_wait(my_bars + st, phase, &never);
+          if (++st == C::kStages) st = 0, phase ^= 1;
+        }
+      }
+      break;
+    }
     const uint8_t *kp = my_ring + st * C::kStage, *vp = kp + C::kSlab;
     const float *sp = my_scales + st * 2 * kQ8Page;
     const bool named = (live >> st) & 1;
@@ -507,7 +523,13 @@ __global__ void __launch_bounds__(kQ8Threads, (HD == 128 ? 5 : 6) - NT)
         sm_l[warp][8 * nt + 2 * c + e] = x;
       }
     }
-  __syncthreads();  // (every warp has consumed its own loads: the ring is free)
+  __syncthreads();  // (no load is on its way any more: the ring is free)
+  if (const volatile int *gave_up = &abort_flag; *gave_up) {
+    // reported already; nothing is written but what makes the joined rows NaN
+    if (p.n_split > 1 && threadIdx.x < kRows && row0 + static_cast<int>(threadIdx.x) < p.R)
+      p.ws_ml[(row_base + row0 + threadIdx.x) * p.n_split + split] = q8_no_partial();
+    return;
+  }
   float *part = reinterpret_cast<float *>(ring);  // [warp][row][HD]
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)

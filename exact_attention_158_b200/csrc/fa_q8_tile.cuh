@@ -696,6 +696,7 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
         }
       }
       q8_sides_barrier();
+      ok = ok && *abort_flag == 0;  // the other side's waits too
       if (side == 0 && warp_rows && ok) {
         const float m1 = xm[lrow], l1 = xm[128 + lrow];
         poison = poison || xm[256 + lrow] != 0.f;
@@ -739,6 +740,8 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
         __syncwarp();
       }
     }
+    // given up (and reported): nothing is written but what makes the joined rows NaN
+    if (!ok && mine && p.n_split > 1) p.ws_ml[(row_base + row) * p.n_split + split] = q8_no_partial();
   }
   __syncwarp();
   tc_fence_before();
