@@ -1024,6 +1024,86 @@ Span row_span(const void *x, const long long *strides, int T, int H, int d) {
   return Span{static_cast<const char *>(x) + 2 * lo, static_cast<size_t>(hi - lo) * 2};
 }
 
+using Wide = __int128;  // strides are the caller's and may be anything
+
+// Strided rows: `bytes` contiguous bytes at p + sum of i_a s_a for all 0 <= i_a < n_a, strides in bytes.
+struct Rows {
+  const void *p;
+  long long bytes, n[3];
+  Wide s[3];
+};
+
+// Is there a sum r + sum of i_a s_a (0 <= i_a < n_a, s_a >= 0) in (lo, hi)?  Dimensions are taken with the
+// largest stride first, where only the i_a that leave the interval in reach of the rest are followed:
+// one or two per dimension in layouts whose dimensions lie inside one another, as all dense ones and
+// slices of them do.  What is not decided in kRowSteps steps counts as found.
+struct RowDim {
+  Wide n, s;
+};
+constexpr int kRowSteps = 1 << 12;
+
+bool sum_within(Wide r, const RowDim *dim, int dims, Wide lo, Wide hi, int *steps) {
+  if (++*steps > kRowSteps) return true;
+  if (dims == 0) return r > lo && r < hi;
+  Wide rest = 0;
+  for (int a = 1; a < dims; ++a) rest += (dim[a].n - 1) * dim[a].s;
+  auto floor_div = [](Wide a, Wide b) { return a / b - (a % b < 0); };
+  const Wide s = dim[0].s;
+  const Wide first = std::max<Wide>(0, floor_div(lo - rest - r, s) + 1);
+  const Wide last = std::min<Wide>(dim[0].n - 1, floor_div(hi - 1 - r, s));
+  for (Wide i = first; i <= last; ++i)
+    if (sum_within(r + i * s, dim + 1, dims - 1, lo, hi, steps)) return true;
+  return false;
+}
+
+// The same with strides of any sign, in any order.
+bool any_sum_within(Wide r, const RowDim *in, int count, Wide lo, Wide hi) {
+  RowDim dim[6];
+  int dims = 0;
+  for (int a = 0; a < count; ++a) {
+    RowDim x = in[a];
+    if (x.s < 0) {  // counted from its other end
+      r += (x.n - 1) * x.s;
+      x.s = -x.s;
+    }
+    if (x.n <= 1 || x.s == 0) continue;
+    int b = 0;
+    while (b < dims && dim[b].s != x.s) ++b;
+    if (b < dims) dim[b].n += x.n - 1;  // two indices of one stride are one
+    else dim[dims++] = x;
+  }
+  std::sort(dim, dim + dims, [](const RowDim &a, const RowDim &b) { return a.s > b.s; });
+  int steps = 0;
+  return sum_within(r, dim, dims, lo, hi, &steps);
+}
+
+// Does a row of x share a byte with a row of y?
+bool rows_meet(const Rows &x, const Rows &y) {
+  RowDim dim[6];
+  for (int a = 0; a < 3; ++a) {
+    dim[a] = RowDim{x.n[a], x.s[a]};
+    dim[3 + a] = RowDim{y.n[a], -static_cast<Wide>(y.s[a])};
+  }
+  const Wide r = static_cast<Wide>(reinterpret_cast<uintptr_t>(x.p)) - static_cast<Wide>(reinterpret_cast<uintptr_t>(y.p));
+  return any_sum_within(r, dim, 6, -static_cast<Wide>(x.bytes), y.bytes);
+}
+
+// Do two different rows of x share a byte?  The first index in which they differ is the larger one's.
+bool rows_meet_themselves(const Rows &x) {
+  for (int a = 0; a < 3; ++a) {
+    RowDim dim[3];
+    Wide r = x.s[a];
+    dim[0] = RowDim{static_cast<Wide>(x.n[a]) - 1, x.s[a]};
+    if (x.n[a] < 2) continue;
+    for (int b = a + 1; b < 3; ++b) {
+      r -= (static_cast<Wide>(x.n[b]) - 1) * x.s[b];
+      dim[b - a] = RowDim{2 * static_cast<Wide>(x.n[b]) - 1, x.s[b]};
+    }
+    if (any_sum_within(r, dim, 3 - a, -static_cast<Wide>(x.bytes), x.bytes)) return true;
+  }
+  return false;
+}
+
 // How the heads of a token are split over threads: not at all where the tokens alone give every SM
 // kRopeWarps warps, else into as many groups as that takes, down to one head each (a decode step).
 // (8191 tokens written as int8 and read back, 48 heads of 128: 45 us with 6 or 12 warps, 47 with 24, 49
@@ -1344,12 +1424,28 @@ fa_status fa_rope(const void *q, const long long *q_strides, void *q_out,
     p.x[i].H = heads[i];
     for (int a = 0; a < 3; ++a) {
       if (is[i][a] % in_unit || os[i][a] % out_unit) return FA_ERR_ALIGNMENT;
-      // rows of the output may not lie on one another
-      const long long n = a == 1 ? heads[i] : extent[a];
-      if (n > 1 && std::llabs(os[i][a]) < d) return FA_ERR_INVALID_ARG;
       p.x[i].in_s[a] = is[i][a];
       p.x[i].out_s[a] = os[i][a];
     }
+  }
+  // what is written lies neither on itself nor on anything read (but the same tensor in place) or written
+  auto rows_of = [&](const void *x, const long long *strides, int i, fa_out_dtype type) {
+    const long long e = type == FA_OUT_F32 ? 4 : 2;
+    Rows r{x, d * e, {B, heads[i], N}, {}};
+    for (int a = 0; a < 3; ++a) r.s[a] = (a == 1 ? heads[i] : extent[a]) > 1 ? static_cast<Wide>(strides[a]) * e : 0;
+    return r;
+  };
+  for (int i = 0; i < 2; ++i) {
+    if (heads[i] == 0) continue;
+    const Rows y = rows_of(out[i], os[i], i, out_dtype);
+    if (rows_meet_themselves(y)) return FA_ERR_INVALID_ARG;
+    for (int j = 0; j < 2; ++j) {
+      if (heads[j] == 0) continue;
+      if (!(i == j && in[i] == out[i]) && rows_meet(y, rows_of(in[j], is[j], j, in_dtype))) return FA_ERR_INVALID_ARG;
+      if (j > i && rows_meet(y, rows_of(out[j], os[j], j, out_dtype))) return FA_ERR_INVALID_ARG;
+    }
+    if (rot > 0 && rows_meet(y, Rows{positions, 4LL * N, {B, 1, 1}, {4 * static_cast<Wide>(pos_stride), 0, 0}})) return FA_ERR_INVALID_ARG;
+    if (rot > 0 && rows_meet(y, Rows{freqs, 4LL * rot, {1, 1, 1}, {}})) return FA_ERR_INVALID_ARG;
   }
   fa_status st = check_rope(positions, freqs, rot, layout, amplitude, d, inverse, &p.table);
   if (st != FA_OK) return st;

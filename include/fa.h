@@ -291,8 +291,9 @@ fa_status fa_decode_paged_noalloc(const void *q, const void *k_pool, const void 
  *                  q_out_strides[3] (host arrays), features contiguous: a projection's
  *                  [B, N, heads, d] is read and attention's [B, H, N, d] written without a copy, or
  *                  the other way round.  Input and output may be the same tensor (same pointer,
- *                  strides and type); otherwise they must not overlap.  Output strides of a
- *                  dimension longer than 1 are at least d in magnitude.
+ *                  strides and type).  Otherwise no row of an output may share memory with another
+ *                  row that is written, or with anything read (FA_ERR_INVALID_ARG); rows that only
+ *                  alternate in one buffer, as a projection's q and k do, share none.
  *   k, k_out       the same with Hk heads (Hk = 0: none, pointers ignored).
  *   in_dtype, out_dtype   bf16 or fp32, for q and k alike.
  *   positions      int32, device: position of (b, n) at positions[b * pos_stride + n] (pos_stride 0:
