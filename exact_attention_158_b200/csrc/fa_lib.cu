@@ -1490,7 +1490,6 @@ fa_status fa_cache_append(const void *k, const long long *k_strides, const void 
   for (int i = 0; i < (Hq > 0 ? 4 : 2); ++i)
     for (int a = 0; a < 2; ++a) {
       if (strides[i][a] % 8) return FA_ERR_ALIGNMENT;
-      if (i == 3 && (a == 0 ? T : Hq) > 1 && std::llabs(strides[i][a]) < d) return FA_ERR_INVALID_ARG;
       to[i][a] = strides[i][a];
     }
   p.q = static_cast<const uint16_t *>(q);
@@ -1510,9 +1509,24 @@ fa_status fa_cache_append(const void *k, const long long *k_strides, const void 
   if (Hq > 0 && q == q_out)  // in place is the same tensor
     for (int a = 0; a < 2; ++a)
       if ((a == 0 ? T : Hq) > 1 && q_strides[a] != q_out_strides[a]) return FA_ERR_INVALID_ARG;
-  // the pools and scales are written: they may lie neither on one another nor on the rows read or
-  // written beside them (a strided tensor counts from its first to its last element); q_out in turn
-  // not on the slots and positions
+  // q_out is written: like fa_rope's outputs it lies neither on itself nor on anything read, but for q
+  // in place
+  auto rows_of = [&](const void *x, const long long *st, int heads) {
+    return Rows{x, 2LL * d, {T, heads, 1}, {T > 1 ? 2 * static_cast<Wide>(st[0]) : 0,
+                                            heads > 1 ? 2 * static_cast<Wide>(st[1]) : 0, 0}};
+  };
+  if (Hq > 0) {
+    const Rows y = rows_of(q_out, q_out_strides, Hq);
+    if (rows_meet_themselves(y) || rows_meet(y, rows_of(k, k_strides, Hk)) || rows_meet(y, rows_of(v, v_strides, Hk)))
+      return FA_ERR_INVALID_ARG;
+    if (q != q_out && rows_meet(y, rows_of(q, q_strides, Hq))) return FA_ERR_INVALID_ARG;
+    if (rows_meet(y, Rows{slots, 8LL * T, {1, 1, 1}, {}})) return FA_ERR_INVALID_ARG;
+    if (rot > 0 && (rows_meet(y, Rows{positions, 4LL * T, {1, 1, 1}, {}}) ||
+                    rows_meet(y, Rows{freqs, 4LL * rot, {1, 1, 1}, {}})))
+      return FA_ERR_INVALID_ARG;
+  }
+  // the pools and scales are written: they may lie neither on one another nor on what is read or
+  // written beside them (a strided tensor counts from its first to its last element)
   const size_t rows = static_cast<size_t>(num_blocks) * Hk * fa::kCachePage;
   const size_t pool_bytes = rows * d * (type == FA_CACHE_BF16 ? 2 : 1);
   const size_t scale_bytes = type == FA_CACHE_BF16 ? 0 : rows * 4;
@@ -1521,18 +1535,16 @@ fa_status fa_cache_append(const void *k, const long long *k_strides, const void 
   const Span kx = row_span(k, k_strides, T, Hk, d), vx = row_span(v, v_strides, T, Hk, d);
   const Span qx = Hq > 0 ? row_span(q, q_strides, T, Hq, d) : Span{nullptr, 0};
   const Span qox = Hq > 0 ? row_span(q_out, q_out_strides, T, Hq, d) : Span{nullptr, 0};
-  const void *ins[6] = {slots, positions, kx.p, vx.p, qx.p, qox.p};
-  const size_t in_bytes[6] = {static_cast<size_t>(T) * 8, rot ? static_cast<size_t>(T) * 4 : 0,
-                              kx.bytes, vx.bytes, qx.bytes, qox.bytes};
+  const void *ins[7] = {slots, positions, freqs, kx.p, vx.p, qx.p, qox.p};
+  const size_t in_bytes[7] = {static_cast<size_t>(T) * 8, rot ? static_cast<size_t>(T) * 4 : 0,
+                              static_cast<size_t>(rot) * 4, kx.bytes, vx.bytes, qx.bytes, qox.bytes};
   for (int a = 0; a < 4; ++a) {
     if (out_bytes[a] == 0) continue;
-    for (int b = 0; b < 6; ++b)
+    for (int b = 0; b < 7; ++b)
       if (in_bytes[b] && overlaps(outs[a], out_bytes[a], ins[b], in_bytes[b])) return FA_ERR_INVALID_ARG;
     for (int b = a + 1; b < 4; ++b)
       if (out_bytes[b] && overlaps(outs[a], out_bytes[a], outs[b], out_bytes[b])) return FA_ERR_INVALID_ARG;
   }
-  for (int b = 0; b < 2; ++b)
-    if (Hq > 0 && in_bytes[b] && overlaps(qox.p, qox.bytes, ins[b], in_bytes[b])) return FA_ERR_INVALID_ARG;
   DeviceInfo *dev = nullptr;
   int dev_id = 0;
   if ((st = current_device(&dev, &dev_id)) != FA_OK) return st;

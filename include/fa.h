@@ -337,7 +337,9 @@ fa_status fa_rope(const void *q, const long long *q_strides, void *q_out,
  *   k_scale, v_scale   as above for FA_CACHE_E4M3 and FA_CACHE_INT8; ignored (may be null) for
  *                  FA_CACHE_BF16.
  *   q, q_out       bf16 [T, Hq, d] with strides as k (Hq = 0: none, pointers ignored); every token's
- *                  q is rotated, padding too.  May be the same tensor (same pointer and strides).
+ *                  q is rotated, padding too.  May be the same tensor (same pointer and strides);
+ *                  otherwise q_out's rows may share memory neither with one another nor with
+ *                  anything read (FA_ERR_INVALID_ARG), as in fa_rope.
  *   positions      int32 [T], device;  freqs, rot, layout, amplitude as for fa_rope (rot = 0: no
  *                  rotation, positions and freqs may be null).
  *   T >= 0 (nothing is launched for 0), Hk >= 1, Hq >= 0;  d: 64 or 128;  (num_blocks + 1) * Hk <=

@@ -5,6 +5,7 @@ import itertools
 import random
 
 import pytest
+import torch
 
 import exact_attention_158_b200 as fa
 from exact_attention_158_b200 import build as fab
@@ -101,3 +102,28 @@ def test_rope_against_every_pair_of_rows(lib):
         assert got == (INVALID if meet or (p == y and not same) else MISALIGNED), (B, H, N, strides, y - p)
         seen[got] += 1
     assert min(seen.values()) > 300
+
+
+def append(lib, k, ks, v, vs, q=None, qs=(0, 0), qo=None, qos=(0, 0), T=4, Hq=0, Hk=2, pos=1 << 41,
+           fr=1 << 42, slots=1 << 43, rot=16, vp=1 << 45, kp=1 << 44):
+    return lib.fa_cache_append(k, st(ks), v, st(vs), kp, vp, 1 << 46, 1 << 47, 1, slots, 8, q, st(qs), qo,
+                               st(qos), pos, fr, rot, 0, 1.0, T, Hq, Hk, D, None)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="a call that is not refused would be launched")
+def test_append_queries_over_what_is_read(lib):
+    T, Hq, Hk = 4, 6, 2
+    W = (Hq + 2 * Hk) * D
+    k, v, q = A + 2 * Hq * D, A + 2 * (Hq + Hk) * D, A
+    s = (W, D)
+    a = dict(k=k, ks=s, v=v, vs=s, q=q, qs=s, T=T, Hq=Hq, Hk=Hk)
+    dense = (Hq * D, D)
+    assert append(lib, qo=k, qos=dense, **a) == INVALID          # over k
+    assert append(lib, qo=v, qos=dense, **a) == INVALID          # over v
+    assert append(lib, qo=q + 2 * D, qos=s, **a) == INVALID      # q, one head further on
+    assert append(lib, qo=q + 2 * W, qos=s, **a) == INVALID      # q, one token further on
+    assert append(lib, qo=2 * A, qos=(D, D), **a) == INVALID     # over itself
+    assert append(lib, qo=2 * A, qos=(2 * D, 3 * D), **dict(a, T=4)) == INVALID  # rows 0, 3 and 2, 1 meet
+    for name in ("slots", "pos", "fr"):
+        assert append(lib, qo=2 * A, qos=dense, **dict(a, **{name: 2 * A + 64})) == INVALID, name
+    assert append(lib, qo=2 * A, qos=dense, **dict(a, fr=(1 << 44) + 64)) == INVALID  # the pool over freqs

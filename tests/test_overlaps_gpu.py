@@ -24,3 +24,34 @@ def test_rotating_a_fused_projection_in_place(dtype, layout):
         fa.fa_rope(q, k, pos, freqs, layout, q_out=q, k_out=x[:, :, 1:1 + Hk].transpose(1, 2))
     with pytest.raises(fa.FaError):
         fa.fa_rope(q[:, :, 1:], None, pos[:, 1:].contiguous(), freqs, layout, q_out=q[:, :, :-1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float8_e4m3fn, torch.int8])
+def test_queries_of_a_fused_projection_in_place(dtype):
+    import exact_attention_158_b200 as fa
+    T, Hq, Hk, d = 37, 6, 2, 64
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn((T, Hq + 2 * Hk, d), generator=g, device="cuda").to(torch.bfloat16)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") + 900
+    slots = torch.randperm(64, generator=g, device="cuda")[:T]
+    freqs, amp = fa.rope_frequencies(64)
+    q, k, v = x[:, :Hq], x[:, Hq:Hq + Hk], x[:, Hq + Hk:]
+    kv = x[:, Hq:].clone()
+
+    def call(**kw):
+        pools = [torch.zeros((4, Hk, 16, d), device="cuda").to(dtype) for _ in range(2)]
+        scales = [None if dtype == torch.bfloat16 else torch.zeros((4, Hk, 16), device="cuda") for _ in range(2)]
+        y = fa.fa_cache_append(k, v, *pools, slots, *scales, pos, freqs, q=q, **kw)
+        return y, fa.fa_cache_read(*pools, slots, *scales)
+
+    # head-major beside token-major: the rows alternate, and share nothing
+    room = torch.zeros((Hq, 2 * T, d), dtype=torch.bfloat16, device="cuda")
+    want, want_kv = call()
+    got, _ = call(q_out=room[:, ::2].transpose(0, 1))
+    assert torch.equal(got, want) and torch.equal(room[:, 1::2], torch.zeros_like(room[:, 1::2]))
+    for q_out in (x[:, 1:1 + Hq], x[:, Hk * 2:Hk * 2 + Hq], want[:1].expand(T, -1, -1)):
+        with pytest.raises(fa.FaError):
+            call(q_out=q_out)
+    got, got_kv = call(q_out=q)
+    assert torch.equal(q, want) and torch.equal(x[:, Hq:], kv)
+    assert all(torch.equal(a, b) for a, b in zip(got_kv, want_kv))
