@@ -11,8 +11,10 @@
 // bf16's 2^-8); sums and statistics are fp32.
 // The reference m_r is chosen for that product: the largest s + log2 vs so far, so that the largest
 // p vs lies near 1 and fp16 loses 2^-25 of it at most, whatever the scales are.  It moves only when a
-// p vs passes 2^10 (fp16 ends at 2^16) or a p 2^100 (the fp32 sum; values of scale 0 set no
-// reference, so the scores hold one 2^64 below their own maximum).
+// p vs passes 2^10 (fp16 ends at 2^16) or the sum of p 2^112 (it is fp32, and a warp may add 2^16
+// tokens).  A score holds the reference no further below itself than 2^96, which leaves the smallest
+// scale the cache keeps, 2^-109, a p vs of 2^-13; a value of scale 0, which asks for no reference,
+// 2^60: the further away, the coarser a score's fp32 difference to it (2^-19 there).
 //
 // Bound: HBM.  Each warp walks its own pages (16 tokens of one head: 16 d bytes of K, as many of V,
 // 64 bytes of scales each), kept a few ahead in shared memory by TMA; a chunk of the context is
@@ -32,9 +34,9 @@ namespace fa {
 constexpr int kQ8Page = 16;
 constexpr int kQ8Warps = 4;
 constexpr int kQ8Threads = 32 * kQ8Warps;
-constexpr float kQ8MostPv = 0x1p10f, kQ8MostP = 0x1p100f;  // past these the reference moves
+constexpr float kQ8MostPv = 0x1p10f, kQ8MostP = 0x1p112f;  // past these the reference moves
 constexpr uint32_t kQ8MostPvBits = 0x6400u;                // 2^10 in fp16
-constexpr float kQ8Slack = 64.f;                           // log2: p stays below 2^64 after a move
+constexpr float kQ8Far = 96.f, kQ8FarZero = 60.f;          // log2: how far below a score the reference may lie
 
 enum Q8Type { kQ8E4m3 = 1, kQ8Int8 = 2 };
 
@@ -468,7 +470,7 @@ __global__ void __launch_bounds__(kQ8Threads, (HD == 128 ? 5 : 6) - NT)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const float y = sa[nt][2 * r + e];
-            if (y != -INFINITY) x = fmaxf(x, fmaxf(y - kQ8Slack, y + lv[r]));
+            if (y != -INFINITY) x = fmaxf(x, lv[r] == -INFINITY ? y - kQ8FarZero : y + fmaxf(lv[r], -kQ8Far));
           }
           float go = mine ? 1.f : 0.f;
 #pragma unroll
