@@ -146,6 +146,14 @@ struct Q8Cfg {
   static constexpr int kSmem = kRing + kScales + kBars + 1024;  // + alignment of the ring
 };
 
+// x 2^d for d <= 0.  For the sums l: they count scores against references that hold the values' scales too,
+// so a reference may move by more than 2^126 (from values of scale 0 to loud ones) under a sum that stays a
+// normal number, where 2^d alone does not.  (The output's sums follow the references: ex2(d) serves them.)
+__device__ __forceinline__ float q8_shift(float x, float d) {
+  const float half = ex2(0.5f * d);
+  return x * half * half;
+}
+
 // ln 2 (M + log2 l).  M holds the values' log2 vs, which l undoes: l's exponent is added to M first
 // (small numbers of opposite sign), and only the fraction's logarithm is approximated.
 __device__ __forceinline__ float q8_lse(float M, float l) {
@@ -480,9 +488,10 @@ __global__ void __launch_bounds__(kQ8Threads, (HD == 128 ? 5 : 6) - NT)
           }
           if (go == 0.f) continue;
           const float mn = fmaxf(m[nt][e], x);
-          const float a = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - mn);
+          const bool first = m[nt][e] == -INFINITY;
+          const float a = first ? 0.f : ex2(m[nt][e] - mn);
+          l[nt][e] = first ? l[nt][e] * 0.f : q8_shift(l[nt][e], m[nt][e] - mn);
           m[nt][e] = mn;
-          l[nt][e] *= a;
 #pragma unroll
           for (int j = 0; j < kMT; ++j) {
             acc[nt][j][e] *= a;
@@ -562,7 +571,7 @@ __global__ void __launch_bounds__(kQ8Threads, (HD == 128 ? 5 : 6) - NT)
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kQ8Warps; ++w) {
-      if (sm_l[w][row] != 0.f) sum += ex2(sm_m[w][row] - M) * sm_l[w][row];
+      if (sm_l[w][row] != 0.f) sum += q8_shift(sm_l[w][row], sm_m[w][row] - M);
       const float4 x = *reinterpret_cast<const float4 *>(part + (w * kRows + row) * HD + e0);
       a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
     }
@@ -576,7 +585,7 @@ __global__ void __launch_bounds__(kQ8Threads, (HD == 128 ? 5 : 6) - NT)
   }
 }
 
-// Joins the chunks of every row: M = max m_c, l = sum 2^(m_c - M) l_c, O = sum 2^(m_c - M) O_c / l; a
+// Joins the chunks of every row: M = max m_c, l = sum 2^(m_c - M) l_c (q8_shift), O = sum 2^(m_c - M) O_c / l; a
 // chunk without a visible token has l = 0 and takes no part.
 //
 // kWide: a CTA per row, for few rows or many chunks (one long context), where a thread that walked the
@@ -608,7 +617,7 @@ __global__ void __launch_bounds__(256) fa_q8_combine_kernel(const Q8Params p) {
       const float2 x = ml[i];
       if (x.y == 0.f) continue;
       const float f = ex2(x.x - M);
-      sum = fmaf(f, x.y, sum);
+      sum += q8_shift(x.y, x.x - M);
       add(f, *reinterpret_cast<const float4 *>(po + static_cast<size_t>(i) * HD));
     }
     q8_write4<HD>(p, row, e0, a, M, sum);
@@ -628,7 +637,7 @@ __global__ void __launch_bounds__(256) fa_q8_combine_kernel(const Q8Params p) {
       const float2 x = ml[i];
       const float f = x.y == 0.f ? 0.f : ex2(x.x - M);
       weight[i] = f;
-      if (x.y != 0.f) sum = fmaf(f, x.y, sum);
+      if (x.y != 0.f) sum += q8_shift(x.y, x.x - M);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);

@@ -120,6 +120,22 @@ def test_values_of_a_few_binades_above_the_smallest_kept(dtype, Hq, Hk, T, S, L)
 
 
 @pytest.mark.parametrize("Hq,Hk,T", FEW)
+@pytest.mark.parametrize("S,L", [(2, 333), (1, 2500)])
+@pytest.mark.parametrize("up", [20, 70, 110])
+def test_a_loud_token_among_values_of_zero(Hq, Hk, T, S, L, up):
+    # zeros set no reference, so theirs lies far below the loud token's: their weights still count
+    for first in (5, L // 2, L - 9):
+        a = make(2, S, Hq, Hk, 64, L, INT8, T)
+        a[4] *= 0
+        scale = a[4][:, :, 0].clone().fill_(2.0 ** up)
+        n = a[5].shape[1]
+        for s in range(S):
+            a[4][s * n + first // 16, :, first % 16] = scale[0]
+        a[0] *= 0.25
+        verify(a, f"loud at {first}", causal=T is not None)
+
+
+@pytest.mark.parametrize("Hq,Hk,T", FEW)
 def test_values_of_zero_alone(Hq, Hk, T):
     a = make(3, 2, Hq, Hk, 64, 700, E4M3, T)
     a[4] *= 0
