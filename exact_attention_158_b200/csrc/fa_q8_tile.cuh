@@ -10,7 +10,7 @@
 //   warps 8-11   codes -> fp16 K and V tiles in the swizzled layout the tensor core reads
 //   warps 12-13  products: one thread issues for each side
 //   warp  14     codes out of the pool by bulk copies, three tiles ahead
-//   warp  15     a tile's scales, live tokens and F
+//   warp  15     a tile's scales and live tokens
 // TMEM (512 columns): S [side][2] x 64, then O [side] x d.  With more than 128 rows the sides hold two
 // row tiles; with fewer they share one row tile and take the tiles of tokens in turn.  A side's S is
 // double, so Q K^T of the next tile and P V of the last run during its softmax.  (With 128-token tiles S
@@ -18,17 +18,20 @@
 // per 128 tokens and two row tiles against 5300 here, and 4500 against 3600 with one row tile.)
 //
 // Scales.  A key's scale multiplies its column of scores in fp32, read from shared memory by every
-// row (16 broadcast 16-byte loads per row and tile).  A value's scale is folded into V instead, which
-// saves as many loads and a multiplication per score: V = code * f in fp16, f = vs 2^a / F with F a
-// power of two no smaller than any vs so far; O is rescaled when F has to grow.  f and the product
-// are rounded to fp16 (2^-11 each, like p).  V uses fp16 from its top (2^15) down and p from 2^6 to
-// 2^15, so a token whose values are 2^20 times the others' and whose weight is 2^-20 takes nothing from
-// either.  A value scale that is not finite would reach rows that do not see its token as 0 * NaN: V is
-// 0 there, and rows that do see it are marked and written as NaN.
+// row (16 broadcast 16-byte loads per row and tile).  A value's scale vs = f 2^e is split: f goes into V =
+// code * f in fp16, and the power of two into the exponent of p = 2^(s + e - m), whose reference m then
+// follows the largest p vs as in fa_q8.cuh; the row's sum takes p 2^-e.  One e for a tile of tokens (the
+// power of two above its largest vs) costs nothing, so that is the form wherever the tile's scales
+// lie within 2^8 of one another; f is then 2^-9 at least, and a token loses less than 2^-22 of the row's
+// largest p vs.  Else (wide) each token has its own e and p takes a second exponential for the sum: what a
+// loud token would take from f and p of the others does not depend on whether a row sees it.  A tile
+// far below an earlier one is wide too, since 2^(s + e - m) may leave fp32's range where 2^(s - m), which
+// the sum needs, does not.  f, code * f and p are rounded to fp16 (2^-11 each).  A value scale that is not finite would reach rows that do
+// not see its token as 0 * NaN: V is 0 there, and rows that do see it are marked and written as NaN.
 //
-// A row's softmax is one pass over its scores in registers: p = 2^(s ks - m) against the reference it
+// A row's softmax is one pass over its scores in registers: p = 2^(s ks + e - m) against the reference it
 // has; where one passes 2^15, and on a row's first tile, the reference moves so that the largest p is
-// 2^6, and O is rescaled in TMEM (as it is when F has grown).
+// 2^6, and O is rescaled in TMEM.
 //
 // Queries go to fp16 against one power of two for all rows of the CTA (q8_q_unit; it is part of the key
 // scales).  int8's conversion leaves every four features in the order 0, 2, 1, 3; q is stored in that
@@ -53,7 +56,12 @@ constexpr int kQ8MostVBufs = 4;
 constexpr int kQ8CodeBufs = 3;              // tiles of codes on their way
 constexpr float kQ8TileMost = 15.f;         // log2 of the largest p: fp16 ends at 2^16
 constexpr float kQ8TileStart = 6.f;         // and after the reference has moved
-// f at the largest vs: e4m3 codes are at most 448, int8 codes 127
+constexpr int kQ8TileNear = 8;              // log2 of how far a tile's scales may lie apart and share one e,
+constexpr int kQ8TileFar = 64;              // and of how far below an earlier tile's they may lie
+// e's range: 2^-89 leaves the smallest scale, 2^-109, f = 2^-20, and a row's sum of p 2^-e in fp32's
+// range; 2^126 is the largest whose inverse is a normal number
+constexpr int kQ8LeastE = -89, kQ8MostE = 126;
+// f = 1 as V holds it: e4m3 codes are at most 448, int8 codes 127
 template <int kType> __device__ constexpr float q8_vtop() { return kType == kQ8E4m3 ? 0x1p6f : 0x1p8f; }
 
 template <int HD>
@@ -66,11 +74,11 @@ struct Q8TileCfg {
   static constexpr int kCodeBytes = kQ8Tok * HD;      // of K or V of one tile
   static constexpr int kScaleBufs = 8;
   static constexpr int kBars = 2 * kQ8KBufs + 2 * kQ8MostVBufs + 2 * kQ8CodeBufs + 2 * kScaleBufs + 4 + 4 + 4 + 2 + 2;
-  // Q (two row tiles, or one and two more V tiles in its place), K and V tiles, codes, scales (ks, f, live
-  // and bad tokens, F)
+  // Q (two row tiles, or one and two more V tiles in its place), K and V tiles, codes, scales (ks, f, e, live
+  // and bad tokens, the tile's)
   static_assert(kQBytes == 2 * kTileBytes, "two V tiles in the place of a row tile's Q");
   static constexpr size_t kNeed = 1024 + 2 * kQBytes + (kQ8KBufs + 2) * kTileBytes +
-                                  2 * kQ8CodeBufs * kCodeBytes + kScaleBufs * (kQ8Tok * 8 + 32) + kBars * 8 + 48;
+                                  2 * kQ8CodeBufs * kCodeBytes + kScaleBufs * (kQ8Tok * 12 + 32) + kBars * 8 + 48;
   static constexpr size_t kSmem = kNeed > 116 * 1024 ? kNeed : 116 * 1024;
   static constexpr uint32_t kColO = 256;  // S: [side][2] x 64 columns before it
   // fp16 operands: the type fields of A and B are 0
@@ -105,15 +113,33 @@ __device__ __forceinline__ void q8_pin(float (&x)[32]) {
   for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(x[i]));
 }
 
+// The power of two above vs, as its exponent in e's range.
+__device__ __forceinline__ int q8_e(float vs) {
+  return min(max(static_cast<int>((__float_as_uint(vs) >> 23) & 0xffu) - 126, kQ8LeastE), kQ8MostE);
+}
+__device__ __forceinline__ float q8_pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// Where a lane's largest p passes 2^15, or its row has seen nothing yet, its reference moves so that the
+// largest is 2^6: m and l follow, `a` is multiplied by what O needs, and the step is returned (0: none).
+// (a row that has seen nothing has l = 0; an infinite score makes its row NaN through inf - inf)
+__device__ __forceinline__ float q8_move(float t, bool over, float &m, float &l, float &a) {
+  const float d = over ? t - kQ8TileStart : 0.f;
+  if (l != 0.f) {
+    l = q8_shift(l, -d);
+    a *= ex2(-d);
+  }
+  m += d;
+  return d;
+}
+
 // A row's 64 scores (TMEM) -> p in fp16 (TMEM, over the scores: token pairs in the first 32 columns) and
 // the sum of p.  k: the tokens that the row sees (kMasked: not all of them).  m and l are the row's
-// reference and sum so far; where the reference has to move, l is brought to the new one and `a` is
-// multiplied by what O needs.  All scores are in registers at once and the steps are kept apart
-// (arguments, largest, exponentials): taken a few at a time, each few wait for their loads of ks.
+// reference and sum so far, e is the tile's.  All scores are in registers at once and the steps are kept
+// apart (arguments, largest, exponentials): taken a few at a time, each few wait for their loads of ks.
 template <bool kMasked>
-__device__ __forceinline__ float q8_weigh(uint32_t s_tmem, const uint32_t (&k)[2], const float *ks, float &m,
+__device__ __forceinline__ float q8_weigh(uint32_t s_tmem, const uint32_t (&k)[2], const float *ks, float e, float &m,
                                           float &l, float &a) {
-  const uint64_t neg2 = f2_pack(-m, -m);
+  const uint64_t off2 = f2_pack(e - m, e - m);
   float x[64];
   tmem_ld32(s_tmem, reinterpret_cast<uint32_t *>(x));
   tmem_ld32(s_tmem + 32, reinterpret_cast<uint32_t *>(x) + 32);
@@ -124,25 +150,20 @@ __device__ __forceinline__ float q8_weigh(uint32_t s_tmem, const uint32_t (&k)[2
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const ulonglong2 f = reinterpret_cast<const ulonglong2 *>(ks)[i];
-    f2_unpack(f2_fma(f2_pack(x[4 * i], x[4 * i + 1]), f.x, neg2), x[4 * i], x[4 * i + 1]);
-    f2_unpack(f2_fma(f2_pack(x[4 * i + 2], x[4 * i + 3]), f.y, neg2), x[4 * i + 2], x[4 * i + 3]);
+    f2_unpack(f2_fma(f2_pack(x[4 * i], x[4 * i + 1]), f.x, off2), x[4 * i], x[4 * i + 1]);
+    f2_unpack(f2_fma(f2_pack(x[4 * i + 2], x[4 * i + 3]), f.y, off2), x[4 * i + 2], x[4 * i + 3]);
     if (kMasked) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        x[4 * i + e] = (k[i / 8] >> (4 * (i % 8) + e)) & 1 ? x[4 * i + e] : -INFINITY;
+      for (int c = 0; c < 4; ++c)
+        x[4 * i + c] = (k[i / 8] >> (4 * (i % 8) + c)) & 1 ? x[4 * i + c] : -INFINITY;
     }
     top[(2 * i) % 4] = fmax3(top[(2 * i) % 4], x[4 * i], x[4 * i + 1]);
     top[(2 * i + 1) % 4] = fmax3(top[(2 * i + 1) % 4], x[4 * i + 2], x[4 * i + 3]);
   }
   const float t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-  // (a row that has seen nothing has l = 0; an infinite score makes its row NaN through inf - inf)
   const bool over = t > kQ8TileMost || (l == 0.f && t != -INFINITY);
   if (__any_sync(0xffffffffu, over)) {
-    const float d = over ? t - kQ8TileStart : 0.f;
-    const float r = l == 0.f ? 1.f : ex2(-d);
-    m += d;
-    l *= r;
-    a *= r;
+    const float d = q8_move(t, over, m, l, a);
     const uint64_t d2 = f2_pack(d, d);
 #pragma unroll
     for (int i = 0; i < 32; ++i)
@@ -161,6 +182,46 @@ __device__ __forceinline__ float q8_weigh(uint32_t s_tmem, const uint32_t (&k)[2
   float u, v;
   f2_unpack(f2_add(sum[0], sum[1]), u, v);
   return u + v;
+}
+
+// The same for a wide tile, with an e per token; returns the sum of p 2^-e.  This form is rare: it reads
+// the scores twice, four at a time in loops, so that neither its registers nor its instructions stand in
+// the others' way (unrolled over 32 scores, tree_batch took 6% longer without ever coming here).
+__device__ __forceinline__ float q8_weigh_wide(uint32_t s_tmem, const uint32_t (&k)[2], const float *ks,
+                                               const float *es, float &m, float &l, float &a) {
+  const uint64_t sees = (static_cast<uint64_t>(k[1]) << 32) | k[0];
+  auto four = [&](int h, float (&x)[4], float (&e)[4]) {  // s + e - m, and e
+    tmem_ld4(s_tmem + h, reinterpret_cast<uint32_t *>(x));
+    tmem_wait_ld();
+    const float4 f = *reinterpret_cast<const float4 *>(ks + h), g = *reinterpret_cast<const float4 *>(es + h);
+    const float fs[4] = {f.x, f.y, f.z, f.w};
+    e[0] = g.x, e[1] = g.y, e[2] = g.z, e[3] = g.w;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      asm volatile("" : "+f"(x[c]));
+      x[c] = (sees >> (h + c)) & 1 ? fmaf(x[c], fs[c], e[c] - m) : -INFINITY;
+    }
+  };
+  float t = -INFINITY, sum = 0.f, x[4], e[4];
+#pragma unroll 1
+  for (int h = 0; h < kQ8Tok; h += 4) {
+    four(h, x, e);
+    t = fmax3(fmax3(t, x[0], x[1]), x[2], x[3]);
+  }
+  q8_move(t, t > kQ8TileMost || (l == 0.f && t != -INFINITY), m, l, a);
+#pragma unroll 1
+  for (int h = 0; h < kQ8Tok; h += 4) {
+    four(h, x, e);
+    uint32_t pk[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      pk[c] = pack_fp16x2(ex2(x[2 * c]), ex2(x[2 * c + 1]));
+      sum += ex2(x[2 * c] - e[2 * c]) + ex2(x[2 * c + 1] - e[2 * c + 1]);
+    }
+    tmem_st2(s_tmem + h / 2, pk);  // over scores that have been read
+    tmem_wait_st();
+  }
+  return sum;
 }
 
 // 32 features of a row, in the conversion's order, from its sums: to the output, or as a partial.
@@ -232,10 +293,11 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
   uint8_t *sC = sV + NV * C::kTileBytes;       // [j % NC]: its codes, K then V, as they lie in the pool
   float *sKs = reinterpret_cast<float *>(sC + 2 * NC * C::kCodeBytes);  // [j % NS][token]: ks scale log2(e)
   uint32_t *sFt = reinterpret_cast<uint32_t *>(sKs + NS * kQ8Tok);      // [j % NS][token]: f in fp16, twice
-  uint16_t *sLive = reinterpret_cast<uint16_t *>(sFt + NS * kQ8Tok);    // [j % NS][page]
+  float *sE = reinterpret_cast<float *>(sFt + NS * kQ8Tok);             // [j % NS][token]: e, of a wide tile
+  uint16_t *sLive = reinterpret_cast<uint16_t *>(sE + NS * kQ8Tok);     // [j % NS][page]
   uint16_t *sBad = sLive + NS * 4;             // [j % NS][page]: live tokens whose vs is not finite
-  float *sF = reinterpret_cast<float *>(sBad + NS * 4);  // [j % NS][4]: F of the tile
-  uint64_t *bars = reinterpret_cast<uint64_t *>(sF + NS * 4);
+  float *sTile = reinterpret_cast<float *>(sBad + NS * 4);  // [j % NS][4]: the tile's e, 2^-e, 1 if it is wide
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sTile + NS * 4);
   // Barriers are indexed as the buffers they guard; the counts are even (or every reader takes every
   // tile), so that a side that waits for every other tile of tokens sees each phase of its own.  A
   // buffer is freed by an arrival from each issuer (or converter warp) that reads it.
@@ -450,14 +512,16 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
     } else {
       // scales: lane i < 16 has tokens 4 i .. 4 i + 3 of the tile
       const float score_scale = p.scale_log2 * q8_inverse(q_unit);
-      float F = 0x1p-126f;
       float4 ks, vs;
+      bool has = false;  // this lane's page is named
+      int e_most = kQ8LeastE;
       int blk = named(0, entry_of(0)), entry = entry_of(1);
       auto fetch = [&](int b4) {
         const int b = __shfl_sync(0xffffffffu, b4, (lane / 4) & 3);
         const size_t at = (static_cast<size_t>(max(b, 0)) * p.Hk + kh) * kQ8Page + 4 * (lane % 4);
         ks = vs = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (b >= 0 && lane < 16) {
+        has = b >= 0 && lane < 16;
+        if (has) {
           ks = *reinterpret_cast<const float4 *>(p.ks + at);
           vs = *reinterpret_cast<const float4 *>(p.vs + at);
         }
@@ -470,23 +534,33 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
         const float4 k4 = make_float4(ks.x * score_scale, ks.y * score_scale, ks.z * score_scale, ks.w * score_scale);
         const int left = L - (j0 + j) * kQ8Tok - kQ8Page * lane;  // and for lane i < 4, of page i
         const uint32_t live = blk < 0 || left <= 0 ? 0u : left >= 16 ? 0xffffu : (1u << left) - 1u;
-        float top = 0.f;  // the tile's largest finite vs
-        bool bad = false;
+        float top = 0.f, low = INFINITY;  // the tile's largest finite vs and its smallest above 0
+        bool bad = false, zero = false;   // live tokens whose vs is not finite, or 0
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
+          const bool alive = has && c < left4;
           if (c >= left4) v[c] = 0.f;  // a slot past the end may hold anything
           const bool fin = fabsf(v[c]) < INFINITY;
           bad = bad || !fin;
+          zero = zero || (alive && v[c] == 0.f);
           top = fmaxf(top, fin ? v[c] : 0.f);
+          low = fminf(low, fin && v[c] > 0.f ? v[c] : INFINITY);
         }
         blk = named(j + 1, entry);
         entry = entry_of(j + 2);
         fetch(blk);  // of tile j + 1
 #pragma unroll
-        for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        for (int off = 8; off > 0; off >>= 1) {
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+          low = fminf(low, __shfl_xor_sync(0xffffffffu, low, off));
+        }
         top = __shfl_sync(0xffffffffu, top, 0);
-        if (top > F)  // the power of two above it
-          F = __uint_as_float(min(((__float_as_uint(top) >> 23) & 0xffu) + 1u, 254u) << 23);
+        low = __shfl_sync(0xffffffffu, low, 0);
+        const int e_tile = q8_e(top);
+        // (a value of 0 next to others is as far away as can be: its weight would set their reference)
+        e_most = max(e_most, e_tile);
+        const bool wide = (__any_sync(0xffffffffu, zero) && top > 0.f) || q8_e(low) < e_tile - kQ8TileNear ||
+                          e_tile < e_most - kQ8TileFar;
         uint32_t badmask = 0;  // of page `lane`
         if (__any_sync(0xffffffffu, bad)) {
 #pragma unroll
@@ -496,13 +570,14 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
             if (!(fabsf(v[c]) < INFINITY)) v[c] = 0.f;
           }
         }
-        // (vs / F first: neither factor leaves the normal range)
-        const float inv = q8_inverse(F);
         uint32_t f[4];
+        float e4[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const float x = v[c] * inv * q8_vtop<kType>();
+          const int e = wide ? q8_e(v[c]) : e_tile;
+          const float x = v[c] * q8_pow2(-e) * q8_vtop<kType>();
           f[c] = pack_fp16x2(x, x);
+          e4[c] = static_cast<float>(e);
         }
         // A wait by parity must not be overtaken by a phase: the barrier's next one needs these scales.
         // (k_free of tile j - 4 would say as much, but Q K^T of tile j can complete before this wait.)
@@ -510,12 +585,15 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
         if (lane < 16) {
           *reinterpret_cast<float4 *>(sKs + buf * kQ8Tok + 4 * lane) = k4;
           *reinterpret_cast<uint4 *>(sFt + buf * kQ8Tok + 4 * lane) = make_uint4(f[0], f[1], f[2], f[3]);
+          if (wide) *reinterpret_cast<float4 *>(sE + buf * kQ8Tok + 4 * lane) = make_float4(e4[0], e4[1], e4[2], e4[3]);
         }
         if (lane < kQ8TilePages) {
           sLive[buf * 4 + lane] = static_cast<uint16_t>(live);
           sBad[buf * 4 + lane] = static_cast<uint16_t>(badmask);
         }
-        if (lane == 0) sF[buf * 4] = F;
+        if (lane == 0)
+          *reinterpret_cast<float4 *>(sTile + buf * 4) =
+              make_float4(static_cast<float>(e_tile), q8_pow2(-e_tile), wide ? 1.f : 0.f, 0.f);
         __syncwarp();
         if (lane == 0) mbar_arrive(sc_full + buf);
       }
@@ -600,7 +678,7 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
     const int first_own = L - p.T;  // the first of the queries' own tokens
     const uint64_t bits = (p.tree && mine) ? p.tree[static_cast<size_t>(s) * p.T + t] : ~0ull;
     const bool warp_rows = row0 + 128 * rtile + (warp % 4) * 32 < p.R;  // any row in this warp
-    float m = 0.f, l = 0.f, F = 0.f;
+    float m = 0.f, l = 0.f;
     bool poison = false;  // the row sees a token whose values are no numbers
     bool ok = true;
     for (int i = 0; i < cnt; ++i) {
@@ -618,8 +696,7 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
         continue;
       }
       const int tok0 = (j0 + j) * kQ8Tok;
-      const float F_old = F;
-      F = sF[buf * 4];
+      const float4 tile = *reinterpret_cast<const float4 *>(sTile + buf * 4);
       uint32_t k[2];  // the tokens that this row sees
       {
         const uint2 live = *reinterpret_cast<const uint2 *>(sLive + buf * 4);
@@ -638,14 +715,17 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
           }
         }
       }
-      const bool all = __all_sync(0xffffffffu, (k[0] & k[1]) == 0xffffffffu);
+      const bool wide = tile.z != 0.f, all = __all_sync(0xffffffffu, (k[0] & k[1]) == 0xffffffffu && !wide);
       {
         const uint2 bad = *reinterpret_cast<const uint2 *>(sBad + buf * 4);
         poison = poison || ((k[0] & bad.x) | (k[1] & bad.y)) != 0;
       }
-      float a = F == F_old ? 1.f : F_old * q8_inverse(F);  // what O is to be multiplied by
+      float a = 1.f;  // what O is to be multiplied by
       const uint32_t ts = tS + lane_off + 64 * (i & 1);
-      const float sum = all ? q8_weigh<false>(ts, k, ksb, m, l, a) : q8_weigh<true>(ts, k, ksb, m, l, a);
+      float sum;
+      if (__builtin_expect(all, 1)) sum = tile.y * q8_weigh<false>(ts, k, ksb, tile.x, m, l, a);
+      else if (__builtin_expect(!wide, 1)) sum = tile.y * q8_weigh<true>(ts, k, ksb, tile.x, m, l, a);
+      else sum = q8_weigh_wide(ts, k, ksb, sE + buf * kQ8Tok, m, l, a);
       if (i > 0 && __any_sync(0xffffffffu, a != 1.f)) {
         // the side's previous product must be in O before it is rescaled
         const int pb = 2 * side + ((i - 1) & 1);
@@ -672,7 +752,7 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
     ok = __all_sync(0xffffffffu, ok && (cnt == 0 || mbar_wait(pv_done + 2 * side + (last & 1), (last >> 1) & 1,
                                                               abort_flag)));
     tc_fence_after();
-    const float f = F / q8_vtop<kType>();  // of this side's O
+    const float f = 1.f / q8_vtop<kType>();  // of O
     if constexpr (!kTwo) {
       // join the sides: the odd tiles' sums go through shared memory, the even side writes.  Both are
       // brought to the larger reference.
@@ -703,7 +783,7 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
         const float M = l == 0.f ? m1 : l1 == 0.f ? m : fmaxf(m, m1);
         const float a0 = l == 0.f ? 0.f : ex2(m - M), a1 = l1 == 0.f ? 0.f : ex2(m1 - M);
         const bool none = l == 0.f;
-        l = (none ? 0.f : l * a0) + (l1 == 0.f ? 0.f : l1 * a1);
+        l = (none ? 0.f : q8_shift(l, m - M)) + (l1 == 0.f ? 0.f : q8_shift(l1, m1 - M));
         m = M;
 #pragma unroll 1
         for (int c = 0; c < HD; c += 32) {

@@ -388,7 +388,9 @@ size_t fa_q8_workspace_size(int S, int Hq, int Hk, int Lq, int d, int max_blocks
  *
  *   q              bf16 [S, Hq, d] (decode) or [S, Hq, Lq, d], contiguous.
  *   k_pool, v_pool   codes [num_blocks, Hk, 16, d];  k_scale, v_scale: fp32 [num_blocks, Hk, 16];
- *                  all 16-byte aligned.  type: FA_CACHE_E4M3 or FA_CACHE_INT8.  Scales are >= 0; a
+ *                  all 16-byte aligned.  type: FA_CACHE_E4M3 or FA_CACHE_INT8.  Scales are >= 0
+ *                  and below 2^126, however far apart; a row's result does not depend on tokens
+ *                  that it does not see, whatever their scales, beyond the rounding of its sums.  A
  *                  NaN scale makes its token NaN for the rows that see it.  The tokens of a sequence
  *                  hold no e4m3 NaN codes (0x7f, 0xff; fa_cache_append writes none); other slots of
  *                  the pool may hold anything.

@@ -106,12 +106,14 @@ def verify(a, what, causal=False, masks=None):
     return got
 
 
-# rows per key head: 4 and 18 take the kernel of few rows
+# rows per key head: 4 and 18 take the kernel of few rows; 40 and 120 one row tile of the kernel of many
+# rows, 200 and 328 two (a whole and a ragged one, then a third)
 FEW = [(4, 1, None), (6, 1, 3)]
+MANY = [(8, 1, 5), (6, 2, 40), (5, 1, 40), (8, 1, 41)]
 
 
 @pytest.mark.parametrize("dtype", [E4M3, INT8])
-@pytest.mark.parametrize("Hq,Hk,T", FEW)
+@pytest.mark.parametrize("Hq,Hk,T", FEW + MANY)
 @pytest.mark.parametrize("S,L", [(2, 333), (1, 2500)])
 def test_values_of_a_few_binades_above_the_smallest_kept(dtype, Hq, Hk, T, S, L):
     a = make(1, S, Hq, Hk, 128, L, dtype, T)
@@ -119,7 +121,7 @@ def test_values_of_a_few_binades_above_the_smallest_kept(dtype, Hq, Hk, T, S, L)
     verify(a, "tiny values", causal=T is not None)
 
 
-@pytest.mark.parametrize("Hq,Hk,T", FEW)
+@pytest.mark.parametrize("Hq,Hk,T", FEW + MANY)
 @pytest.mark.parametrize("S,L", [(2, 333), (1, 2500)])
 @pytest.mark.parametrize("up", [20, 70, 110])
 def test_a_loud_token_among_values_of_zero(Hq, Hk, T, S, L, up):
@@ -135,8 +137,59 @@ def test_a_loud_token_among_values_of_zero(Hq, Hk, T, S, L, up):
         verify(a, f"loud at {first}", causal=T is not None)
 
 
-@pytest.mark.parametrize("Hq,Hk,T", FEW)
+@pytest.mark.parametrize("Hq,Hk,T", FEW + MANY)
 def test_values_of_zero_alone(Hq, Hk, T):
     a = make(3, 2, Hq, Hk, 64, 700, E4M3, T)
     a[4] *= 0
     verify(a, "zeros", causal=T is not None)
+
+
+@pytest.mark.parametrize("dtype", [E4M3, INT8])
+@pytest.mark.parametrize("Hq,Hk,T", FEW[1:] + MANY)
+@pytest.mark.parametrize("up", [9, 24, 31, 60, 110])
+def test_a_loud_token_that_other_rows_do_not_see(dtype, Hq, Hk, T, up):
+    # one of the queries' own tokens: the rows before it (causal), the nodes off its branch (tree)
+    L, mid = 230, T // 2
+    a = make(4, 2, Hq, Hk, 128, L, dtype, T)
+    for s in range(2):
+        scale_by(a[4], a, s, L - T + mid, 2.0 ** up)
+    verify(a, "hidden", causal=True)
+    masks = [[(1 << t) | (1 << (t // 2)) | 1 for t in range(T)] for _ in range(2)]  # few see the middle node
+    verify(a, "off the branch", masks=masks)
+
+
+@pytest.mark.parametrize("dtype", [E4M3, INT8])
+@pytest.mark.parametrize("Hq,Hk,T", FEW + MANY)
+@pytest.mark.parametrize("up", [24, 40])
+def test_a_loud_token_of_next_to_no_weight(dtype, Hq, Hk, T, up):
+    L = 500
+    a = make(5, 1, Hq, Hk, 128, L, dtype, T)
+    u = torch.randn(128, generator=torch.Generator().manual_seed(6)).to(torch.bfloat16)
+    a[0][:] = u.cuda()
+    codes, scale = R.quantise(-4.0 * u.float()[None], dtype)  # a score of about -45
+    for at in (3, 200, 450):
+        a[1][at // 16, :, at % 16] = codes[0].cuda()
+        a[3][at // 16, :, at % 16] = scale[0].cuda()
+        scale_by(a[4], a, 0, at, 2.0 ** up)
+    verify(a, "weightless", causal=T is not None)
+
+
+@pytest.mark.parametrize("dtype", [E4M3, INT8])
+@pytest.mark.parametrize("Hq,Hk,T", FEW + MANY)
+@pytest.mark.parametrize("spread", [4, 7, 8, 9, 30])
+def test_scales_rise_and_fall_along_the_context(dtype, Hq, Hk, T, spread):
+    # by `spread` binades up and down again within 50 tokens, and by 40 over the whole context
+    L = 1100
+    a = make(7, 2, Hq, Hk, 64, L, dtype, T)
+    at = torch.arange(a[5].shape[1] * 16)
+    wave = torch.exp2(spread * (1 - (at % 50 - 25).abs() / 25) + 40 * (at % 700) / 700).float().cuda()
+    n = a[5].shape[1]
+    a[4] *= wave.view(1, n, 1, 16).expand(2, -1, -1, -1).reshape(2 * n, 1, 16)
+    verify(a, "wave", causal=T is not None)
+
+
+@pytest.mark.parametrize("dtype", [E4M3, INT8])
+@pytest.mark.parametrize("Hq,Hk,T", FEW + MANY)
+def test_scales_alike(dtype, Hq, Hk, T):
+    a = make(8, 2, Hq, Hk, 128, 1500, dtype, T)
+    verify(a, "alike", causal=T is not None)
