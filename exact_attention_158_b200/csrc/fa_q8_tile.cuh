@@ -34,8 +34,10 @@
 // 2^6, and O is rescaled in TMEM.
 //
 // Queries go to fp16 against one power of two for all rows of the CTA (q8_q_unit; it is part of the key
-// scales).  int8's conversion leaves every four features in the order 0, 2, 1, 3; q is stored in that
-// order too, and O's columns are put back when it is written.
+// scales), unless their largest features lie more than 2^12 apart: then each row has its own, and
+// every tile is taken in the wide form, which multiplies by it.  int8's conversion leaves every four
+// features in the order 0, 2, 1, 3; q is stored in that order too, and O's columns are put back when
+// it is written.
 //
 // Bound: per 128 rows x 64 tokens the products take about 510 cycles at d = 128 and the exponentials
 // 512 (16 a cycle); the 16 KB of codes take about 700 cycles of the SM's share of HBM.  Measured, two
@@ -61,6 +63,9 @@ constexpr int kQ8TileFar = 64;              // and of how far below an earlier t
 // e's range: 2^-89 leaves the smallest scale, 2^-109, f = 2^-20, and a row's sum of p 2^-e in fp32's
 // range; 2^126 is the largest whose inverse is a normal number
 constexpr int kQ8LeastE = -89, kQ8MostE = 126;
+// The largest feature of a row, against the largest of the CTA's rows, from which on they share a power of
+// two: it then lies at 2^2 or above in fp16 and loses 2^-27 of it at most.
+constexpr float kQ8RowsNear = 0x1p-12f;
 // f = 1 as V holds it: e4m3 codes are at most 448, int8 codes 127
 template <int kType> __device__ constexpr float q8_vtop() { return kType == kQ8E4m3 ? 0x1p6f : 0x1p8f; }
 
@@ -78,7 +83,7 @@ struct Q8TileCfg {
   // and bad tokens, the tile's)
   static_assert(kQBytes == 2 * kTileBytes, "two V tiles in the place of a row tile's Q");
   static constexpr size_t kNeed = 1024 + 2 * kQBytes + (kQ8KBufs + 2) * kTileBytes +
-                                  2 * kQ8CodeBufs * kCodeBytes + kScaleBufs * (kQ8Tok * 12 + 32) + kBars * 8 + 48;
+                                  2 * kQ8CodeBufs * kCodeBytes + kScaleBufs * (kQ8Tok * 12 + 32) + kBars * 8 + 80 + 1024;
   static constexpr size_t kSmem = kNeed > 116 * 1024 ? kNeed : 116 * 1024;
   static constexpr uint32_t kColO = 256;  // S: [side][2] x 64 columns before it
   // fp16 operands: the type fields of A and B are 0
@@ -184,11 +189,11 @@ __device__ __forceinline__ float q8_weigh(uint32_t s_tmem, const uint32_t (&k)[2
   return u + v;
 }
 
-// The same for a wide tile, with an e per token; returns the sum of p 2^-e.  This form is rare: it reads
+// The same for a wide tile, with an e per token and the row's own power of two; returns the sum of p 2^-e.  This form is rare: it reads
 // the scores twice, four at a time in loops, so that neither its registers nor its instructions stand in
 // the others' way (unrolled over 32 scores, tree_batch took 6% longer without ever coming here).
 __device__ __forceinline__ float q8_weigh_wide(uint32_t s_tmem, const uint32_t (&k)[2], const float *ks,
-                                               const float *es, float &m, float &l, float &a) {
+                                               const float *es, float row_scale, float &m, float &l, float &a) {
   const uint64_t sees = (static_cast<uint64_t>(k[1]) << 32) | k[0];
   auto four = [&](int h, float (&x)[4], float (&e)[4]) {  // s + e - m, and e
     tmem_ld4(s_tmem + h, reinterpret_cast<uint32_t *>(x));
@@ -199,7 +204,7 @@ __device__ __forceinline__ float q8_weigh_wide(uint32_t s_tmem, const uint32_t (
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       asm volatile("" : "+f"(x[c]));
-      x[c] = (sees >> (h + c)) & 1 ? fmaf(x[c], fs[c], e[c] - m) : -INFINITY;
+      x[c] = (sees >> (h + c)) & 1 ? fmaf(x[c], fs[c] * row_scale, e[c] - m) : -INFINITY;
     }
   };
   float t = -INFINITY, sum = 0.f, x[4], e[4];
@@ -310,7 +315,9 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
   uint64_t *drain = pv_done + 4;                // [side] every product of an issuer has completed
   uint64_t *q_full = drain + 2;                 // [row tile]
   float *sTop = reinterpret_cast<float *>(bars + C::kBars);  // [8]: the warps' largest |q|
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sTop + 8);
+  float *sLow = sTop + 8;                       // [8]: and the smallest of their rows' largest, rows of 0 apart
+  float *sRow = sLow + 8;                       // [row tile][128]: 1 / the row's own power of two, else 1
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sRow + 256);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
   unsigned u = blockIdx.x;
@@ -377,29 +384,34 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
+  float row_top = 0.f;
   if (warp < 8) {
     const int row = row0 + (kTwo ? 128 * (warp / 4) : 0) + threadIdx.x % 128;
-    float top = 0.f;
     if (row < p.R) {
       const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (row_base + row) * HD);
 #pragma unroll
       for (int c = 0; c < HD / 8; ++c) {
         const uint4 v = src[c];
-        top = q8_finite_max(q8_finite_max(q8_finite_max(q8_finite_max(top, v.x), v.y), v.z), v.w);
+        row_top = q8_finite_max(q8_finite_max(q8_finite_max(q8_finite_max(row_top, v.x), v.y), v.z), v.w);
       }
     }
+    float top = row_top, low = row_top > 0.f ? row_top : INFINITY;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    if (lane == 0) sTop[warp] = top;
+    for (int off = 16; off > 0; off >>= 1) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      low = fminf(low, __shfl_xor_sync(0xffffffffu, low, off));
+    }
+    if (lane == 0) sTop[warp] = top, sLow[warp] = low;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  float q_top = sTop[0];
+  float q_top = sTop[0], q_low = sLow[0];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) q_top = fmaxf(q_top, sTop[i]);
-  const float q_unit = q8_q_unit(q_top);
+  for (int i = 1; i < 8; ++i) q_top = fmaxf(q_top, sTop[i]), q_low = fminf(q_low, sLow[i]);
+  const bool rows_apart = q_low < q_top * kQ8RowsNear;
+  const float q_unit = q8_q_unit(rows_apart && warp < 8 ? row_top : q_top);  // the CTA's or this thread's row's
 
   if (warp >= 8 && warp < 12) {
     // ------------------------------------------------------------------ codes -> fp16 tiles
@@ -511,7 +523,7 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
       }
     } else {
       // scales: lane i < 16 has tokens 4 i .. 4 i + 3 of the tile
-      const float score_scale = p.scale_log2 * q8_inverse(q_unit);
+      const float score_scale = rows_apart ? p.scale_log2 : p.scale_log2 * q8_inverse(q_unit);
       float4 ks, vs;
       bool has = false;  // this lane's page is named
       int e_most = kQ8LeastE;
@@ -560,7 +572,7 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
         // (a value of 0 next to others is as far away as can be: its weight would set their reference)
         e_most = max(e_most, e_tile);
         const bool wide = (__any_sync(0xffffffffu, zero) && top > 0.f) || q8_e(low) < e_tile - kQ8TileNear ||
-                          e_tile < e_most - kQ8TileFar;
+                          e_tile < e_most - kQ8TileFar || rows_apart;
         uint32_t badmask = 0;  // of page `lane`
         if (__any_sync(0xffffffffu, bad)) {
 #pragma unroll
@@ -655,6 +667,7 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
     const bool mine = row < p.R;
     const int cnt = n[side];
     const uint32_t lane_off = static_cast<uint32_t>((warp % 4) * 32) << 16;
+    sRow[128 * rtile + lrow] = rows_apart ? q8_inverse(q_unit) : 1.f;  // (two threads of a row write the same)
     if (kTwo || side == 0) {  // this thread's row of q, in the layout the tensor core reads
       const uint16_t *src = p.q + (row_base + row) * HD;
       uint8_t *dst = sQ + rtile * C::kQBytes;
@@ -725,7 +738,7 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
       float sum;
       if (__builtin_expect(all, 1)) sum = tile.y * q8_weigh<false>(ts, k, ksb, tile.x, m, l, a);
       else if (__builtin_expect(!wide, 1)) sum = tile.y * q8_weigh<true>(ts, k, ksb, tile.x, m, l, a);
-      else sum = q8_weigh_wide(ts, k, ksb, sE + buf * kQ8Tok, m, l, a);
+      else sum = q8_weigh_wide(ts, k, ksb, sE + buf * kQ8Tok, sRow[128 * rtile + lrow], m, l, a);
       if (i > 0 && __any_sync(0xffffffffu, a != 1.f)) {
         // the side's previous product must be in O before it is rescaled
         const int pb = 2 * side + ((i - 1) & 1);

@@ -193,3 +193,30 @@ def test_scales_rise_and_fall_along_the_context(dtype, Hq, Hk, T, spread):
 def test_scales_alike(dtype, Hq, Hk, T):
     a = make(8, 2, Hq, Hk, 128, 1500, dtype, T)
     verify(a, "alike", causal=T is not None)
+
+
+@pytest.mark.parametrize("dtype", [E4M3, INT8])
+@pytest.mark.parametrize("Hq,Hk,T", FEW[1:] + MANY)
+@pytest.mark.parametrize("up", [10, 13, 30, 60, 125])
+def test_queries_of_any_size_side_by_side(dtype, Hq, Hk, T, up):
+    # rows of one key head whose queries are 2^up times the others', as padding that holds anything
+    # may be: each row keeps the precision that it has alone
+    a = make(9, 2, Hq, Hk, 128, 300, dtype, T)
+    loud = torch.zeros(2, Hq, T, dtype=torch.bool)
+    loud[:, :, T // 3] = True
+    loud[1, Hq // 2, ::2] = True
+    a[0][loud] *= 2.0 ** up
+    a[0][0, 0, T - 1] = 0.0
+    got = verify_rows(a, ~loud)
+    assert torch.isfinite(got[0][~loud]).all()
+
+
+def verify_rows(a, rows):
+    """As verify (causal), of the rows given; the others' scores may be of any size."""
+    import exact_attention_158_b200 as fa
+    got = fa.fa_prefill_paged_q8(*a, out_dtype=torch.float32)
+    assert fa.device_status() == 0
+    want, bounds = reference(a, True, None)
+    for g, w, b, n in zip(got, want, bounds, ("O", "LSE")):
+        R.check(g.cpu()[rows], w[rows], b[rows], f"rows {n}")
+    return got
