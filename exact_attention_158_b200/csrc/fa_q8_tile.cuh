@@ -112,6 +112,18 @@ __device__ __forceinline__ uint32_t mul_fp16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// Four columns of a lane's row of tensor memory, and two back.
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t *r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st2(uint32_t taddr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};" ::"r"(taddr), "r"(r[0]), "r"(r[1])
+               : "memory");
+}
+
 // Keeps uses of registers that a tcgen05.ld fills behind the wait that precedes this.
 __device__ __forceinline__ void q8_pin(float (&x)[32]) {
 #pragma unroll
