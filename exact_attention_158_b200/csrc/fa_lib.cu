@@ -1079,17 +1079,38 @@ bool any_sum_within(Wide r, const RowDim *in, int count, Wide lo, Wide hi) {
 
 // Does a row of x share a byte with a row of y?
 bool rows_meet(const Rows &x, const Rows &y) {
+  const Wide r = static_cast<Wide>(reinterpret_cast<uintptr_t>(x.p)) - static_cast<Wide>(reinterpret_cast<uintptr_t>(y.p));
+  Wide lo = r, hi = r;  // of all differences: most tensors lie apart as a whole
+  for (int a = 0; a < 3; ++a) {
+    const Wide u = (x.n[a] - 1) * x.s[a], v = (y.n[a] - 1) * y.s[a];
+    (u < 0 ? lo : hi) += u;
+    (v < 0 ? hi : lo) -= v;
+  }
+  if (hi <= -x.bytes || lo >= y.bytes) return false;
   RowDim dim[6];
   for (int a = 0; a < 3; ++a) {
     dim[a] = RowDim{x.n[a], x.s[a]};
-    dim[3 + a] = RowDim{y.n[a], -static_cast<Wide>(y.s[a])};
+    dim[3 + a] = RowDim{y.n[a], -y.s[a]};
   }
-  const Wide r = static_cast<Wide>(reinterpret_cast<uintptr_t>(x.p)) - static_cast<Wide>(reinterpret_cast<uintptr_t>(y.p));
   return any_sum_within(r, dim, 6, -static_cast<Wide>(x.bytes), y.bytes);
 }
 
 // Do two different rows of x share a byte?  The first index in which they differ is the larger one's.
 bool rows_meet_themselves(const Rows &x) {
+  // dimensions that lie inside one another, smallest stride first: no
+  Wide size[3], reach = x.bytes;
+  int order[3] = {0, 1, 2};
+  for (int a = 0; a < 3; ++a) size[a] = x.n[a] < 2 ? 0 : x.s[a] < 0 ? -x.s[a] : x.s[a];
+  if (size[order[0]] > size[order[1]]) std::swap(order[0], order[1]);
+  if (size[order[1]] > size[order[2]]) std::swap(order[1], order[2]);
+  if (size[order[0]] > size[order[1]]) std::swap(order[0], order[1]);
+  bool inside = true;
+  for (int a : order) {
+    if (x.n[a] < 2) continue;
+    inside = inside && size[a] >= reach;
+    reach += (x.n[a] - 1) * size[a];
+  }
+  if (inside) return false;
   for (int a = 0; a < 3; ++a) {
     RowDim dim[3];
     Wide r = x.s[a];
