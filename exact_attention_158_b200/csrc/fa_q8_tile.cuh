@@ -130,9 +130,10 @@ __device__ __forceinline__ void q8_pin(float (&x)[32]) {
   for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(x[i]));
 }
 
-// The power of two above vs, as its exponent in e's range.
-__device__ __forceinline__ int q8_e(float vs) {
-  return min(max(static_cast<int>((__float_as_uint(vs) >> 23) & 0xffu) - 126, kQ8LeastE), kQ8MostE);
+// The power of two above a scale, as its exponent in e's range.
+__device__ __forceinline__ uint32_t q8_exponent(float x) { return (__float_as_uint(x) >> 23) & 0xffu; }
+__device__ __forceinline__ int q8_e(uint32_t exponent) {
+  return min(max(static_cast<int>(exponent) - 126, kQ8LeastE), kQ8MostE);
 }
 __device__ __forceinline__ float q8_pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
@@ -558,57 +559,63 @@ __global__ void __launch_bounds__(kQ8TileThreads, 1) fa_q8_tile_kernel(const Q8P
         const float4 k4 = make_float4(ks.x * score_scale, ks.y * score_scale, ks.z * score_scale, ks.w * score_scale);
         const int left = L - (j0 + j) * kQ8Tok - kQ8Page * lane;  // and for lane i < 4, of page i
         const uint32_t live = blk < 0 || left <= 0 ? 0u : left >= 16 ? 0xffffu : (1u << left) - 1u;
-        float top = 0.f, low = INFINITY;  // the tile's largest finite vs and its smallest above 0
-        bool bad = false, zero = false;   // live tokens whose vs is not finite, or 0
+        // The exponents of the tile's largest finite vs, and of its smallest (as 255 less it), in one word: 0
+        // counts as the smallest, its token's weight would set the others' reference
+        uint32_t range = 0;
+        bool bad = false;  // a live token's vs is not finite
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const bool alive = has && c < left4;
-          if (c >= left4) v[c] = 0.f;  // a slot past the end may hold anything
-          const bool fin = fabsf(v[c]) < INFINITY;
-          bad = bad || !fin;
-          zero = zero || (alive && v[c] == 0.f);
-          top = fmaxf(top, fin ? v[c] : 0.f);
-          low = fminf(low, fin && v[c] > 0.f ? v[c] : INFINITY);
+          if (!alive) v[c] = 0.f;  // a slot past the end may hold anything
+          const uint32_t x = q8_exponent(v[c]);
+          bad = bad || x == 255u;
+          range = __vmaxu2(range, alive && x != 255u ? (x << 16) + 255u - x : 0u);
         }
         blk = named(j + 1, entry);
         entry = entry_of(j + 2);
         fetch(blk);  // of tile j + 1
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1) {
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-          low = fminf(low, __shfl_xor_sync(0xffffffffu, low, off));
+        if constexpr (!kTwo) {
+          // and tile j + 2's as far as L2: this warp sets the pace where one row tile is all the work (128 rows
+          // by 8192 tokens, one to an SM: 170 us without, 150 so; with two row tiles it does not)
+          const int b = __shfl_sync(0xffffffffu, entry, (lane / 4) & 3);
+          if (lane < 16 && lane % 4 == 0 && b >= 0 && b < p.num_blocks) {
+            const size_t at = (static_cast<size_t>(b) * p.Hk + kh) * kQ8Page;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.ks + at));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.vs + at));
+          }
         }
-        top = __shfl_sync(0xffffffffu, top, 0);
-        low = __shfl_sync(0xffffffffu, low, 0);
-        const int e_tile = q8_e(top);
-        // (a value of 0 next to others is as far away as can be: its weight would set their reference)
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) range = __vmaxu2(range, __shfl_xor_sync(0xffffffffu, range, off));
+        const int e_tile = q8_e(range >> 16);
         e_most = max(e_most, e_tile);
-        const bool wide = (__any_sync(0xffffffffu, zero) && top > 0.f) || q8_e(low) < e_tile - kQ8TileNear ||
-                          e_tile < e_most - kQ8TileFar || rows_apart;
+        const bool wide = q8_e(255u - (range & 0xffffu)) < e_tile - kQ8TileNear || e_tile < e_most - kQ8TileFar || rows_apart;
         uint32_t badmask = 0;  // of page `lane`
         if (__any_sync(0xffffffffu, bad)) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint32_t m = (__ballot_sync(0xffffffffu, !(fabsf(v[c]) < INFINITY)) >> (4 * (lane & 3))) & 0xfu;
-            for (int i = 0; i < 4; ++i) badmask |= ((m >> i) & 1u) << (4 * i + c);
+            // lane i's token c is token 4 i + c of the page
+            badmask |= ((m & 1u) | (m & 2u) << 3 | (m & 4u) << 6 | (m & 8u) << 9) << c;
             if (!(fabsf(v[c]) < INFINITY)) v[c] = 0.f;
           }
         }
-        uint32_t f[4];
-        float e4[4];
+        const float unit = q8_pow2(-e_tile) * q8_vtop<kType>();
+        float x[4] = {v[0] * unit, v[1] * unit, v[2] * unit, v[3] * unit}, e4[4];
+        if (wide) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int e = wide ? q8_e(v[c]) : e_tile;
-          const float x = v[c] * q8_pow2(-e) * q8_vtop<kType>();
-          f[c] = pack_fp16x2(x, x);
-          e4[c] = static_cast<float>(e);
+          for (int c = 0; c < 4; ++c) {
+            const int e = q8_e(q8_exponent(v[c]));
+            x[c] = v[c] * q8_pow2(-e) * q8_vtop<kType>();
+            e4[c] = static_cast<float>(e);
+          }
         }
         // A wait by parity must not be overtaken by a phase: the barrier's next one needs these scales.
         // (k_free of tile j - 4 would say as much, but Q K^T of tile j can complete before this wait.)
         if (j >= NS && !__all_sync(0xffffffffu, mbar_wait(sc_free + buf, (j / NS - 1) & 1, abort_flag))) break;
         if (lane < 16) {
           *reinterpret_cast<float4 *>(sKs + buf * kQ8Tok + 4 * lane) = k4;
-          *reinterpret_cast<uint4 *>(sFt + buf * kQ8Tok + 4 * lane) = make_uint4(f[0], f[1], f[2], f[3]);
+          *reinterpret_cast<uint4 *>(sFt + buf * kQ8Tok + 4 * lane) = make_uint4(
+              pack_fp16x2(x[0], x[0]), pack_fp16x2(x[1], x[1]), pack_fp16x2(x[2], x[2]), pack_fp16x2(x[3], x[3]));
           if (wide) *reinterpret_cast<float4 *>(sE + buf * kQ8Tok + 4 * lane) = make_float4(e4[0], e4[1], e4[2], e4[3]);
         }
         if (lane < kQ8TilePages) {
