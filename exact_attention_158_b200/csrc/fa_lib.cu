@@ -1020,7 +1020,8 @@ struct Span {
 Span row_span(const void *x, const long long *strides, int T, int H, int d) {
   const long long n[2] = {T, H};
   long long lo = 0, hi = d;
-  for (int a = 0; a < 2; ++a) (strides[a] < 0 ? lo : hi) += (n[a] - 1) * strides[a];
+  for (int a = 0; a < 2; ++a)
+    if (n[a] > 1) (strides[a] < 0 ? lo : hi) += (n[a] - 1) * strides[a];
   return Span{static_cast<const char *>(x) + 2 * lo, static_cast<size_t>(hi - lo) * 2};
 }
 
@@ -1444,6 +1445,7 @@ fa_status fa_rope(const void *q, const long long *q_strides, void *q_out,
     p.x[i].out = out[i];
     p.x[i].H = heads[i];
     for (int a = 0; a < 3; ++a) {
+      if ((a == 1 ? heads[i] : extent[a]) == 1) continue;  // its stride means nothing
       if (is[i][a] % in_unit || os[i][a] % out_unit) return FA_ERR_ALIGNMENT;
       p.x[i].in_s[a] = is[i][a];
       p.x[i].out_s[a] = os[i][a];
@@ -1510,6 +1512,7 @@ fa_status fa_cache_append(const void *k, const long long *k_strides, const void 
   long long *to[4] = {p.k_s, p.v_s, p.q_s, p.qo_s};
   for (int i = 0; i < (Hq > 0 ? 4 : 2); ++i)
     for (int a = 0; a < 2; ++a) {
+      if ((a == 0 ? T : i < 2 ? Hk : Hq) == 1) continue;  // its stride means nothing
       if (strides[i][a] % 8) return FA_ERR_ALIGNMENT;
       to[i][a] = strides[i][a];
     }

@@ -301,7 +301,8 @@ fa_status fa_decode_paged_noalloc(const void *q, const void *k_pool, const void 
  *   freqs          double [rot / 2], device: radians per position.  May be null with rot = 0.
  *   rot            a multiple of 16 in [0, d];  amplitude finite;  d: 64 or 128.
  *   B, N >= 0 (nothing is launched for 0), B * N <= INT_MAX;  Hq >= 1, Hk >= 0.
- * Pointers are 16-byte aligned and strides multiples of 16 bytes (else FA_ERR_ALIGNMENT).
+ * Pointers are 16-byte aligned, and so are strides (else FA_ERR_ALIGNMENT); that of a dimension of
+ * one element is not looked at.
  * Returns FA_OK once the kernel is queued.
  */
 typedef enum {

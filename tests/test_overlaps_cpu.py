@@ -127,3 +127,20 @@ def test_append_queries_over_what_is_read(lib):
     for name in ("slots", "pos", "fr"):
         assert append(lib, qo=2 * A, qos=dense, **dict(a, **{name: 2 * A + 64})) == INVALID, name
     assert append(lib, qo=2 * A, qos=dense, **dict(a, fr=(1 << 44) + 64)) == INVALID  # the pool over freqs
+
+
+def test_strides_of_single_elements_are_not_looked_at(lib):
+    # a misaligned stride that matters is told before the amplitude, which is refused in any case
+    def status(qs, qos, B, Hq, N):
+        return lib.fa_rope(A, st(qs), 2 * A, st(qos), None, None, None, None, 0, 0, 1 << 40, 0, 1 << 41, 16, 0,
+                           float("nan"), 0, B, Hq, 0, N, D, None)
+
+    for a in range(3):
+        n = [4, 4, 4]
+        n[a] = 1
+        s = [[4096, 1024, 64], [4096, 1024, 64]]
+        for i in range(2):
+            odd = [list(x) for x in s]
+            odd[i][a] = 1001
+            assert status(*odd, *n) == INVALID
+            assert status(*odd, 4, 4, 4) == MISALIGNED

@@ -55,3 +55,19 @@ def test_queries_of_a_fused_projection_in_place(dtype):
     got, got_kv = call(q_out=q)
     assert torch.equal(q, want) and torch.equal(x[:, Hq:], kv)
     assert all(torch.equal(a, b) for a, b in zip(got_kv, want_kv))
+
+
+def test_a_batch_of_one_with_any_stride():
+    import exact_attention_158_b200 as fa
+    N, H, d = 9, 2, 64
+    room = torch.randn(2 * N * H * d + 10, device="cuda").to(torch.bfloat16)
+    x = room.as_strided((1, H, N, d), (N * H * d + 5, d, H * d, 1))  # a batch's odd stride, one element
+    pos = torch.arange(N, dtype=torch.int32, device="cuda")
+    freqs, _ = fa.rope_frequencies(64)
+    got, _ = fa.fa_rope(x, None, pos, freqs)
+    want, _ = fa.fa_rope(x.contiguous(), None, pos, freqs)
+    assert torch.equal(got, want)
+    one = room.as_strided((1, H, d), (77, d, 1))  # one token
+    pools = [torch.zeros((1, H, 16, d), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    fa.fa_cache_append(one, one, *pools, torch.tensor([3], device="cuda"))
+    assert torch.equal(pools[0][0, :, 3], one[0]) and torch.equal(pools[1][0, :, 3], one[0])
