@@ -1209,8 +1209,8 @@ struct Q8Plan {
 };
 
 // Up to kQ8StreamRows rows fa_q8_stream_kernel, beyond it fa_q8_tile_kernel.  32 sequences of 2048
-// tokens, 8 heads of 128: 16 rows per head take the former 58 us and the latter 96; 17 rows 91 and 96;
-// 32 rows 93 and 96; 64 rows 140 and 94.  One such sequence: 32 rows 24 and 26, 64 rows 24 and 25.
+// tokens, 8 heads of 128: 16 rows per head take the former 58 us and the latter 91; 17 rows 87 and 91;
+// 32 rows 89 and 91; 64 rows 140 and 92.  One such sequence: 32 rows 22 and 28, 64 rows 26 and 28.
 constexpr int kQ8StreamRows = 32;
 // Few rows: chunks enough for two waves of the four CTAs that fit an SM, none longer than 128 pages (so
 // that ragged lengths balance: 64 sequences of 512 to 8192 tokens took 397 us in two chunks each and

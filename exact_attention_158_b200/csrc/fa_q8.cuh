@@ -25,7 +25,7 @@
 // wants 64 or 128 rows per product; with 1 to 32 rows it would multiply padding, and its operands
 // would have to be converted through shared memory.)  64 sequences of 512 to 8192 tokens, 32 heads of
 // 128: 372 us, 6500 GB/s, what a copy reaches; about 370 instructions per page and warp keep the
-// schedulers half busy, so a power-capped clock shows (426 us back to back).
+// schedulers half busy (52% of issue slots), so a power-capped clock shows (404 to 426 us back to back).
 #pragma once
 #include "sm100_ptx.cuh"
 
@@ -185,7 +185,9 @@ __device__ __forceinline__ void q8_write4(const Q8Params &p, size_t row, int e0,
   if (e0 == 0 && p.lse) p.lse[row] = q8_lse(M, l);
 }
 
-// One CTA: one chunk of the context of one (sequence, key head), 8 NT query rows.
+// One CTA: one chunk of the context of one (sequence, key head), 8 NT query rows.  NT = 2 at d = 128 is held
+// to 168 registers, three CTAs to an SM, and spills 20 bytes: 32 sequences of 2048 tokens, 8 key heads,
+// 17 rows take 84 us so and 102 with two CTAs of 211 registers.
 template <int HD, int NT, int kType>
 __global__ void __launch_bounds__(kQ8Threads, (HD == 128 ? 5 : 6) - NT)
     fa_q8_stream_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,

@@ -13,9 +13,10 @@
 //   warp  15     a tile's scales and live tokens
 // TMEM (512 columns): S [side][2] x 64, then O [side] x d.  With more than 128 rows the sides hold two
 // row tiles; with fewer they share one row tile and take the tiles of tokens in turn.  A side's S is
-// double, so Q K^T of the next tile and P V of the last run during its softmax.  (With 128-token tiles S
-// fills the same columns once: softmax, P V and Q K^T of a side then follow one another, 5800 cycles
-// per 128 tokens and two row tiles against 5300 here, and 4500 against 3600 with one row tile.)
+// double, so Q K^T of the next tile and P V of the last run during its softmax.  (128-token tiles fill the
+// same columns with one S: softmax, P V and Q K^T of a side then follow one another.  The step away from
+// them, with a warp each for loads and scales and the order by length, took trees of 48 nodes from 190
+// to 125 us and 512-token chunks from 405 to 304.)
 //
 // Scales.  A key's scale multiplies its column of scores in fp32, read from shared memory by every
 // row (16 broadcast 16-byte loads per row and tile).  A value's scale vs = f 2^e is split: f goes into V =
@@ -40,11 +41,11 @@
 // it is written.
 //
 // Bound: per 128 rows x 64 tokens the products take about 510 cycles at d = 128 and the exponentials
-// 512 (16 a cycle); the 16 KB of codes take about 700 cycles of the SM's share of HBM.  Measured, two
-// row tiles take 2650 cycles a tile of tokens, 2100 of them the two sides' softmax warps side by side:
-// two warps to a scheduler issue an instruction every three cycles or so, which the exponential unit
-// (1024 of the 2100) does not hide.  512-token chunks of 4 sequences: 304 us, 620 TFLOP/s; trees of 48
-// nodes, 32 sequences: 125 us (DRAM's floor 28 us, the products' 35).
+// 512 (16 a cycle); the 16 KB of codes take about 700 cycles of the SM's share of HBM.  Measured, a tile
+// of tokens takes 2570 cycles with two row tiles and 1760 with one, and no unit is full: tensor pipe 36%,
+// exponentials 37%, issue slots 42%, the softmax warps, two to a scheduler, waiting for one step after
+// another.  Start and end of a CTA come on top, once or twice per SM.  512-token chunks of 4 sequences:
+// 312 us, 604 TFLOP/s; trees of 48 nodes, 32 sequences: 127 us (DRAM's floor 28 us, the products' 35).
 #pragma once
 #include "fa_q8.cuh"
 
@@ -94,7 +95,10 @@ struct Q8TileCfg {
   static_assert(kSmem > 114 * 1024, "one CTA per SM: it takes all of the tensor memory");
 };
 
-constexpr int kQ8SortSeqs = 128;  // up to here every CTA ranks the sequences itself
+// Up to here every CTA ranks the sequences itself.  128 sequences of 100 to 2000 tokens, 2 key heads, 40 rows:
+// 66 us ranked and 82 in the batch's order (all of one length: 68 and 66).  256 would gain as much as
+// they lose: 127 us ranked and 137 not when ragged, 131 and 121 when alike; 512 ragged ones 270 and 260.
+constexpr int kQ8SortSeqs = 128;
 
 // Two bf16 features times a power of two, in fp16.
 __device__ __forceinline__ uint32_t q8_fp16_of(uint32_t bf16x2, float unit) {

@@ -327,7 +327,8 @@ fa_status fa_rope(const void *q, const long long *q_strides, void *q_out,
  * codes = the values nearest to x / scale, ties to even (both fp32 quotients, rounded to nearest);
  * it stands for code * scale.  A row whose largest magnitude is below 2^-100 is stored as zeros with
  * scale 0, one that holds an infinity or a NaN with scale NaN and codes 0.  A bf16 pool takes
- * the rows rounded to bf16.  Keys are quantised from the fp32 result of the rotation.
+ * the rows rounded to bf16 (the 16-bit attention entry points that read one have as many key heads as
+ * query heads: write it with Hk = H).  Keys are quantised from the fp32 result of the rotation.
  *
  *   k, v           bf16 [T, Hk, d] with element strides of token and head in k_strides[2],
  *                  v_strides[2] (host arrays), features contiguous.
@@ -340,7 +341,9 @@ fa_status fa_rope(const void *q, const long long *q_strides, void *q_out,
  *   q, q_out       bf16 [T, Hq, d] with strides as k (Hq = 0: none, pointers ignored); every token's
  *                  q is rotated, padding too.  May be the same tensor (same pointer and strides);
  *                  otherwise q_out's rows may share memory neither with one another nor with
- *                  anything read (FA_ERR_INVALID_ARG), as in fa_rope.
+ *                  anything read (FA_ERR_INVALID_ARG), as in fa_rope.  For one sequence's T tokens
+ *                  the strides (d, T * d) give [Hq, T, d], as the chunk and tree calls below take
+ *                  it; for several sequences no pair of strides does, and their q is copied.
  *   positions      int32 [T], device;  freqs, rot, layout, amplitude as for fa_rope (rot = 0: no
  *                  rotation, positions and freqs may be null).
  *   T >= 0 (nothing is launched for 0), Hk >= 1, Hq >= 0;  d: 64 or 128;  (num_blocks + 1) * Hk <=
@@ -396,7 +399,12 @@ size_t fa_q8_workspace_size(int S, int Hq, int Hk, int Lq, int d, int max_blocks
  *                  hold no e4m3 NaN codes (0x7f, 0xff; fa_cache_append writes none); other slots of
  *                  the pool may hold anything.
  *   block_table    int32 [S, max_blocks_per_seq], device; a page whose entry is outside
- *                  [0, num_blocks) is left out and reported (FA_ERR_INVALID_ARG).
+ *                  [0, num_blocks) is left out and reported (FA_ERR_INVALID_ARG).  Entries past a
+ *                  sequence's last page are not read.  How a context is cut into chunks, and so the
+ *                  workspace, goes by max_blocks_per_seq (the lengths are not known on the host):
+ *                  a table much wider than the contexts makes more or longer chunks than they need.
+ *                  Above 32 rows (Hq / Hk * Lq) a few sequences behind a wide table may not be cut
+ *                  at all and take several times as long; there, pass a table as wide as the longest.
  *   seq_lens       int32 [S], device, each in [Lq, 16 * max_blocks_per_seq], or <= 0 for an empty
  *                  slot of a padded batch: its rows get O = 0, LSE = -inf.  Other lengths are
  *                  clamped into the interval and reported.
